@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(HERE, "libqsa.so")
  QSA_ERR_BAD_INDEX) = range(7)
 QSA_DTYPE_F32, QSA_DTYPE_BF16 = 0, 1
 (QSA_OP_COMPRESS, QSA_OP_INDEX, QSA_OP_SELECT, QSA_OP_ATTN, QSA_OP_FORWARD, QSA_OP_FORWARD_LOWMEM,
- QSA_OP_ATTN_UNION, QSA_OP_FORWARD_PREFIXED) = range(8)
+ QSA_OP_ATTN_UNION, QSA_OP_FORWARD_PREFIXED, QSA_OP_PAGED_ATTN, QSA_OP_PROMPT_ATTN,
+ QSA_OP_PROMPT_ATTN_BWD) = range(11)
 
 
 class qsa_config_t(ctypes.Structure):
@@ -45,6 +46,12 @@ class qsa_cache_t(ctypes.Structure):
                 ("v", ctypes.c_void_p), ("n_slots", ctypes.c_int32), ("n_cap", ctypes.c_int64)]
 
 
+class qsa_pages_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
 class QSAError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {status_string(status)} (status {status})")
@@ -60,6 +67,7 @@ def _load():
     C = ctypes.POINTER(qsa_config_t)
     K = ctypes.POINTER(qsa_cache_t)
     S = ctypes.POINTER(qsa_segment_t)
+    G = ctypes.POINTER(qsa_pages_t)
     sig = {
         "qsa_compress_keys": [C, K, P, P, P, I32, P],
         "qsa_index_scores": [C, K, S, I32, I32, P, P, P, I64, P],
@@ -74,6 +82,10 @@ def _load():
         "qsa_select_fallbacks": [P, ctypes.POINTER(ctypes.c_int64)],
         "qsa_selftest_wait_timeout": [P],
         "qsa_select_topk_noalloc": [C, S, I32, I32, P, I64, P, P, P],
+        "qsa_append_kv": [C, G, S, I32, I32, P, I64, P, I64, P, I64, P, P],
+        "qsa_paged_attn_fwd": [C, G, S, I32, I32, P, P, P, P, SZ, P],
+        "qsa_prompt_attn_fwd": [C, S, I32, I32, P, P, P, P, P, P, SZ, P],
+        "qsa_prompt_attn_bwd": [C, S, I32, I32, P, P, P, P, P, P, P, P, P, P, SZ, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -243,6 +255,114 @@ def qsa_forward_prefixed(cfg, cache, segs, prefixes, n_tokens, q, q_idx, w, o, l
     _check(get_lib().qsa_forward_prefixed(ctypes.byref(cfg), ctypes.byref(cache), arr, prefixes, n, n_tokens,
                                           _ptr(q), _ptr(q_idx), _ptr(w), _ptr(o), _ptr(lse), _ptr(sel), _ptr(nsel),
                                           _ptr(workspace), ws_bytes, _stream(stream)), "qsa_forward_prefixed")
+
+
+def make_pages(k, v, table) -> qsa_pages_t:
+    """Paged cache: k/v [n_pages,G,page_tokens,D], table [rows,max_pages] int32 (CUDA tensors).
+    A slot cache k/v [slots,G,N,D] is paged with table = arange(slots)[:, None]."""
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or table.dim() != 2:
+        raise ValueError("make_pages: k and v are [n_pages, G, page_tokens, D] of one dtype, table is [rows, max_pages]")
+    if str(table.dtype) != "torch.int32":
+        raise ValueError("make_pages: table is int32")
+    _one_device("make_pages", k, v, table)
+    pages = qsa_pages_t(_ptr(k), _ptr(v), _ptr(table), k.shape[0], k.shape[2], table.shape[0], table.shape[1])
+    pages.tensors = (k, v, table)
+    return pages
+
+
+def _one_device(where, *tensors):
+    """The tensors' device; they are contiguous and on the current one."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: a tensor is not contiguous")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{where}: tensors on {dev} and {t.device}")
+        dev = t.device
+    if dev is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors on {dev}, but the current device is {torch.cuda.current_device()}")
+    return dev
+
+
+def _shaped(where, cfg, n_tokens, pages=None, **tensors):
+    """Checks the dtype and shape of token-major tensors: q-like names hold
+    n_q_heads rows per token, k/v-like names n_kv_groups; lse is fp32."""
+    want = "torch.bfloat16" if cfg.dtype == QSA_DTYPE_BF16 else "torch.float32"
+    if pages is not None:
+        pk = pages.tensors[0]
+        if str(pk.dtype) != want or pk.shape[1] != cfg.n_kv_groups or pk.shape[3] != cfg.head_dim:
+            raise ValueError(f"{where}: pages are {tuple(pk.shape)} {pk.dtype}, not {want} with "
+                             f"{cfg.n_kv_groups} groups of {cfg.head_dim}")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        heads = cfg.n_kv_groups if name in ("k", "v", "dk", "dv") else cfg.n_q_heads
+        shape = (n_tokens, heads) if name == "lse" else (n_tokens, heads, cfg.head_dim)
+        dtype = "torch.float32" if name == "lse" else want
+        if tuple(t.shape) != shape or str(t.dtype) != dtype:
+            raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype}, not {shape} {dtype}")
+
+
+def _token_stride(where, name, t) -> int:
+    """Elements between a [T, heads, D] tensor's tokens; its heads are dense."""
+    if t.shape[0] and (t.stride(2) != 1 or t.stride(1) != t.shape[2]):
+        raise ValueError(f"{where}: the heads of a token of {name} are not contiguous")
+    return max(t.stride(0), t.shape[1] * t.shape[2]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def qsa_append_kv(cfg, pages, segs, n_tokens, k, v, q=None, q_out=None, stream=None):
+    """Writes the tokens' k (rotated) and v to the paged cache, and the rotated q to q_out.
+    k, v, q: [T, heads, D]; the tokens may be strided (slices of a fused projection)."""
+    where = "qsa_append_kv"
+    arr, n = segs
+    _shaped(where, cfg, n_tokens, pages, k=k, v=v, q=q, q_out=q_out)
+    _one_device(where, q_out, *pages.tensors)
+    for t in (k, v, q):
+        if t is not None and t.device != pages.tensors[0].device:
+            raise ValueError(f"{where}: tensors on {t.device} and {pages.tensors[0].device}")
+    _check(get_lib().qsa_append_kv(ctypes.byref(cfg), ctypes.byref(pages), arr, n, n_tokens, _ptr(k),
+                                   _token_stride(where, "k", k), _ptr(v), _token_stride(where, "v", v), _ptr(q),
+                                   0 if q is None else _token_stride(where, "q", q), _ptr(q_out), _stream(stream)),
+           where)
+
+
+def qsa_paged_attn_fwd(cfg, pages, segs, n_tokens, q, o, lse=None, workspace=None, stream=None):
+    """Dense causal attention of the new tokens over the paged cache (workspace: QSA_OP_PAGED_ATTN)."""
+    where = "qsa_paged_attn_fwd"
+    arr, n = segs
+    _shaped(where, cfg, n_tokens, pages, q=q, o=o, lse=lse)
+    _one_device(where, q, o, lse, workspace, *pages.tensors)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(get_lib().qsa_paged_attn_fwd(ctypes.byref(cfg), ctypes.byref(pages), arr, n, n_tokens, _ptr(q), _ptr(o),
+                                        _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)), where)
+
+
+def qsa_prompt_attn_fwd(cfg, segs, n_tokens, q, k, v, o, lse=None, workspace=None, stream=None):
+    """Dense causal attention over packed whole prompts: q, o [T,H,D], k, v [T,G,D]
+    (workspace: QSA_OP_PROMPT_ATTN)."""
+    where = "qsa_prompt_attn_fwd"
+    arr, n = segs
+    _shaped(where, cfg, n_tokens, q=q, k=k, v=v, o=o, lse=lse)
+    _one_device(where, q, k, v, o, lse, workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(get_lib().qsa_prompt_attn_fwd(ctypes.byref(cfg), arr, n, n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(o),
+                                         _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)), where)
+
+
+def qsa_prompt_attn_bwd(cfg, segs, n_tokens, q, k, v, o, lse, dout, dq, dk, dv, workspace=None, stream=None):
+    """Backward of qsa_prompt_attn_fwd: writes dq, dk, dv in the I/O dtype
+    (workspace: QSA_OP_PROMPT_ATTN_BWD)."""
+    where = "qsa_prompt_attn_bwd"
+    arr, n = segs
+    _shaped(where, cfg, n_tokens, q=q, k=k, v=v, o=o, lse=lse, dout=dout, dq=dq, dk=dk, dv=dv)
+    _one_device(where, q, k, v, o, lse, dout, dq, dk, dv, workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(get_lib().qsa_prompt_attn_bwd(ctypes.byref(cfg), arr, n, n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(o),
+                                         _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
+                                         ws_bytes, _stream(stream)), where)
 
 
 def qsa_device_status(stream=None):

@@ -1,0 +1,171 @@
+// dense.cuh -- work tables of the dense causal attention kernels (over a paged
+// cache and over packed prompts): units, their order, and the split of the
+// last units over the grid.
+//
+// A unit is (tile, KV group): `rows` consecutive query rows of one segment and
+// group, row r = token r / hpg, head r % hpg of the group, against the keys
+// 0 .. position of the tile's last token, in chunks of `kc` keys.  Units are
+// ordered longest first (segments by length, a segment's tiles from its end).
+// Whole rounds of units are dealt to the grid back and forth; the units left
+// over form one flat sequence of chunks that is cut so that every CTA ends
+// with the same number of chunks.  A unit cut between CTAs is computed in
+// pieces, each leaving an unnormalised fp32 partial result, which
+// dense_combine_kernel joins in a fixed order.  Units with few rows (decode)
+// are nothing but such a sequence: keys split over the GPU.
+#pragma once
+#include "qsa_internal.cuh"
+
+namespace qsa {
+namespace dense {
+constexpr int kMaxGrid = 148;              // CTAs (or CTA pairs) a table is cut for
+constexpr int kPartFloats = kHeadDim + 4;  // a row's partial: 256 sums, maximum and sum of its softmax, 2 unused
+}  // namespace dense
+
+struct DensePoint {
+  int32_t unit, chunk;
+};
+
+struct DenseTable {
+  int32_t n;
+  int32_t q_offset[kMaxSegs];
+  int32_t q_len[kMaxSegs];
+  int32_t pos0[kMaxSegs];
+  int32_t slot[kMaxSegs];
+  int32_t item0[kMaxSegs + 1];             // tiles of the segments before
+  int32_t G, hpg;
+  int32_t rows, kc;                        // query rows per tile, keys per chunk
+  int32_t grid;                            // CTAs (or pairs)
+  int32_t rounds;                          // whole units per CTA; unit rounds*grid is the first of the tail
+  int32_t prows;                           // rows of a partial result
+  int32_t pad_;
+  DensePoint cut[dense::kMaxGrid + 1];     // CTA c takes the tail from cut[c] up to cut[c+1]
+};
+
+// Units cut into pieces: the CTAs first..last each may hold one.
+struct DenseSplits {
+  int32_t n;
+  int32_t unit[dense::kMaxGrid];
+  int16_t first[dense::kMaxGrid], last[dense::kMaxGrid];
+};
+
+struct DenseUnit {
+  int si;                // segment
+  int grp;
+  int64_t row0;          // first row of the tile in the segment's rows
+  int nrows;             // valid rows (>= 1)
+  int64_t kv_len;        // keys 0 .. kv_len-1 are those of the tile's last token
+  int nchunks;
+};
+
+__host__ __device__ __forceinline__ DenseUnit dense_unit(const DenseTable& t, int u) {
+  DenseUnit x;
+  const int tile = u / t.G;
+  x.grp = u - tile * t.G;
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.item0[mid] <= tile) lo = mid; else hi = mid - 1;
+  }
+  x.si = lo;
+  const int64_t total = (int64_t)t.q_len[lo] * t.hpg;
+  x.row0 = (int64_t)(t.item0[lo + 1] - 1 - tile) * t.rows;     // tiles from the segment's end
+  const int64_t left = total - x.row0;
+  x.nrows = (int)(left < t.rows ? left : t.rows);
+  const int64_t last_tok = (x.row0 + x.nrows - 1) / t.hpg;
+  x.kv_len = (int64_t)t.pos0[lo] + last_tok + 1;
+  x.nchunks = (int)((x.kv_len + t.kc - 1) / t.kc);
+  return x;
+}
+
+// One piece of work of a CTA: chunks c0 .. c1-1 of a unit.  part < 0: the
+// whole unit; else the slot of its partial result.
+struct DensePiece {
+  int unit, c0, c1, part;
+};
+
+// Walks a CTA's pieces: its whole units, then its stretch of the tail.
+struct DenseWalk {
+  int cta, round, unit;
+  __host__ __device__ __forceinline__ void init(const DenseTable& t, int c) {
+    cta = c;
+    round = 0;
+    unit = t.cut[c].unit;
+  }
+  // Fills p and, for the caller, the unit; false at the end.
+  __host__ __device__ __forceinline__ bool next(const DenseTable& t, DensePiece& p, DenseUnit& x) {
+    if (round < t.rounds) {
+      p.unit = round * t.grid + ((round & 1) ? t.grid - 1 - cta : cta);
+      ++round;
+      x = dense_unit(t, p.unit);
+      p.c0 = 0;
+      p.c1 = x.nchunks;
+      p.part = -1;
+      return true;
+    }
+    const DensePoint a = t.cut[cta], b = t.cut[cta + 1];
+    while (unit < b.unit || (unit == b.unit && b.chunk > 0)) {
+      x = dense_unit(t, unit);
+      p.unit = unit;
+      p.c0 = unit == a.unit ? a.chunk : 0;
+      p.c1 = unit == b.unit ? b.chunk : x.nchunks;
+      p.part = (p.c0 == 0 && p.c1 == x.nchunks) ? -1 : 2 * cta + (unit == a.unit ? 0 : 1);
+      ++unit;
+      if (p.c0 < p.c1) return true;
+    }
+    return false;
+  }
+};
+
+// Joins the pieces of each cut unit: with m the largest of the pieces' maxima
+// (log2 units), l = sum l_p 2^(m_p - m), o = sum o_p 2^(m_p - m) / l.  A piece
+// without a key of a row has m_p = -inf and counts nothing.  One warp per row,
+// 8 dims per lane; pieces are added in the order of their keys.
+template <typename T>
+__global__ void __launch_bounds__(128)
+    dense_combine_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseSplits sp,
+                         const float* part, T* o, float* lse, int H) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x;
+  const int u = sp.unit[i];
+  const DenseUnit x = dense_unit(t, u);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.y * 4 + warp;
+  if (r >= x.nrows) return;
+  auto piece = [&](int c) -> const float* {      // null: CTA c has no piece of the unit
+    const DensePoint a = t.cut[c], b = t.cut[c + 1];
+    if (a.unit > u || b.unit < u || (b.unit == u && b.chunk == 0) || (a.unit == b.unit && a.chunk == b.chunk))
+      return nullptr;
+    return part + ((int64_t)(2 * c + (a.unit == u ? 0 : 1)) * t.prows + r) * dense::kPartFloats;
+  };
+  float m = -INFINITY;
+  for (int c = sp.first[i]; c <= sp.last[i]; ++c)
+    if (const float* p = piece(c)) m = fmaxf(m, p[kHeadDim]);
+  float l = 0.f, acc[8] = {};
+  for (int c = sp.first[i]; c <= sp.last[i]; ++c) {
+    const float* p = piece(c);
+    if (!p) continue;
+    const float mp = p[kHeadDim];
+    if (mp == -INFINITY) continue;
+    const float w = exp2f(mp - m);
+    l += w * p[kHeadDim + 1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = *reinterpret_cast<const float2*>(p + lane * 2 + k * 64);
+      acc[2 * k] += w * f.x;
+      acc[2 * k + 1] += w * f.y;
+    }
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;     // l = 0: no key at all
+  const int64_t row = x.row0 + r;
+  const int64_t tok = t.q_offset[x.si] + row / t.hpg;
+  const int64_t at = tok * H + (int64_t)x.grp * t.hpg + row % t.hpg;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    o[at * kHeadDim + lane * 2 + k * 64] = IO<T>::from_f(acc[2 * k] * inv);
+    o[at * kHeadDim + lane * 2 + k * 64 + 1] = IO<T>::from_f(acc[2 * k + 1] * inv);
+  }
+  if (lse && lane == 0) lse[at] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+}  // namespace qsa

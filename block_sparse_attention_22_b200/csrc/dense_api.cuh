@@ -1,0 +1,424 @@
+// dense_api.cuh -- host side of the paged append and the dense attention
+// (qsa_append_kv, qsa_paged_attn_fwd, qsa_prompt_attn_fwd, qsa_prompt_attn_bwd):
+// argument checks, work tables, launches.  Included once, by qsa_api.cu.
+#pragma once
+#include "append.cuh"
+#include "dense.cuh"
+#include "dense_simt.cuh"
+
+namespace qsa {
+namespace {
+
+// ------------------------------------------------------------------ checks
+qsa_status_t check_pages(const qsa_config_t* c, const qsa_pages_t* p) {
+  if (!p || !p->k || !p->v || !p->table || !aligned16(p->k) || !aligned16(p->v) || ((uintptr_t)p->table & 3u))
+    return QSA_ERR_INVALID_ARG;
+  if (p->n_pages <= 0 || p->page_tokens <= 0 || p->n_rows <= 0 || p->max_pages <= 0) return QSA_ERR_INVALID_ARG;
+  if (p->page_tokens % 16 != 0) return QSA_ERR_UNSUPPORTED;
+  // cache rows are TMA coordinates (int32)
+  if ((int64_t)p->n_pages * c->n_kv_groups > INT32_MAX / p->page_tokens) return QSA_ERR_UNSUPPORTED;
+  return QSA_OK;
+}
+
+// Segments within the table and the token arrays, and no token row in two of them.
+qsa_status_t check_dense_segments(const qsa_segment_t* segs, int32_t n_segs, int32_t n_tokens,
+                                  const qsa_pages_t* pages, bool prompt) {
+  if (n_segs < 0 || n_tokens < 0 || (n_segs > 0 && !segs)) return QSA_ERR_INVALID_ARG;
+  bool sorted = true;
+  int64_t end = 0;
+  for (int i = 0; i < n_segs; ++i) {
+    const qsa_segment_t& s = segs[i];
+    if (s.q_len < 0 || s.q_offset < 0 || s.pos0 < 0) return QSA_ERR_INVALID_ARG;
+    if ((int64_t)s.q_offset + s.q_len > n_tokens) return QSA_ERR_INVALID_ARG;
+    if ((int64_t)s.pos0 + s.q_len > INT32_MAX) return QSA_ERR_INVALID_ARG;
+    if (prompt && s.pos0 != 0) return QSA_ERR_INVALID_ARG;
+    if (pages && (s.slot < 0 || s.slot >= pages->n_rows ||
+                  (int64_t)s.pos0 + s.q_len > (int64_t)pages->max_pages * pages->page_tokens))
+      return QSA_ERR_INVALID_ARG;
+    if (s.q_len == 0) continue;
+    if (s.q_offset < end) sorted = false;
+    end = (int64_t)s.q_offset + s.q_len;
+  }
+  if (sorted) return QSA_OK;
+  std::vector<std::pair<int32_t, int32_t>> r;
+  for (int i = 0; i < n_segs; ++i)
+    if (segs[i].q_len > 0) r.emplace_back(segs[i].q_offset, segs[i].q_len);
+  std::sort(r.begin(), r.end());
+  for (size_t i = 1; i < r.size(); ++i)
+    if ((int64_t)r[i - 1].first + r[i - 1].second > r[i].first) return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
+
+// ------------------------------------------------------------------ plan
+// Shape of one kind of launch.
+struct DenseKind {
+  int rows, kc, grid;
+};
+// A unit's fixed cost (loading Q, the epilogue) in chunks, for levelling.
+constexpr int64_t kUnitCost = 2;
+// Fewest chunks a CTA takes of the tail: below it a piece's partial result
+// costs more than the chunks it saves.
+constexpr int64_t kMinTail = 4;
+
+int64_t unit_chunks(const DenseTable& t, int u) { return dense_unit(t, u).nchunks; }
+
+// Fills rounds, cut and the list of cut units of a table whose segments are set.
+void cut_table(DenseTable& t, DenseSplits& sp) {
+  const int grid = t.grid;
+  const int n_units = t.item0[t.n] * t.G;
+  std::vector<int32_t> chunks((size_t)n_units);
+  int64_t total = 0;
+  for (int u = 0; u < n_units; ++u) {
+    chunks[u] = (int32_t)unit_chunks(t, u);
+    total += chunks[u] + kUnitCost;
+  }
+  // the most whole rounds after which no CTA has more than its share of everything
+  std::vector<int64_t> load((size_t)grid, 0), best = load;
+  t.rounds = 0;
+  for (int r = 0; (r + 1) * grid <= n_units; ++r) {
+    int64_t mx = 0;
+    for (int c = 0; c < grid; ++c) {
+      load[c] += chunks[r * grid + ((r & 1) ? grid - 1 - c : c)] + kUnitCost;
+      mx = std::max(mx, load[c]);
+    }
+    if (mx * grid <= total + (int64_t)grid * kUnitCost) {
+      t.rounds = r + 1;
+      best = load;
+    }
+  }
+  const int tail0 = t.rounds * grid;
+  int64_t tail = 0, whole = 0;
+  for (int u = tail0; u < n_units; ++u) tail += chunks[u] + kUnitCost;
+  for (int c = 0; c < grid; ++c) whole += best[c];
+  // cuts for CTAs filled up to `share` (at least kMinTail chunks at a time); true if that holds everything
+  auto lay = [&](int64_t share) -> bool {
+    int u = tail0;
+    int64_t at = 0;                     // chunks of unit u already taken
+    int64_t carry = 0;                  // what the CTAs so far took too little (or too much, negative)
+    for (int c = 0; c < grid; ++c) {
+      t.cut[c] = {u, (int32_t)at};
+      int64_t want = carry + std::max<int64_t>(share - best[c], kMinTail + kUnitCost);
+      while (u < n_units && want > 0) {
+        const int64_t left = chunks[u] - at;
+        if (want >= left + kUnitCost || left + kUnitCost - want < kMinTail) {
+          want -= left + kUnitCost;
+          ++u;
+          at = 0;
+        } else {
+          if (want - kUnitCost >= kMinTail) {
+            at += want - kUnitCost;
+            want = 0;
+          }
+          break;
+        }
+      }
+      carry = want;
+    }
+    return u >= n_units;
+  };
+  // the smallest share that holds everything: a unit cut in n pieces costs n times kUnitCost
+  int64_t lo = cdiv(whole + tail, grid), hi = lo + (kMinTail + 2 * kUnitCost);
+  while (!lay(hi)) {
+    lo = hi;
+    hi += hi - cdiv(whole + tail, grid);
+  }
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (lay(mid)) hi = mid; else lo = mid;
+  }
+  lay(hi);
+  t.cut[grid] = {n_units, 0};
+  sp.n = 0;
+  // a unit is cut iff some CTA's stretch starts inside it
+  for (int c = 1; c < grid; ++c) {
+    if (t.cut[c].chunk == 0) continue;
+    const int unit = t.cut[c].unit;
+    if (sp.n > 0 && sp.unit[sp.n - 1] == unit) {
+      sp.last[sp.n - 1] = (int16_t)c;
+      continue;
+    }
+    int first = c - 1;                  // the CTA that holds the unit's first chunk
+    while (first > 0 && (t.cut[first].unit == unit && t.cut[first].chunk > 0)) --first;
+    sp.unit[sp.n] = unit;
+    sp.first[sp.n] = (int16_t)first;
+    sp.last[sp.n] = (int16_t)c;
+    ++sp.n;
+  }
+}
+
+// Calls launch(table, splits) for batches of at most kMaxSegs of the non-empty
+// segments, longest first.
+template <typename Launch>
+qsa_status_t for_each_dense(const Geo& g, std::vector<qsa_segment_t> segs, const DenseKind& kind, Launch launch) {
+  segs.erase(std::remove_if(segs.begin(), segs.end(), [](const qsa_segment_t& s) { return s.q_len <= 0; }), segs.end());
+  std::stable_sort(segs.begin(), segs.end(), [](const qsa_segment_t& a, const qsa_segment_t& b) {
+    return (int64_t)a.pos0 + a.q_len > (int64_t)b.pos0 + b.q_len;
+  });
+  size_t i = 0;
+  while (i < segs.size()) {
+    DenseTable t;
+    DenseSplits sp;
+    memset(&t, 0, sizeof t);
+    memset(&sp, 0, sizeof sp);
+    t.G = g.G;
+    t.hpg = g.hpg;
+    t.rows = kind.rows;
+    t.kc = kind.kc;
+    t.grid = kind.grid;
+    int64_t tiles = 0, most = 0;
+    for (; i < segs.size() && t.n < kMaxSegs; ++i) {
+      const qsa_segment_t& s = segs[i];
+      const int64_t rows = (int64_t)s.q_len * g.hpg, it = cdiv(rows, kind.rows);
+      if (t.n > 0 && (tiles + it) * g.G > INT32_MAX / 4) break;
+      if ((tiles + it) * g.G > INT32_MAX / 4) return QSA_ERR_UNSUPPORTED;
+      t.q_offset[t.n] = s.q_offset;
+      t.q_len[t.n] = s.q_len;
+      t.pos0[t.n] = s.pos0;
+      t.slot[t.n] = s.slot;
+      tiles += it;
+      t.item0[++t.n] = (int32_t)tiles;
+      most = std::max(most, std::min<int64_t>(rows, kind.rows));
+    }
+    t.prows = (int32_t)most;
+    cut_table(t, sp);
+    const qsa_status_t r = launch(t, sp);
+    if (r != QSA_OK) return r;
+  }
+  return QSA_OK;
+}
+
+// Segments of few query rows (decode) and the others, with the shape of their launches.
+void dense_kinds(const Geo& g, bool tc, const qsa_segment_t* segs, int n, std::vector<qsa_segment_t>& narrow,
+                 std::vector<qsa_segment_t>& wide, DenseKind& kn, DenseKind& kw) {
+  (void)tc;
+  kn = {dense_simt::kRowsNarrow, dense_simt::kKeys, kNumSms};
+  kw = {dense_simt::kRowsWide, dense_simt::kKeys, kNumSms};
+  for (int i = 0; i < n; ++i)
+    if (segs[i].q_len > 0) ((int64_t)segs[i].q_len * g.hpg <= kn.rows ? narrow : wide).push_back(segs[i]);
+}
+
+// Bytes of a table's partial results.
+size_t partial_bytes(const DenseTable& t, const DenseSplits& sp) {
+  return sp.n > 0 ? (size_t)2 * t.grid * t.prows * dense::kPartFloats * 4 : 0;
+}
+
+size_t dense_fwd_ws(const Geo& g, bool tc, const qsa_segment_t* segs, int n) {
+  std::vector<qsa_segment_t> narrow, wide;
+  DenseKind kn, kw;
+  dense_kinds(g, tc, segs, n, narrow, wide, kn, kw);
+  size_t ws = 0;
+  auto note = [&](const DenseTable& t, const DenseSplits& sp) {
+    ws = std::max(ws, partial_bytes(t, sp));
+    return QSA_OK;
+  };
+  if (for_each_dense(g, narrow, kn, note) != QSA_OK || for_each_dense(g, wide, kw, note) != QSA_OK) return SIZE_MAX;
+  return align_up(ws, 256);
+}
+
+// ------------------------------------------------------------------ forward
+template <typename T, int ROWS, bool PAGED>
+cudaError_t launch_dense_simt(const Geo& g, const DenseTable& t, const KvSource& kv, const void* q, void* o,
+                              float* lse, float* part, cudaStream_t st) {
+  const int smem = dense_simt::fwd_smem(ROWS);
+  cudaError_t e = cudaFuncSetAttribute(dense_fwd_simt_kernel<T, ROWS, PAGED>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return launch_chained(dense_fwd_simt_kernel<T, ROWS, PAGED>, dim3(t.grid), dim3(dense_simt::kThreads), smem, st, t,
+                        kv, (const T*)q, (T*)o, lse, part, g.H, g.scale);
+}
+
+template <typename T>
+cudaError_t launch_dense_combine(const Geo& g, const DenseTable& t, const DenseSplits& sp, const float* part, void* o,
+                                 float* lse, cudaStream_t st) {
+  count_launch();
+  return launch_chained(dense_combine_kernel<T>, dim3(sp.n, (unsigned)cdiv(t.prows, 4)), dim3(128), 0, st, t, sp,
+                        part, (T*)o, lse, g.H);
+}
+
+template <typename T, bool PAGED>
+qsa_status_t run_dense_fwd(const Geo& g, const qsa_segment_t* segs, int n, const KvSource& kv, const void* q, void* o,
+                           float* lse, void* ws, size_t ws_bytes, cudaStream_t st) {
+  const size_t need = dense_fwd_ws(g, sizeof(T) == 2, segs, n);
+  if (need == SIZE_MAX) return QSA_ERR_UNSUPPORTED;
+  if (need > 0 && (!ws || ws_bytes < need)) return QSA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(ws)) return QSA_ERR_INVALID_ARG;
+  std::vector<qsa_segment_t> narrow, wide;
+  DenseKind kn, kw;
+  dense_kinds(g, sizeof(T) == 2, segs, n, narrow, wide, kn, kw);
+  auto run = [&](bool is_wide) {
+    return [&, is_wide](const DenseTable& t, const DenseSplits& sp) -> qsa_status_t {
+      cudaError_t e = is_wide ? launch_dense_simt<T, dense_simt::kRowsWide, PAGED>(g, t, kv, q, o, lse, (float*)ws, st)
+                              : launch_dense_simt<T, dense_simt::kRowsNarrow, PAGED>(g, t, kv, q, o, lse, (float*)ws, st);
+      if (e == cudaSuccess && sp.n > 0) e = launch_dense_combine<T>(g, t, sp, (const float*)ws, o, lse, st);
+      return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+    };
+  };
+  const qsa_status_t r = for_each_dense(g, wide, kw, run(true));
+  return r != QSA_OK ? r : for_each_dense(g, narrow, kn, run(false));
+}
+
+// ------------------------------------------------------------------ backward
+size_t dense_bwd_ws(const Geo& g, int32_t n_tokens) { return align_up((size_t)n_tokens * g.H * 4, 256); }
+
+template <typename T>
+qsa_status_t run_dense_bwd(const Geo& g, const qsa_segment_t* segs, int n, DenseBwdArgs a, const void* o, float* delta,
+                           cudaStream_t st) {
+  qsa_status_t r = for_each_table(
+      segs, n, [&](const qsa_segment_t& s) { return (int64_t)s.q_len; },
+      [&](const SegTable& t) -> cudaError_t {
+        count_launch();
+        return launch_chained(dense_delta_kernel<T>, dim3((unsigned)cdiv((int64_t)t.item0[t.n] * g.H, 8)), dim3(256), 0,
+                              st, t, (const T*)o, (const T*)a.dout, delta, g.H);
+      });
+  if (r != QSA_OK) return r;
+  cudaError_t e = cudaFuncSetAttribute(dense_dq_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       dense_simt::kBwdSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(dense_dkv_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             dense_simt::kBwdSmem);
+  if (e != cudaSuccess) return QSA_ERR_CUDA;
+  r = for_each_dense(g, std::vector<qsa_segment_t>(segs, segs + n), DenseKind{dense_simt::kBRows, dense_simt::kBKeys, 1},
+                     [&](const DenseTable& t, const DenseSplits&) -> qsa_status_t {
+                       count_launch();
+                       return launch_chained(dense_dq_simt_kernel<T>, dim3((unsigned)(t.item0[t.n] * g.G)),
+                                             dim3(dense_simt::kThreads), dense_simt::kBwdSmem, st, t, a) == cudaSuccess
+                                  ? QSA_OK
+                                  : QSA_ERR_CUDA;
+                     });
+  if (r != QSA_OK) return r;
+  return for_each_table(
+      segs, n, [&](const qsa_segment_t& s) { return cdiv(s.q_len, dense_simt::kBKeys); },
+      [&](const SegTable& t) -> cudaError_t {
+        count_launch();
+        return launch_chained(dense_dkv_simt_kernel<T>, dim3((unsigned)(t.item0[t.n] * g.G)), dim3(dense_simt::kThreads),
+                              dense_simt::kBwdSmem, st, t, g.G, g.hpg, a);
+      });
+}
+
+// Runs an entry point's body; host memory that runs out is an error code, not
+// an exception through the C interface.
+template <typename Body>
+qsa_status_t guarded(Body body) {
+  try {
+    return body();
+  } catch (...) {
+    return QSA_ERR_CUDA;
+  }
+}
+
+}  // namespace
+}  // namespace qsa
+
+using namespace qsa;
+
+QSA_API qsa_status_t qsa_append_kv(const qsa_config_t* cfg, const qsa_pages_t* pages, const qsa_segment_t* segs,
+                                   int32_t n_segs, int32_t n_tokens, const void* k, int64_t ld_k, const void* v,
+                                   int64_t ld_v, const void* q, int64_t ld_q, void* q_out, void* stream) {
+  return guarded([&]() -> qsa_status_t {
+    qsa_status_t s = check_cfg(cfg);
+    if (s != QSA_OK) return s;
+    if ((s = check_pages(cfg, pages)) != QSA_OK) return s;
+    if ((s = check_dense_segments(segs, n_segs, n_tokens, pages, false)) != QSA_OK) return s;
+    if (seg_rows(segs, n_segs) == 0) return QSA_OK;
+    if (!k || !v || !aligned16(k) || !aligned16(v) || (!q) != (!q_out) || !aligned16(q) || !aligned16(q_out))
+      return QSA_ERR_INVALID_ARG;
+    const int64_t per16 = cfg->dtype == QSA_DTYPE_BF16 ? 8 : 4;
+    auto bad_ld = [&](int64_t ld, int heads) { return ld < (int64_t)heads * kHeadDim || ld % per16 != 0; };
+    if (bad_ld(ld_k, cfg->n_kv_groups) || bad_ld(ld_v, cfg->n_kv_groups) || (q && bad_ld(ld_q, cfg->n_q_heads)))
+      return QSA_ERR_INVALID_ARG;
+    if (q && q == q_out && ld_q != (int64_t)cfg->n_q_heads * kHeadDim) return QSA_ERR_INVALID_ARG;
+    const Geo g = make_geo(cfg, nullptr);
+    AppendArgs a;
+    memset(&a, 0, sizeof a);
+    a.k = k;
+    a.v = v;
+    a.q = q;
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.ld_q = ld_q;
+    a.q_out = q_out;
+    a.kp = pages->k;
+    a.vp = pages->v;
+    a.table = pages->table;
+    a.n_pages = pages->n_pages;
+    a.page_tokens = pages->page_tokens;
+    a.max_pages = pages->max_pages;
+    int rd = (int)floor((double)cfg->head_dim * (double)cfg->rope_fraction);
+    rd -= rd & 1;
+    a.half = rd / 2;
+    for (int i = 0; i < a.half; ++i) a.theta[i] = pow(cfg->rope_base, -(2.0 * (double)i) / (double)rd);
+    return for_each_table(
+        segs, n_segs, [&](const qsa_segment_t& sg) { return (int64_t)sg.q_len; },
+        [&](const SegTable& t) -> cudaError_t {
+          count_launch();
+          const dim3 grid((unsigned)t.item0[t.n]), block(append::kThreads);
+          return cfg->dtype == QSA_DTYPE_BF16
+                     ? launch_chained(append_kernel<__nv_bfloat16>, grid, block, 0, (cudaStream_t)stream, g, t, a)
+                     : launch_chained(append_kernel<float>, grid, block, 0, (cudaStream_t)stream, g, t, a);
+        });
+  });
+}
+
+QSA_API qsa_status_t qsa_paged_attn_fwd(const qsa_config_t* cfg, const qsa_pages_t* pages, const qsa_segment_t* segs,
+                                        int32_t n_segs, int32_t n_tokens, const void* q, void* o, float* lse,
+                                        void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> qsa_status_t {
+    qsa_status_t s = check_cfg(cfg);
+    if (s != QSA_OK) return s;
+    if ((s = check_pages(cfg, pages)) != QSA_OK) return s;
+    if ((s = check_dense_segments(segs, n_segs, n_tokens, pages, false)) != QSA_OK) return s;
+    if (seg_rows(segs, n_segs) == 0) return QSA_OK;
+    if (!q || !o || !aligned16(q) || !aligned16(o) || ((uintptr_t)lse & 3u)) return QSA_ERR_INVALID_ARG;
+    const Geo g = make_geo(cfg, nullptr);
+    const KvSource kv{pages->k, pages->v, pages->table, pages->n_pages, pages->page_tokens, pages->max_pages};
+    return cfg->dtype == QSA_DTYPE_BF16
+               ? run_dense_fwd<__nv_bfloat16, true>(g, segs, n_segs, kv, q, o, lse, workspace, ws_bytes,
+                                                    (cudaStream_t)stream)
+               : run_dense_fwd<float, true>(g, segs, n_segs, kv, q, o, lse, workspace, ws_bytes, (cudaStream_t)stream);
+  });
+}
+
+QSA_API qsa_status_t qsa_prompt_attn_fwd(const qsa_config_t* cfg, const qsa_segment_t* segs, int32_t n_segs,
+                                         int32_t n_tokens, const void* q, const void* k, const void* v, void* o,
+                                         float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> qsa_status_t {
+    qsa_status_t s = check_cfg(cfg);
+    if (s != QSA_OK) return s;
+    if ((s = check_dense_segments(segs, n_segs, n_tokens, nullptr, true)) != QSA_OK) return s;
+    if (seg_rows(segs, n_segs) == 0) return QSA_OK;
+    if (!q || !k || !v || !o || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
+        ((uintptr_t)lse & 3u))
+      return QSA_ERR_INVALID_ARG;
+    const Geo g = make_geo(cfg, nullptr);
+    const KvSource kv{k, v, nullptr, 0, 0, 0};
+    return cfg->dtype == QSA_DTYPE_BF16
+               ? run_dense_fwd<__nv_bfloat16, false>(g, segs, n_segs, kv, q, o, lse, workspace, ws_bytes,
+                                                     (cudaStream_t)stream)
+               : run_dense_fwd<float, false>(g, segs, n_segs, kv, q, o, lse, workspace, ws_bytes,
+                                             (cudaStream_t)stream);
+  });
+}
+
+QSA_API qsa_status_t qsa_prompt_attn_bwd(const qsa_config_t* cfg, const qsa_segment_t* segs, int32_t n_segs,
+                                         int32_t n_tokens, const void* q, const void* k, const void* v, const void* o,
+                                         const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                                         void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> qsa_status_t {
+    qsa_status_t s = check_cfg(cfg);
+    if (s != QSA_OK) return s;
+    if ((s = check_dense_segments(segs, n_segs, n_tokens, nullptr, true)) != QSA_OK) return s;
+    if (seg_rows(segs, n_segs) == 0) return QSA_OK;
+    for (const void* p : {q, k, v, o, dout, (const void*)dq, (const void*)dk, (const void*)dv})
+      if (!p || !aligned16(p)) return QSA_ERR_INVALID_ARG;
+    if (!lse || ((uintptr_t)lse & 3u)) return QSA_ERR_INVALID_ARG;
+    const Geo g = make_geo(cfg, nullptr);
+    if (!workspace || ws_bytes < dense_bwd_ws(g, n_tokens)) return QSA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QSA_ERR_INVALID_ARG;
+    float* delta = (float*)workspace;
+    const DenseBwdArgs a{q, k, v, lse, delta, dout, dq, dk, dv, g.H, g.scale};
+    return cfg->dtype == QSA_DTYPE_BF16
+               ? run_dense_bwd<__nv_bfloat16>(g, segs, n_segs, a, o, delta, (cudaStream_t)stream)
+               : run_dense_bwd<float>(g, segs, n_segs, a, o, delta, (cudaStream_t)stream);
+  });
+}

@@ -1,0 +1,506 @@
+// dense_simt.cuh -- dense causal GQA attention in fp32 on CUDA cores: forward
+// over a paged cache or packed prompts, and the gradient over packed prompts.
+//
+// The formulas are those of qsa_paged_attn_fwd, qsa_prompt_attn_fwd and
+// qsa_prompt_attn_bwd (qsa.h).  fp32 products have no tensor-core form of the
+// same precision, so the work is FFMA on tiles held in shared memory, rows
+// padded by 4 floats so that the 16-byte reads of neighbouring rows fall into
+// different banks.  A thread owns R query rows x 4 keys of a 64-key chunk's
+// scores and the same R rows x 16 dims of the result; the 16 threads of a row
+// are half a warp, so the softmax exchanges by shuffles.  cp.async brings the
+// next chunk's K during the softmax and products of this one and its V during
+// the next scores.
+//
+// Masked places may hold anything: keys past the sequence are filled with
+// zeros instead of being read, scores of keys after the row's position are
+// replaced, and in a chunk that holds such keys their V rows are skipped
+// row by row (0 * NaN would spread).
+#pragma once
+#include "qsa_internal.cuh"
+#include "sm100.cuh"
+#include "dense.cuh"
+
+namespace qsa {
+namespace dense_simt {
+constexpr int kThreads = 256;
+constexpr int kKeys = 64;
+constexpr int kLd = kHeadDim + 4;
+constexpr int kPLd = kKeys + 4;
+constexpr int kRowsWide = 64, kRowsNarrow = 16;
+constexpr int fwd_smem(int rows) { return (rows * kLd + 2 * kKeys * kLd + rows * kPLd + kKeys) * 4; }
+// gradient kernels: 64 rows (Q, dO) and 32 keys (K, V)
+constexpr int kBRows = 64, kBKeys = 32, kBLd = kBKeys + 4;
+constexpr int kBwdSmem = (2 * kBRows * kLd + 2 * kBKeys * kLd + 2 * kBRows * kBLd + 2 * kBRows) * 4;
+}  // namespace dense_simt
+
+// Where keys and values lie: paged, or packed token rows.
+struct KvSource {
+  const void* k;
+  const void* v;
+  const int32_t* table;      // paged only
+  int32_t n_pages, page_tokens, max_pages;
+};
+
+// Element offset of the row of position j (-1: its page is out of range).
+template <bool PAGED>
+__device__ __forceinline__ int64_t kv_row(const KvSource& s, const DenseTable& t, int si, int grp, int64_t j) {
+  if (PAGED) {
+    const int64_t pi = j / s.page_tokens;
+    const int32_t page = s.table[(int64_t)t.slot[si] * s.max_pages + pi];
+    if (page < 0 || page >= s.n_pages) return -1;
+    return (((int64_t)page * t.G + grp) * s.page_tokens + (j - pi * s.page_tokens)) * kHeadDim;
+  }
+  return ((int64_t)(t.q_offset[si] + j) * t.G + grp) * kHeadDim;
+}
+
+// Copies `rows` rows of 256 floats into shared memory (stride kLd); row r from
+// src(r), zeros where src(r) is null.
+template <typename T, typename Src>
+__device__ __forceinline__ void simt_load_rows(float* dst, int rows, const T* any, Src src) {
+  for (int i = threadIdx.x; i < rows * (kHeadDim / 4); i += dense_simt::kThreads) {
+    const int r = i / (kHeadDim / 4), c = (i % (kHeadDim / 4)) * 4;
+    const T* p = src(r);
+    float* to = dst + r * dense_simt::kLd + c;
+    if constexpr (sizeof(T) == 4) {
+      sm100::cp_async16(sm100::smem_u32(to), p ? p + c : any, p ? 16u : 0u);
+    } else {
+      uint2 x = p ? *reinterpret_cast<const uint2*>(p + c) : make_uint2(0, 0);
+      const float2 a = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x.x));
+      const float2 b = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x.y));
+      *reinterpret_cast<float4*>(to) = make_float4(a.x, a.y, b.x, b.y);
+    }
+  }
+}
+
+__device__ __forceinline__ void simt_store4(float* dst, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void simt_store4(__nv_bfloat16* dst, float a, float b, float c, float d) {
+  __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<uint32_t*>(&x), *reinterpret_cast<uint32_t*>(&y));
+}
+
+// out[i][j] = a row (ra + i) . b row (rb + 16 j), rows of 256 floats
+template <int R, int N>
+__device__ __forceinline__ void simt_dots(const float* a, const float* b, int ra, int rb, float (&out)[R][N]) {
+  using dense_simt::kLd;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) out[i][j] = 0.f;
+#pragma unroll 2
+  for (int d = 0; d < kHeadDim; d += 4) {
+    float4 x[R], y[N];
+#pragma unroll
+    for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const float4*>(a + (ra + i) * kLd + d);
+#pragma unroll
+    for (int j = 0; j < N; ++j) y[j] = *reinterpret_cast<const float4*>(b + (rb + 16 * j) * kLd + d);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        out[i][j] = fmaf(x[i].x, y[j].x, out[i][j]);
+        out[i][j] = fmaf(x[i].y, y[j].y, out[i][j]);
+        out[i][j] = fmaf(x[i].z, y[j].z, out[i][j]);
+        out[i][j] = fmaf(x[i].w, y[j].w, out[i][j]);
+      }
+  }
+}
+
+// acc[i][16] += sum over n keys of p[row ra + i][key] * b[key][dims]; the
+// thread's dims are 4 tx + 64 jj.  With limit[i] < n only the first limit[i]
+// keys of row i are added.
+template <int R>
+__device__ __forceinline__ void simt_accumulate(const float* p, int ldp, const float* b, int ra, int tx, int n,
+                                                bool limited, const int (&limit)[R], float (&acc)[R][16]) {
+  using dense_simt::kLd;
+  for (int k = 0; k < n; k += 4) {
+    float4 w[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) w[i] = *reinterpret_cast<const float4*>(p + (ra + i) * ldp + k);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      float4 y[4];
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) y[jj] = *reinterpret_cast<const float4*>(b + (k + kk) * kLd + 4 * tx + 64 * jj);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float f = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
+        if (limited && k + kk >= limit[i]) continue;
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          acc[i][4 * jj] = fmaf(f, y[jj].x, acc[i][4 * jj]);
+          acc[i][4 * jj + 1] = fmaf(f, y[jj].y, acc[i][4 * jj + 1]);
+          acc[i][4 * jj + 2] = fmaf(f, y[jj].z, acc[i][4 * jj + 2]);
+          acc[i][4 * jj + 3] = fmaf(f, y[jj].w, acc[i][4 * jj + 3]);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int ROWS, bool PAGED>
+__global__ void __launch_bounds__(dense_simt::kThreads)
+    dense_fwd_simt_kernel(const __grid_constant__ DenseTable t, KvSource kv, const T* q, T* o, float* lse,
+                          float* part, int H, float scale) {
+  using namespace dense_simt;
+  constexpr int R = ROWS / 16;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;
+  float* Ks = Qs + ROWS * kLd;
+  float* Vs = Ks + kKeys * kLd;
+  float* Ps = Vs + kKeys * kLd;
+  int* ok = reinterpret_cast<int*>(Ps + ROWS * kPLd);         // key of the chunk can be attended
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, ra = ty * R;
+  const float s2 = scale * 1.4426950408889634f;
+  pdl_wait();
+  pdl_trigger();
+  DenseWalk walk;
+  walk.init(t, blockIdx.x);
+  DensePiece p;
+  DenseUnit x;
+  while (walk.next(t, p, x)) {
+    const int si = x.si;
+    auto q_at = [&](int r) -> int64_t {            // row of the token-major arrays, in heads
+      const int64_t row = x.row0 + r;
+      return (int64_t)(t.q_offset[si] + row / t.hpg) * H + (int64_t)x.grp * t.hpg + row % t.hpg;
+    };
+    auto load_kv = [&](float* dst, const void* base, int c, bool note) {
+      simt_load_rows(dst, kKeys, (const T*)base, [&](int r) -> const T* {
+        const int64_t j = (int64_t)c * kKeys + r;
+        const int64_t off = j < x.kv_len ? kv_row<PAGED>(kv, t, si, x.grp, j) : -1;
+        if (PAGED && j < x.kv_len && off < 0) report_error(kErrBadIndex);
+        return off < 0 ? nullptr : (const T*)base + off;
+      });
+      if (note && threadIdx.x < kKeys) {
+        const int64_t j = (int64_t)c * kKeys + threadIdx.x;
+        ok[threadIdx.x] = j < x.kv_len && kv_row<PAGED>(kv, t, si, x.grp, j) >= 0;
+      }
+      sm100::cp_async_commit();
+    };
+    simt_load_rows(Qs, ROWS, q, [&](int r) -> const T* { return r < x.nrows ? q + q_at(r) * kHeadDim : nullptr; });
+    load_kv(Ks, kv.k, p.c0, true);
+    load_kv(Vs, kv.v, p.c0, false);
+    int64_t pos[R];
+    float m[R], l[R], acc[R][16];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      pos[i] = t.pos0[si] + (x.row0 + ra + i) / t.hpg;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[i][k] = 0.f;
+    }
+    const int64_t first_pos = t.pos0[si] + x.row0 / t.hpg;
+    for (int c = p.c0; c < p.c1; ++c) {
+      const int64_t j0 = (int64_t)c * kKeys;
+      sm100::cp_async_wait<1>();
+      __syncthreads();
+      float s[R][4];
+      simt_dots<R, 4>(Qs, Ks, ra, tx, s);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float mc = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = tx + 16 * j;
+          s[i][j] = (j0 + key <= pos[i] && ok[key]) ? s[i][j] * s2 : -INFINITY;
+          mc = fmaxf(mc, s[i][j]);
+        }
+#pragma unroll
+        for (int off = 8; off; off >>= 1) mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, off));
+        const float mn = fmaxf(m[i], mc), mb = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m[i] - mb);          // 0 while the row has no key yet
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = exp2f(s[i][j] - mb);
+          sum += e;
+          Ps[(ra + i) * kPLd + tx + 16 * j] = e;
+        }
+#pragma unroll
+        for (int off = 8; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        l[i] = l[i] * f + sum;
+        m[i] = mn;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[i][k] *= f;
+      }
+      __syncthreads();                             // K and ok read, P written
+      if (c + 1 < p.c1) load_kv(Ks, kv.k, c + 1, true); else sm100::cp_async_commit();
+      sm100::cp_async_wait<1>();
+      __syncthreads();
+      int limit[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) limit[i] = (int)min((int64_t)kKeys, pos[i] - j0 + 1);
+      simt_accumulate<R>(Ps, kPLd, Vs, ra, tx, kKeys, j0 + kKeys - 1 > first_pos, limit, acc);
+      __syncthreads();
+      if (c + 1 < p.c1) load_kv(Vs, kv.v, c + 1, false); else sm100::cp_async_commit();
+    }
+    sm100::cp_async_wait_all();
+    __syncthreads();                               // shared memory free for the next piece
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (ra + i >= x.nrows) continue;
+      if (p.part < 0) {
+        const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
+        const int64_t at = q_at(ra + i);
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+          simt_store4(o + at * kHeadDim + 4 * tx + 64 * jj, acc[i][4 * jj] * inv, acc[i][4 * jj + 1] * inv,
+                      acc[i][4 * jj + 2] * inv, acc[i][4 * jj + 3] * inv);
+        if (lse && tx == 0) lse[at] = l[i] != 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
+      } else {
+        float* dst = part + ((int64_t)p.part * t.prows + ra + i) * dense::kPartFloats;
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+          *reinterpret_cast<float4*>(dst + 4 * tx + 64 * jj) =
+              make_float4(acc[i][4 * jj], acc[i][4 * jj + 1], acc[i][4 * jj + 2], acc[i][4 * jj + 3]);
+        if (tx == 0) {
+          dst[kHeadDim] = m[i];
+          dst[kHeadDim + 1] = l[i];
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ gradient
+struct DenseBwdArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* lse;        // [T][H]
+  const float* delta;      // [T][H]
+  const void* dout;
+  void* dq;
+  void* dk;
+  void* dv;
+  int H;
+  float scale;
+};
+
+// delta[i][h] = dout[i][h] . o[i][h], one warp per row of the segments.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    dense_delta_kernel(SegTable st, const T* o, const T* dout, float* delta, int H) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int item = (int)(w / H);
+  if (item >= st.item0[st.n]) return;
+  const int si = find_segment(st, item);
+  const int64_t at = (int64_t)(st.q_offset[si] + item - st.item0[si]) * H + w % H;
+  Vec8<T> a, b;
+  a.load(o + at * kHeadDim + lane * 8);
+  b.load(dout + at * kHeadDim + lane * 8);
+  float fa[8], fb[8], s = 0.f;
+  a.get(fa);
+  b.get(fb);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaf(fa[i], fb[i], s);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (lane == 0) delta[at] = s;
+}
+
+// P and dS of 64 rows x 32 keys into Ps and Ds ([row][key]); row statistics in
+// st_lse (log2 units) and st_delta; masked entries are zero.  row_pos0: the
+// tile's first row, in rows of the segment.
+__device__ __forceinline__ void simt_p_ds(const float* Qs, const float* Os, const float* Ks, const float* Vs,
+                                          float* Ps, float* Ds, const float* st_lse, const float* st_delta,
+                                          int64_t row0, int nrows, int hpg, int64_t j0, int64_t n_keys, float s2) {
+  using namespace dense_simt;
+  const int tx = threadIdx.x & 15, ra = (threadIdx.x >> 4) * 4;
+  float s[4][2], dp[4][2];
+  simt_dots<4, 2>(Qs, Ks, ra, tx, s);
+  simt_dots<4, 2>(Os, Vs, ra, tx, dp);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ra + i;
+    const int64_t pos = (row0 + r) / hpg;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int key = tx + 16 * j;
+      const bool seen = r < nrows && j0 + key <= pos && j0 + key < n_keys;
+      const float p = seen ? exp2f(fmaf(s[i][j], s2, -st_lse[r])) : 0.f;
+      Ps[r * kBLd + key] = p;
+      Ds[r * kBLd + key] = seen ? p * (dp[i][j] - st_delta[r]) : 0.f;
+    }
+  }
+}
+
+// dq of one (64-row tile, group): loops over its keys.
+template <typename T>
+__global__ void __launch_bounds__(dense_simt::kThreads)
+    dense_dq_simt_kernel(const __grid_constant__ DenseTable t, DenseBwdArgs a) {
+  using namespace dense_simt;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;
+  float* Os = Qs + kBRows * kLd;
+  float* Ks = Os + kBRows * kLd;
+  float* Vs = Ks + kBKeys * kLd;
+  float* Ps = Vs + kBKeys * kLd;
+  float* Ds = Ps + kBRows * kBLd;
+  float* st_lse = Ds + kBRows * kBLd;
+  float* st_delta = st_lse + kBRows;
+  const float s2 = a.scale * 1.4426950408889634f;
+  const int tx = threadIdx.x & 15, ra = (threadIdx.x >> 4) * 4;
+  pdl_wait();
+  pdl_trigger();
+  const DenseUnit x = dense_unit(t, blockIdx.x);
+  const int si = x.si;
+  auto q_at = [&](int r) -> int64_t {
+    const int64_t row = x.row0 + r;
+    return (int64_t)(t.q_offset[si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg + row % t.hpg;
+  };
+  auto rows_of = [&](const void* base) {
+    return [&, base](int r) -> const T* {
+      return r < x.nrows ? (const T*)base + q_at(r) * kHeadDim : nullptr;
+    };
+  };
+  simt_load_rows(Qs, kBRows, (const T*)a.q, rows_of(a.q));
+  simt_load_rows(Os, kBRows, (const T*)a.dout, rows_of(a.dout));
+  if (threadIdx.x < kBRows) {
+    const bool v = threadIdx.x < x.nrows;
+    st_lse[threadIdx.x] = v ? a.lse[q_at(threadIdx.x)] * 1.4426950408889634f : 0.f;
+    st_delta[threadIdx.x] = v ? a.delta[q_at(threadIdx.x)] : 0.f;
+  }
+  float acc[4][16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[i][k] = 0.f;
+  const int64_t first_pos = x.row0 / t.hpg;
+  for (int64_t j0 = 0; j0 < x.kv_len; j0 += kBKeys) {
+    __syncthreads();
+    auto keys_of = [&](const void* base) {
+      return [&, base](int r) -> const T* {
+        const int64_t j = j0 + r;
+        return j < x.kv_len ? (const T*)base + ((int64_t)(t.q_offset[si] + j) * t.G + x.grp) * kHeadDim : nullptr;
+      };
+    };
+    simt_load_rows(Ks, kBKeys, (const T*)a.k, keys_of(a.k));
+    simt_load_rows(Vs, kBKeys, (const T*)a.v, keys_of(a.v));
+    sm100::cp_async_wait_all();
+    __syncthreads();
+    simt_p_ds(Qs, Os, Ks, Vs, Ps, Ds, st_lse, st_delta, x.row0, x.nrows, t.hpg, j0, x.kv_len, s2);
+    __syncthreads();
+    int limit[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) limit[i] = (int)min((int64_t)kBKeys, (x.row0 + ra + i) / t.hpg - j0 + 1);
+    simt_accumulate<4>(Ds, kBLd, Ks, ra, tx, kBKeys, j0 + kBKeys - 1 > first_pos, limit, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (ra + i >= x.nrows) continue;
+    T* dst = (T*)a.dq + q_at(ra + i) * kHeadDim;
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj)
+      simt_store4(dst + 4 * tx + 64 * jj, acc[i][4 * jj] * a.scale, acc[i][4 * jj + 1] * a.scale,
+                  acc[i][4 * jj + 2] * a.scale, acc[i][4 * jj + 3] * a.scale);
+  }
+}
+
+// dk and dv of one (32-key tile, group): loops over the rows that see it.  The
+// block index counts a segment's key tiles from its start (most rows first);
+// a thread owns 4 keys x 8 dims of both.
+template <typename T>
+__global__ void __launch_bounds__(dense_simt::kThreads)
+    dense_dkv_simt_kernel(const __grid_constant__ SegTable st, int G, int hpg, DenseBwdArgs a) {
+  using namespace dense_simt;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;
+  float* Os = Qs + kBRows * kLd;
+  float* Ks = Os + kBRows * kLd;
+  float* Vs = Ks + kBKeys * kLd;
+  float* Ps = Vs + kBKeys * kLd;
+  float* Ds = Ps + kBRows * kBLd;
+  float* st_lse = Ds + kBRows * kBLd;
+  float* st_delta = st_lse + kBRows;
+  const float s2 = a.scale * 1.4426950408889634f;
+  const int kq = (threadIdx.x >> 5) * 4, dl = (threadIdx.x & 31) * 4;
+  pdl_wait();
+  pdl_trigger();
+  const int tile = blockIdx.x / G, grp = blockIdx.x - tile * G;
+  const int si = find_segment(st, tile);
+  const int64_t j0 = (int64_t)(tile - st.item0[si]) * kBKeys;
+  const int64_t n = st.q_len[si], q0 = st.q_offset[si];
+  auto key_at = [&](int r) -> int64_t { return ((q0 + j0 + r) * G + grp) * kHeadDim; };
+  auto keys_of = [&](const void* base) {
+    return [&, base](int r) -> const T* { return j0 + r < n ? (const T*)base + key_at(r) : nullptr; };
+  };
+  simt_load_rows(Ks, kBKeys, (const T*)a.k, keys_of(a.k));
+  simt_load_rows(Vs, kBKeys, (const T*)a.v, keys_of(a.v));
+  float dk[4][8], dv[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dk[i][k] = dv[i][k] = 0.f;
+  for (int64_t row0 = j0 * hpg; row0 < n * hpg; row0 += kBRows) {
+    const int nrows = (int)min((int64_t)kBRows, n * hpg - row0);
+    auto q_at = [&](int r) -> int64_t {
+      const int64_t row = row0 + r;
+      return (q0 + row / hpg) * a.H + (int64_t)grp * hpg + row % hpg;
+    };
+    auto rows_of = [&](const void* base) {
+      return [&, base](int r) -> const T* {
+        return r < nrows ? (const T*)base + q_at(r) * kHeadDim : nullptr;
+      };
+    };
+    __syncthreads();
+    simt_load_rows(Qs, kBRows, (const T*)a.q, rows_of(a.q));
+    simt_load_rows(Os, kBRows, (const T*)a.dout, rows_of(a.dout));
+    if (threadIdx.x < kBRows) {
+      const bool v = threadIdx.x < nrows;
+      st_lse[threadIdx.x] = v ? a.lse[q_at(threadIdx.x)] * 1.4426950408889634f : 0.f;
+      st_delta[threadIdx.x] = v ? a.delta[q_at(threadIdx.x)] : 0.f;
+    }
+    sm100::cp_async_wait_all();
+    __syncthreads();
+    simt_p_ds(Qs, Os, Ks, Vs, Ps, Ds, st_lse, st_delta, row0, nrows, hpg, j0, n, s2);
+    __syncthreads();
+    // keys of the tile after the first row's position: a row before a key does not touch it
+    const bool limited = j0 + kBKeys - 1 > row0 / hpg;
+    for (int r = 0; r < nrows; ++r) {
+      const float4 p = *reinterpret_cast<const float4*>(Ps + r * kBLd + kq);
+      const float4 s = *reinterpret_cast<const float4*>(Ds + r * kBLd + kq);
+      const int64_t pos = limited ? (row0 + r) / hpg : 0;
+      const float pp[4] = {p.x, p.y, p.z, p.w}, ss[4] = {s.x, s.y, s.z, s.w};
+      float4 x[2], y[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        x[h] = *reinterpret_cast<const float4*>(Qs + r * kLd + dl + 128 * h);
+        y[h] = *reinterpret_cast<const float4*>(Os + r * kLd + dl + 128 * h);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (limited && j0 + kq + i > pos) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          dk[i][4 * h] = fmaf(ss[i], x[h].x, dk[i][4 * h]);
+          dk[i][4 * h + 1] = fmaf(ss[i], x[h].y, dk[i][4 * h + 1]);
+          dk[i][4 * h + 2] = fmaf(ss[i], x[h].z, dk[i][4 * h + 2]);
+          dk[i][4 * h + 3] = fmaf(ss[i], x[h].w, dk[i][4 * h + 3]);
+          dv[i][4 * h] = fmaf(pp[i], y[h].x, dv[i][4 * h]);
+          dv[i][4 * h + 1] = fmaf(pp[i], y[h].y, dv[i][4 * h + 1]);
+          dv[i][4 * h + 2] = fmaf(pp[i], y[h].z, dv[i][4 * h + 2]);
+          dv[i][4 * h + 3] = fmaf(pp[i], y[h].w, dv[i][4 * h + 3]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (j0 + kq + i >= n) continue;
+    const int64_t at = key_at(kq + i) + dl;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      simt_store4((T*)a.dk + at + 128 * h, dk[i][4 * h] * a.scale, dk[i][4 * h + 1] * a.scale,
+                  dk[i][4 * h + 2] * a.scale, dk[i][4 * h + 3] * a.scale);
+      simt_store4((T*)a.dv + at + 128 * h, dv[i][4 * h], dv[i][4 * h + 1], dv[i][4 * h + 2], dv[i][4 * h + 3]);
+    }
+  }
+}
+
+}  // namespace qsa

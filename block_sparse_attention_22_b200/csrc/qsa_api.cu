@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <mutex>
 #include <functional>
+#include <utility>
 #include <vector>
 
 #include "qsa_internal.cuh"
@@ -978,6 +979,8 @@ QSA_API qsa_status_t qsa_sparse_attn_bwd(const qsa_config_t* cfg, const qsa_cach
       });
 }
 
+#include "dense_api.cuh"
+
 QSA_API size_t qsa_workspace_size(const qsa_config_t* cfg, const qsa_segment_t* segs,
                                   int32_t n_segs, int32_t n_tokens, qsa_op_t op) {
   if (check_cfg(cfg) != QSA_OK || check_segments(segs, n_segs, n_tokens, nullptr, 0) != QSA_OK)
@@ -994,6 +997,17 @@ QSA_API size_t qsa_workspace_size(const qsa_config_t* cfg, const qsa_segment_t* 
     case QSA_OP_ATTN_UNION: return union_plan(g, segs, n_segs).ws;
     case QSA_OP_FORWARD_PREFIXED:
       return fwd_layout(g, segs, n_segs, n_tokens, cfg->dtype == QSA_DTYPE_BF16, false, true).total;
+    case QSA_OP_PAGED_ATTN:
+    case QSA_OP_PROMPT_ATTN: {
+      size_t ws = SIZE_MAX;
+      if (guarded([&]() -> qsa_status_t {
+            ws = dense_fwd_ws(g, cfg->dtype == QSA_DTYPE_BF16, segs, n_segs);
+            return QSA_OK;
+          }) != QSA_OK)
+        return SIZE_MAX;
+      return ws;
+    }
+    case QSA_OP_PROMPT_ATTN_BWD: return seg_rows(segs, n_segs) > 0 ? dense_bwd_ws(g, n_tokens) : 0;
   }
   return SIZE_MAX;
 }

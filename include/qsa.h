@@ -78,8 +78,8 @@ typedef enum {
   QSA_ERR_WORKSPACE = 3,    /* workspace NULL or smaller than qsa_workspace_size()     */
   QSA_ERR_CUDA = 4,         /* a CUDA runtime call or kernel launch failed             */
   QSA_ERR_TIMEOUT = 5,      /* a bounded device-side wait gave up (qsa_device_status)  */
-  QSA_ERR_BAD_INDEX = 6     /* a caller-supplied sel entry was out of range and skipped
-                               (qsa_device_status)                                     */
+  QSA_ERR_BAD_INDEX = 6     /* a caller-supplied sel or page table entry was out of range
+                               and skipped (qsa_device_status)                         */
 } qsa_status_t;
 
 typedef enum { QSA_DTYPE_F32 = 0, QSA_DTYPE_BF16 = 1 } qsa_dtype_t;
@@ -125,7 +125,10 @@ typedef enum {
   QSA_OP_FORWARD = 4,
   QSA_OP_FORWARD_LOWMEM = 5,
   QSA_OP_ATTN_UNION = 6,
-  QSA_OP_FORWARD_PREFIXED = 7
+  QSA_OP_FORWARD_PREFIXED = 7,
+  QSA_OP_PAGED_ATTN = 8,
+  QSA_OP_PROMPT_ATTN = 9,
+  QSA_OP_PROMPT_ATTN_BWD = 10
 } qsa_op_t;
 
 /* A cached prefix that a segment's sequence shares with other sequences:
@@ -138,6 +141,22 @@ typedef struct {
   int32_t slot;
   int32_t blocks;
 } qsa_prefix_t;
+
+/* A paged K/V cache (device memory, caller-owned).  Position p of the sequence
+ * in table row `slot` lives in page table[slot][p / page_tokens], at row
+ * p % page_tokens of that page.  Pages may be shared by table rows that only
+ * read them.  A slot cache of qsa_cache_t is the case page_tokens = n_cap,
+ * n_pages = n_slots, table[slot] = { slot }. */
+typedef struct {
+  void* k;                /* [n_pages][n_kv_groups][page_tokens][head_dim]  keys, rotated */
+  void* v;                /* [n_pages][n_kv_groups][page_tokens][head_dim]  values        */
+  const int32_t* table;   /* device [n_rows][max_pages] page numbers; entries past a
+                             sequence's last page are not read                            */
+  int32_t n_pages;
+  int32_t page_tokens;    /* tokens per page: a multiple of 16                            */
+  int32_t n_rows;         /* table rows                                                   */
+  int32_t max_pages;      /* table entries per row                                        */
+} qsa_pages_t;
 
 /*
  * Key pooling + block position encoding (design report, QSA item: keys are
@@ -317,6 +336,96 @@ qsa_status_t qsa_forward_lowmem(const qsa_config_t* cfg, const qsa_cache_t* cach
                                 const void* q, const void* q_idx, const float* w, void* o, float* lse,
                                 int32_t* sel, int32_t* nsel, void* workspace, size_t ws_bytes,
                                 void* stream);
+
+/*
+ * Appends the keys and values of new tokens to a paged cache, with the
+ * position rotation applied on the way (Miles docs section 1: rotary base 1e7
+ * at rotary percent 0.25).  For every token i of a segment, at position t, and
+ * every KV group g:
+ *   K[page][g][row][:] = RoPE_t(k[i][g]),   V[page][g][row][:] = v[i][g],
+ * page = table[slot][t / page_tokens], row = t % page_tokens.  RoPE rotates
+ * the first floor(head_dim*rope_fraction) (even) dims in rotate-half pairs,
+ * angles formed in fp64, products in fp32, one rounding to the I/O dtype.
+ * With q, also q_out[i][h] = RoPE_t(q[i][h]) for every query head.
+ * k, v: device, row (i, g) at k + i*ld_k + g*head_dim elements (slices of a
+ * fused projection need no copy); q likewise with ld_q; the leading
+ * dimensions are multiples of 16 bytes and at least one token's row.  q and
+ * q_out may both be NULL.  q_out: device [T][n_q_heads][head_dim], dense; it
+ * may be q itself when ld_q == n_q_heads*head_dim.  No other output may
+ * overlap an input.  Rows of q_out and of the cache that belong to no token
+ * of the batch are left as they were.
+ * Two tokens of one call must not share a cache row.  A page number outside
+ * [0, n_pages) is skipped (its tokens are not stored) and reported by
+ * qsa_device_status as QSA_ERR_BAD_INDEX.
+ */
+qsa_status_t qsa_append_kv(const qsa_config_t* cfg, const qsa_pages_t* pages,
+                           const qsa_segment_t* segs, int32_t n_segs, int32_t n_tokens,
+                           const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                           const void* q, int64_t ld_q, void* q_out, void* stream);
+
+/*
+ * Dense causal GQA attention of new tokens over a paged cache: decode, a few
+ * tokens, and chunks of a prompt, in one call.  It is qsa_sparse_attn_fwd with
+ * every block kept (the same result where budget_tokens covers the context).
+ * For every query token i at position t and head h (group g):
+ *   o[i][h][:] = sum_{j<=t} softmax_j(scale * q[i][h] . K_j) V_j,
+ *   lse[i][h]  = log sum_{j<=t} exp(scale * q[i][h] . K_j)       (natural log),
+ * K_j, V_j the cache rows of position j of the segment's table row.  The cache
+ * must already hold every token <= pos0+q_len-1 (qsa_append_kv).  Cache rows
+ * of later positions, and pages' unused rows, may hold anything, infinities
+ * and NaN included.
+ * q, o: device [T][n_q_heads][head_dim] (I/O dtype); lse: device fp32
+ * [T][n_q_heads] or NULL.  Rows of o and lse of no segment are not written.
+ * A page number outside [0, n_pages) is skipped (its tokens contribute
+ * nothing) and reported by qsa_device_status as QSA_ERR_BAD_INDEX; a query
+ * left without any key gets o = 0 and lse = -inf.
+ * Token rows of different segments must not overlap (QSA_ERR_INVALID_ARG).
+ * workspace >= qsa_workspace_size(..., QSA_OP_PAGED_ATTN) bytes (may be NULL
+ * when that size is 0); contents on entry are ignored; calls whose work may
+ * overlap on the GPU need one each.  The result does not depend on the order
+ * in which the GPU runs the work: repeated calls give the same bits.
+ */
+qsa_status_t qsa_paged_attn_fwd(const qsa_config_t* cfg, const qsa_pages_t* pages,
+                                const qsa_segment_t* segs, int32_t n_segs, int32_t n_tokens,
+                                const void* q, void* o, float* lse, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/*
+ * Dense causal GQA attention over whole prompts of different lengths, packed
+ * one after another (training and prefill without a cache).  Segment i is the
+ * prompt at token rows q_offset .. q_offset+q_len-1 of every array; its pos0
+ * must be 0 and its slot is not read.  For every token i and head h (group g),
+ * over the tokens j <= i of the same prompt:
+ *   o[i][h][:] = sum_j softmax_j(scale * q[i][h] . k[j][g]) v[j][g],  lse as above.
+ * q, o: device [T][n_q_heads][head_dim]; k, v: device [T][n_kv_groups][head_dim]
+ * (I/O dtype, already rotated); lse: device fp32 [T][n_q_heads] or NULL.
+ * Rows of no segment are neither read nor written.  Overlaps, workspace
+ * (QSA_OP_PROMPT_ATTN) and repeatability as qsa_paged_attn_fwd.
+ */
+qsa_status_t qsa_prompt_attn_fwd(const qsa_config_t* cfg, const qsa_segment_t* segs,
+                                 int32_t n_segs, int32_t n_tokens, const void* q, const void* k,
+                                 const void* v, void* o, float* lse, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/*
+ * Backward of qsa_prompt_attn_fwd: for the loss sum of dout . o, with
+ * P_ij = exp(scale q_i . k_j - lse_i) and delta_i = dout_i . o_i,
+ *   dq_i = scale sum_j P_ij (dout_i . v_j - delta_i) k_j
+ *   dk_j = scale sum_{i,h} P_ij (dout_i . v_j - delta_i) q_i
+ *   dv_j = sum_{i,h} P_ij dout_i
+ * (the sums over i, h: every query head of the group).  q, k, v, o, lse as the
+ * forward read and wrote them; dout: device [T][n_q_heads][head_dim].  dq, dk,
+ * dv: device, laid out as q, k, v, in the I/O dtype; rows of the segments are
+ * written (not accumulated into), other rows are left as they were.  fp32
+ * accumulation in a fixed order, one rounding at the end: repeated calls give
+ * the same bits.  bf16: P and the score gradients are rounded to bf16 for the
+ * tensor-core products.  workspace: QSA_OP_PROMPT_ATTN_BWD.
+ */
+qsa_status_t qsa_prompt_attn_bwd(const qsa_config_t* cfg, const qsa_segment_t* segs,
+                                 int32_t n_segs, int32_t n_tokens, const void* q, const void* k,
+                                 const void* v, const void* o, const float* lse, const void* dout,
+                                 void* dq, void* dk, void* dv, void* workspace, size_t ws_bytes,
+                                 void* stream);
 
 /*
  * qsa_select_topk without a caller workspace, for callers that cannot call
