@@ -5,6 +5,7 @@
 #include "append.cuh"
 #include "dense.cuh"
 #include "dense_simt.cuh"
+#include "dense_tc.cuh"
 
 namespace qsa {
 namespace {
@@ -190,9 +191,15 @@ qsa_status_t for_each_dense(const Geo& g, std::vector<qsa_segment_t> segs, const
 // Segments of few query rows (decode) and the others, with the shape of their launches.
 void dense_kinds(const Geo& g, bool tc, const qsa_segment_t* segs, int n, std::vector<qsa_segment_t>& narrow,
                  std::vector<qsa_segment_t>& wide, DenseKind& kn, DenseKind& kw) {
-  (void)tc;
-  kn = {dense_simt::kRowsNarrow, dense_simt::kKeys, kNumSms};
-  kw = {dense_simt::kRowsWide, dense_simt::kKeys, kNumSms};
+  if (tc) {
+    using N = dense_tc::Shape<1>;
+    using W = dense_tc::Shape<2>;
+    kn = {N::kRows, N::kKeys, N::kGrid};
+    kw = {W::kRows, W::kKeys, W::kGrid};
+  } else {
+    kn = {dense_simt::kRowsNarrow, dense_simt::kKeys, kNumSms};
+    kw = {dense_simt::kRowsWide, dense_simt::kKeys, kNumSms};
+  }
   for (int i = 0; i < n; ++i)
     if (segs[i].q_len > 0) ((int64_t)segs[i].q_len * g.hpg <= kn.rows ? narrow : wide).push_back(segs[i]);
 }
@@ -216,16 +223,53 @@ size_t dense_fwd_ws(const Geo& g, bool tc, const qsa_segment_t* segs, int n) {
 }
 
 // ------------------------------------------------------------------ forward
-template <typename T, int ROWS, bool PAGED>
+template <int ROWS, bool PAGED>
 cudaError_t launch_dense_simt(const Geo& g, const DenseTable& t, const KvSource& kv, const void* q, void* o,
                               float* lse, float* part, cudaStream_t st) {
   const int smem = dense_simt::fwd_smem(ROWS);
-  cudaError_t e = cudaFuncSetAttribute(dense_fwd_simt_kernel<T, ROWS, PAGED>,
+  cudaError_t e = cudaFuncSetAttribute(dense_fwd_simt_kernel<ROWS, PAGED>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   count_launch();
-  return launch_chained(dense_fwd_simt_kernel<T, ROWS, PAGED>, dim3(t.grid), dim3(dense_simt::kThreads), smem, st, t,
-                        kv, (const T*)q, (T*)o, lse, part, g.H, g.scale);
+  return launch_chained(dense_fwd_simt_kernel<ROWS, PAGED>, dim3(t.grid), dim3(dense_simt::kThreads), smem, st, t,
+                        kv, (const float*)q, (float*)o, lse, part, g.H, g.scale);
+}
+
+// Map over rows of 256 dims (paged: every cache row; packed: a token's groups
+// side by side), in boxes of `box` rows x 64 dims, 128-byte swizzled.
+bool make_dense_map(CUtensorMap* m, const void* base, int64_t rows, int groups, int box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)kHeadDim * groups, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)kHeadDim * groups * 2};
+  cuuint32_t boxes[2] = {64, (cuuint32_t)box};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CG, bool PAGED>
+cudaError_t launch_dense_tc(const DenseTable& t, const CUtensorMap& mk, const CUtensorMap& mv, const DenseTcArgs& a,
+                            cudaStream_t st) {
+  auto kernel = dense_fwd_tc_kernel<CG, PAGED>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense_tc::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(t.grid * CG);
+  cfg.blockDim = dim3(dense_tc::kThreads);
+  cfg.dynamicSmemBytes = dense_tc::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 1 ? 1 : 2;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, mk, mv, t, a);
 }
 
 template <typename T>
@@ -236,21 +280,38 @@ cudaError_t launch_dense_combine(const Geo& g, const DenseTable& t, const DenseS
                         part, (T*)o, lse, g.H);
 }
 
-template <typename T, bool PAGED>
-qsa_status_t run_dense_fwd(const Geo& g, const qsa_segment_t* segs, int n, const KvSource& kv, const void* q, void* o,
-                           float* lse, void* ws, size_t ws_bytes, cudaStream_t st) {
-  const size_t need = dense_fwd_ws(g, sizeof(T) == 2, segs, n);
+// kv_rows, kv_groups: the shape of the tensor map over K and V (make_dense_map).
+template <bool PAGED>
+qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int n, const KvSource& kv,
+                           int64_t kv_rows, int kv_groups, const void* q, void* o, float* lse, void* ws,
+                           size_t ws_bytes, cudaStream_t st) {
+  const size_t need = dense_fwd_ws(g, tc, segs, n);
   if (need == SIZE_MAX) return QSA_ERR_UNSUPPORTED;
   if (need > 0 && (!ws || ws_bytes < need)) return QSA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return QSA_ERR_INVALID_ARG;
   std::vector<qsa_segment_t> narrow, wide;
   DenseKind kn, kw;
-  dense_kinds(g, sizeof(T) == 2, segs, n, narrow, wide, kn, kw);
+  dense_kinds(g, tc, segs, n, narrow, wide, kn, kw);
+  float* part = (float*)ws;
+  CUtensorMap mk, mv;
+  DenseTcArgs a;
+  if (tc) {
+    a = {kv, (const __nv_bfloat16*)q, (__nv_bfloat16*)o, lse, part, g.H, PAGED ? dense_box(kv.page_tokens) : 64,
+         g.scale};
+    if (!make_dense_map(&mk, kv.k, kv_rows, kv_groups, a.box) || !make_dense_map(&mv, kv.v, kv_rows, kv_groups, a.box))
+      return QSA_ERR_CUDA;
+  }
   auto run = [&](bool is_wide) {
     return [&, is_wide](const DenseTable& t, const DenseSplits& sp) -> qsa_status_t {
-      cudaError_t e = is_wide ? launch_dense_simt<T, dense_simt::kRowsWide, PAGED>(g, t, kv, q, o, lse, (float*)ws, st)
-                              : launch_dense_simt<T, dense_simt::kRowsNarrow, PAGED>(g, t, kv, q, o, lse, (float*)ws, st);
-      if (e == cudaSuccess && sp.n > 0) e = launch_dense_combine<T>(g, t, sp, (const float*)ws, o, lse, st);
+      cudaError_t e;
+      if (tc)
+        e = is_wide ? launch_dense_tc<2, PAGED>(t, mk, mv, a, st) : launch_dense_tc<1, PAGED>(t, mk, mv, a, st);
+      else
+        e = is_wide ? launch_dense_simt<dense_simt::kRowsWide, PAGED>(g, t, kv, q, o, lse, part, st)
+                    : launch_dense_simt<dense_simt::kRowsNarrow, PAGED>(g, t, kv, q, o, lse, part, st);
+      if (e == cudaSuccess && sp.n > 0)
+        e = tc ? launch_dense_combine<__nv_bfloat16>(g, t, sp, part, o, lse, st)
+               : launch_dense_combine<float>(g, t, sp, part, o, lse, st);
       return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
     };
   };
@@ -372,10 +433,9 @@ QSA_API qsa_status_t qsa_paged_attn_fwd(const qsa_config_t* cfg, const qsa_pages
     if (!q || !o || !aligned16(q) || !aligned16(o) || ((uintptr_t)lse & 3u)) return QSA_ERR_INVALID_ARG;
     const Geo g = make_geo(cfg, nullptr);
     const KvSource kv{pages->k, pages->v, pages->table, pages->n_pages, pages->page_tokens, pages->max_pages};
-    return cfg->dtype == QSA_DTYPE_BF16
-               ? run_dense_fwd<__nv_bfloat16, true>(g, segs, n_segs, kv, q, o, lse, workspace, ws_bytes,
-                                                    (cudaStream_t)stream)
-               : run_dense_fwd<float, true>(g, segs, n_segs, kv, q, o, lse, workspace, ws_bytes, (cudaStream_t)stream);
+    return run_dense_fwd<true>(g, cfg->dtype == QSA_DTYPE_BF16, segs, n_segs, kv,
+                               (int64_t)pages->n_pages * cfg->n_kv_groups * pages->page_tokens, 1, q, o, lse, workspace,
+                               ws_bytes, (cudaStream_t)stream);
   });
 }
 
@@ -392,11 +452,8 @@ QSA_API qsa_status_t qsa_prompt_attn_fwd(const qsa_config_t* cfg, const qsa_segm
       return QSA_ERR_INVALID_ARG;
     const Geo g = make_geo(cfg, nullptr);
     const KvSource kv{k, v, nullptr, 0, 0, 0};
-    return cfg->dtype == QSA_DTYPE_BF16
-               ? run_dense_fwd<__nv_bfloat16, false>(g, segs, n_segs, kv, q, o, lse, workspace, ws_bytes,
-                                                     (cudaStream_t)stream)
-               : run_dense_fwd<float, false>(g, segs, n_segs, kv, q, o, lse, workspace, ws_bytes,
-                                             (cudaStream_t)stream);
+    return run_dense_fwd<false>(g, cfg->dtype == QSA_DTYPE_BF16, segs, n_segs, kv, n_tokens, cfg->n_kv_groups, q, o,
+                                lse, workspace, ws_bytes, (cudaStream_t)stream);
   });
 }
 

@@ -139,9 +139,9 @@ __device__ __forceinline__ void simt_accumulate(const float* p, int ldp, const f
   }
 }
 
-template <typename T, int ROWS, bool PAGED>
+template <int ROWS, bool PAGED>
 __global__ void __launch_bounds__(dense_simt::kThreads)
-    dense_fwd_simt_kernel(const __grid_constant__ DenseTable t, KvSource kv, const T* q, T* o, float* lse,
+    dense_fwd_simt_kernel(const __grid_constant__ DenseTable t, KvSource kv, const float* q, float* o, float* lse,
                           float* part, int H, float scale) {
   using namespace dense_simt;
   constexpr int R = ROWS / 16;
@@ -166,11 +166,11 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
       return (int64_t)(t.q_offset[si] + row / t.hpg) * H + (int64_t)x.grp * t.hpg + row % t.hpg;
     };
     auto load_kv = [&](float* dst, const void* base, int c, bool note) {
-      simt_load_rows(dst, kKeys, (const T*)base, [&](int r) -> const T* {
+      simt_load_rows(dst, kKeys, (const float*)base, [&](int r) -> const float* {
         const int64_t j = (int64_t)c * kKeys + r;
         const int64_t off = j < x.kv_len ? kv_row<PAGED>(kv, t, si, x.grp, j) : -1;
         if (PAGED && j < x.kv_len && off < 0) report_error(kErrBadIndex);
-        return off < 0 ? nullptr : (const T*)base + off;
+        return off < 0 ? nullptr : (const float*)base + off;
       });
       if (note && threadIdx.x < kKeys) {
         const int64_t j = (int64_t)c * kKeys + threadIdx.x;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
       }
       sm100::cp_async_commit();
     };
-    simt_load_rows(Qs, ROWS, q, [&](int r) -> const T* { return r < x.nrows ? q + q_at(r) * kHeadDim : nullptr; });
+    simt_load_rows(Qs, ROWS, q, [&](int r) -> const float* { return r < x.nrows ? q + q_at(r) * kHeadDim : nullptr; });
     load_kv(Ks, kv.k, p.c0, true);
     load_kv(Vs, kv.v, p.c0, false);
     int64_t pos[R];

@@ -1,0 +1,571 @@
+// dense_tc.cuh -- dense causal GQA attention, bf16, on tcgen05 tensor cores:
+// forward over a paged cache and over packed prompts.
+//
+// A unit (dense.cuh) is a tile of query rows of one KV group -- row = token *
+// hpg + head, so the heads of a group share every key and value that is
+// loaded -- against keys 0 .. the last token's position, in chunks:
+//   S[row, key] = Q[row, :] . K[key, :]        (K = 256 dims)
+//   O[row, :]  += P[row, key] V[key, :]        (N = 256 dims)
+// with one pass over the keys: a row's reference maximum moves only when a
+// chunk's maximum exceeds it by more than 8 (log2 units), then O and the row's
+// sum so far are rescaled in tensor memory; P stays below 2^8 in between.  P
+// is rounded to bf16 for its product (relative error 2^-8 of each weight, as
+// in the sparse kernels); the row sum adds the unrounded values in fp32.
+//
+// Two forms (CG = CTAs per unit):
+//   CG = 1  128 rows, chunks of 64 keys, one CTA: units of few rows (decode),
+//           bound by the HBM reads of K and V.
+//   CG = 2  256 rows, chunks of 128 keys, a CTA pair (cta_group::2): each CTA
+//           owns 128 rows, loads half of K's keys and half of V's dims, and
+//           the pair's MMAs read both halves, so a key crosses L2 once per
+//           256 rows.  A lone CTA would need 64 bytes per cycle and SM at full
+//           tensor rate (17 TB/s over the GPU), a pair needs half.
+//
+// Per CTA 12 warps: eight softmax warps (two per TMEM lane quadrant, each
+// thread one row and half of a chunk's keys and dims), one TMA producer that
+// fills a ring of five 32 KiB slots in the order the MMAs consume them (K0,
+// K1, V0, K2, V1, ...), one MMA warp (of rank 0; rank 1's forwards "slot
+// full"), two warps that load Q for the next unit.  TMEM: two S buffers (P
+// overwrites the first half of its S), O in columns 256..511.
+//
+// Keys that do not count -- beyond the sequence, on a page out of range, after
+// a row's position -- may hold anything: their scores are replaced by -inf;
+// V rows beyond the sequence and of bad pages are zeroed in shared memory
+// before the product (0 * NaN would spread).  Values of the tile's own tokens
+// (visible to some rows only) are checked for infinities and NaN while Q is
+// loaded; such a key's V row is zeroed too and its contribution added in the
+// epilogue to the rows that attend it.
+// Every mbarrier wait is bounded; a timeout records an error and the CTA
+// drains and returns.
+#pragma once
+#include "qsa_internal.cuh"
+#include "sm100.cuh"
+#include "attn_tc.cuh"
+#include "attn_union_tc.cuh"
+#include "dense.cuh"
+#include "dense_simt.cuh"
+
+namespace qsa {
+namespace dense_tc {
+constexpr int kWarps = 12;
+constexpr int kThreads = kWarps * 32;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 2;
+constexpr int kSlots = 5;
+constexpr int kSlotBytes = 32768;
+constexpr int kQBytes = 65536;                        // 128 rows x 256 dims, 4 slabs of 16 KiB
+constexpr int kOffQ = kSlots * kSlotBytes;            // 163840
+constexpr int kOffCtl = kOffQ + kQBytes;              // 229376
+constexpr int kCtlBytes = 2048;
+constexpr int kSmemBytes = kOffCtl + kCtlBytes + 1024;    // + alignment slack: 232448
+constexpr uint32_t kTmemCols = 512, kTmemO = 256;
+constexpr int kNfBufs = 4;                            // units whose non-finite lists may be in use at once
+template <int CG> struct Shape {
+  static constexpr int kRows = 128 * CG;
+  static constexpr int kKeys = 64 * CG;
+  static constexpr int kGrid = 148 / CG;
+  static constexpr uint32_t kIdescS = sm100::idesc_bf16(128 * CG, kKeys, false, false);
+  static constexpr uint32_t kIdescPV = sm100::idesc_bf16(128 * CG, 256, false, true);
+};
+}  // namespace dense_tc
+
+struct DenseTcArgs {
+  KvSource kv;
+  const __nv_bfloat16* q;   // [T][H][D]
+  __nv_bfloat16* o;
+  float* lse;               // [T][H] or null
+  float* part;
+  int H;
+  int box;                  // rows of a TMA box: keys that are contiguous in the cache
+  float scale;
+};
+
+struct DenseTcCtl {
+  uint64_t slot_full[dense_tc::kSlots];
+  uint64_t peer_full[dense_tc::kSlots];   // rank 0: rank 1's slot is full
+  uint64_t slot_empty[dense_tc::kSlots];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], p_free[2];
+  uint64_t o_full, o_free;
+  uint64_t nf_full[dense_tc::kNfBufs];
+  uint64_t mma_done;
+  float red[2][128];                      // row maxima / sums of the two warps of a row
+  uint32_t nf[dense_tc::kNfBufs][dense_tc::kQWarps][8];   // keys first_pos+1+i whose V is not finite
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(DenseTcCtl) <= dense_tc::kCtlBytes, "control block");
+
+// Largest power of two that divides page_tokens, at most 64: a run of that
+// many keys, starting at a multiple of it, lies in one page.
+inline int dense_box(int page_tokens) {
+  int b = 16;
+  while (b < 64 && page_tokens % (2 * b) == 0) b *= 2;
+  return b;
+}
+
+template <int CG>
+__device__ __forceinline__ void dense_arrive(uint64_t* bar) {   // on rank 0's barrier
+  if constexpr (CG == 1) sm100::mbar_arrive(bar); else sm100::mbar_arrive_cluster(bar, 0);
+}
+
+template <int CG, bool PAGED>
+__global__ void __launch_bounds__(dense_tc::kThreads, 1)
+    dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ DenseTable t, const __grid_constant__ DenseTcArgs a) {
+  using namespace dense_tc;
+  using namespace sm100;
+  constexpr int KC = Shape<CG>::kKeys, NK = KC / 2;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  DenseTcCtl& ctl = *reinterpret_cast<DenseTcCtl*>(smem + kOffCtl);
+  volatile int* abort_flag = &ctl.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
+  const int cta = blockIdx.x / CG;
+
+  // ---------------------------------------------------------------- set-up
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&ctl.slot_full[i], 1);
+      mbar_init(&ctl.peer_full[i], 1);
+      mbar_init(&ctl.slot_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.p_full[i], kSoftmaxWarps * CG);
+      mbar_init(&ctl.p_free[i], 1);
+    }
+    for (int i = 0; i < kNfBufs; ++i) mbar_init(&ctl.nf_full[i], kQWarps);
+    mbar_init(&ctl.q_full, kQWarps * CG);
+    mbar_init(&ctl.q_empty, 1);
+    mbar_init(&ctl.o_full, 1);
+    mbar_init(&ctl.o_free, kSoftmaxWarps * CG);
+    mbar_init(&ctl.mma_done, 1);
+    ctl.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc_cg<CG>(&ctl.tmem_base, kTmemCols);
+  tc_fence_before();
+  if constexpr (CG == 2) cluster_sync_all(); else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+  pdl_wait();
+  pdl_trigger();
+
+  DenseWalk walk;
+  walk.init(t, cta);
+  DensePiece p;
+  DenseUnit x;
+  if (warp == kProducerWarp) {
+    // ============================================================ TMA producer
+    // Lane b < 256 / box issues box b of a slot: `box` keys x 64 dims.
+    const int nbox = 256 / a.box;
+    int64_t item = 0;
+    bool ok = true;
+    while (ok && walk.next(t, p, x)) {
+      if (warp_aborted(abort_flag)) {
+        ok = false;
+        break;
+      }
+      const int n = p.c1 - p.c0;
+      // box `lane` of ring position j: its coordinates; y < 0: not loaded
+      auto place = [&](int j, int& kind, int& off, int& cx, int& key) {
+        kind = (j == 0) ? 0 : (j == 2 * n - 1) ? 1 : (j & 1) ? 0 : 1;
+        const int c = p.c0 + ((j == 0) ? 0 : (j == 2 * n - 1) ? n - 1 : (j & 1) ? (j + 1) / 2 : j / 2 - 1);
+        const int slabs = (CG == 2 && kind == 1) ? 2 : 4;
+        const int slab = lane % slabs, run = lane / slabs;
+        const int lines = 256 / slabs;                       // lines of a slab: 64 or 128
+        off = slab * lines * 128 + run * a.box * 128;
+        cx = slab * 64 + ((CG == 2 && kind == 1) ? (int)rank * 128 : 0);
+        key = c * KC + run * a.box + ((CG == 2 && kind == 0) ? (int)rank * 64 : 0);
+      };
+      auto page_of = [&](int j) -> int32_t {                 // page of this lane's box (paged only)
+        int kind, off, cx, key;
+        place(j, kind, off, cx, key);
+        if (lane >= nbox || key >= x.kv_len) return -1;
+        return a.kv.table[(int64_t)t.slot[x.si] * a.kv.max_pages + key / a.kv.page_tokens];
+      };
+      int32_t page = PAGED ? page_of(0) : 0;
+      for (int j = 0; j < 2 * n; ++j, ++item) {
+        const int slot = (int)(item % kSlots);
+        int kind, off, cx, key;
+        place(j, kind, off, cx, key);
+        int32_t y = -1;
+        if (lane < nbox && key < x.kv_len) {
+          if (PAGED) {
+            if (page >= 0 && page < a.kv.n_pages)
+              y = (page * t.G + x.grp) * a.kv.page_tokens + key % a.kv.page_tokens;
+            else
+              report_error(kErrBadIndex);
+          } else {
+            y = t.q_offset[x.si] + key;
+            cx += x.grp * kHeadDim;
+          }
+        }
+        if (PAGED && j + 1 < 2 * n) page = page_of(j + 1);
+        if (!(ok = warp_wait_sleep(&ctl.slot_empty[slot], (uint32_t)(((item / kSlots) & 1) ^ 1), abort_flag))) break;
+        const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
+        if (lane == 0) mbar_expect_tx(&ctl.slot_full[slot], (uint32_t)__popc(live) * (uint32_t)(a.box * 128));
+        __syncwarp();
+        if (y >= 0) tma_load_2d(smem + slot * kSlotBytes + off, kind == 0 ? &tm_k : &tm_v, cx, y, &ctl.slot_full[slot]);
+      }
+    }
+    if (!ok) {                                               // no copy outlives the CTA
+      volatile int never = 0;
+      for (int64_t i = item > kSlots ? item - kSlots : 0; i < item; ++i)
+        if (lane == 0) mbar_wait(&ctl.slot_full[i % kSlots], (uint32_t)((i / kSlots) & 1), &never);
+    }
+  } else if (warp == kMmaWarp && rank == 0) {
+    // ============================================================ MMA issuer
+    int64_t gc = 0, uc = 0;                                  // chunks and pieces so far
+    const uint32_t sb = smem_u32(smem);
+    bool ok = true;
+    auto slot_ready = [&](int64_t it) -> bool {
+      const uint32_t ph = (uint32_t)((it / kSlots) & 1);
+      if (!warp_wait_sleep(&ctl.slot_full[it % kSlots], ph, abort_flag)) return false;
+      if (CG == 2 && !warp_wait_sleep(&ctl.peer_full[it % kSlots], ph, abort_flag)) return false;
+      return true;
+    };
+    auto pv = [&](int64_t base, int cx, int n) -> bool {     // base: chunks before the piece
+      const int64_t xg = base + cx;
+      const int pb = (int)(xg & 1);
+      if (!warp_wait_sleep(&ctl.p_full[pb], (uint32_t)((xg >> 1) & 1), abort_flag)) return false;
+      if (cx == 0 && !warp_wait_sleep(&ctl.o_free, (uint32_t)((uc & 1) ^ 1), abort_flag)) return false;
+      const int64_t it = 2 * base + union_item(cx, 1, n);
+      const int slot = (int)(it % kSlots);
+      if (!slot_ready(it)) return false;
+      if (CG == 2) fence_acquire_cluster();
+      tc_fence_after();
+      if (lane == 0) {
+        fence_proxy_async_smem();
+        const uint32_t v_addr = sb + slot * kSlotBytes;
+#pragma unroll
+        for (int kk = 0; kk < KC / 16; ++kk) {               // k-steps of 16 keys; P: 8 columns of bf16 pairs each
+          const uint64_t db = desc_sw128(v_addr + kk * 2048, KC * 128, 1024);
+          umma_ts<CG>(tmem + kTmemO, tmem + pb * KC + kk * 8, db, Shape<CG>::kIdescPV, (cx | kk) != 0);
+        }
+        umma_commit_cg<CG>(&ctl.slot_empty[slot]);
+        umma_commit_cg<CG>(&ctl.p_free[pb]);
+        if (cx == n - 1) umma_commit_cg<CG>(&ctl.o_full);
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && walk.next(t, p, x)) {
+      if (warp_aborted(abort_flag)) break;
+      if (!(ok = warp_wait_sleep(&ctl.q_full, (uint32_t)(uc & 1), abort_flag))) break;
+      const int n = p.c1 - p.c0;
+      for (int c = 0; c < n && ok; ++c) {
+        const int b = (int)((gc + c) & 1);
+        const int64_t it = 2 * gc + union_item(c, 0, n);
+        const int slot = (int)(it % kSlots);
+        if (!(ok = slot_ready(it))) break;
+        // S buffer b: P of chunk c-2 (of this or the last piece) was read by a product issued before
+        if (CG == 2) fence_acquire_cluster();
+        tc_fence_after();
+        if (lane == 0) {
+          fence_proxy_async_smem();
+          const uint32_t k_addr = sb + slot * kSlotBytes, q_addr = sb + kOffQ;
+#pragma unroll
+          for (int kk = 0; kk < 16; ++kk) {                  // k-steps of 16 dims
+            const int slab = kk >> 2, sub = kk & 3;
+            const uint64_t da = desc_sw128(q_addr + slab * 16384 + sub * 32, 16, 1024);
+            const uint64_t db = desc_sw128(k_addr + slab * 8192 + sub * 32, 16, 1024);
+            umma_ss<CG>(tmem + b * KC, da, db, Shape<CG>::kIdescS, kk != 0);
+          }
+          umma_commit_cg<CG>(&ctl.slot_empty[slot]);
+          umma_commit_cg<CG>(&ctl.s_full[b]);
+          if (c == n - 1) umma_commit_cg<CG>(&ctl.q_empty);
+        }
+        __syncwarp();
+        if (c > 0) ok = pv(gc, c - 1, n);
+      }
+      if (!ok) break;
+      ok = pv(gc, n - 1, n);
+      gc += n;
+      ++uc;
+    }
+    // every MMA issued above has finished before TMEM is freed
+    if (lane == 0) {
+      if constexpr (CG == 1) umma_commit(&ctl.mma_done); else umma_commit_pair_local(&ctl.mma_done);
+      volatile int never = 0;
+      mbar_wait(&ctl.mma_done, 0, &never);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ============================================================ rank 1: slot full, forwarded to rank 0
+    int64_t item = 0;
+    bool ok = true;
+    while (ok && walk.next(t, p, x)) {
+      if (warp_aborted(abort_flag)) break;
+      for (int j = 0; j < 2 * (p.c1 - p.c0); ++j, ++item) {
+        const int slot = (int)(item % kSlots);
+        if (!(ok = warp_wait_sleep(&ctl.slot_full[slot], (uint32_t)((item / kSlots) & 1), abort_flag))) break;
+        if (lane == 0) mbar_arrive_cluster(&ctl.peer_full[slot], 0);
+        __syncwarp();
+      }
+    }
+  } else if (warp >= kQWarp) {
+    // ============================================================ Q of the next unit; V of its own tokens checked
+    const int qw = warp - kQWarp;
+    int64_t uc = 0;
+    while (walk.next(t, p, x)) {
+      if (warp_aborted(abort_flag)) break;
+      if (!warp_wait_sleep(&ctl.q_empty, (uint32_t)((uc & 1) ^ 1), abort_flag)) break;
+      const int valid = x.nrows - (int)rank * 128;           // rows of this CTA (may be <= 0 or > 128)
+      const int64_t row0 = x.row0 + rank * 128;
+      const uint32_t q_addr = smem_u32(smem + kOffQ);
+#pragma unroll 4
+      for (int i = 0; i < 64; ++i) {
+        const int r = qw * 64 + i;
+        if (r < valid) {
+          const int64_t row = row0 + r;
+          const int64_t at = ((int64_t)t.q_offset[x.si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg + row % t.hpg;
+          cp_async16(q_addr + (lane >> 3) * 16384 + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                     a.q + at * kHeadDim + lane * 8, 16);
+        }
+      }
+      const int64_t first = t.pos0[x.si] + x.row0 / t.hpg;   // position of the unit's first row
+      const int own = (int)(x.kv_len - 1 - first);           // keys that only some rows see (<= 255)
+      uint32_t word = 0;
+      for (int i = qw; i < own; i += kQWarps) {
+        const int64_t off = kv_row<PAGED>(a.kv, t, x.si, x.grp, first + 1 + i);
+        bool nf = false;
+        if (off >= 0) {
+          const uint4 v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.kv.v + off + lane * 8);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            nf |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+        }
+        if (__any_sync(0xffffffffu, nf) && lane == (i >> 5)) word |= 1u << (i & 31);
+      }
+      if (lane < 8) ctl.nf[uc % kNfBufs][qw][lane] = word;
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl.nf_full[uc % kNfBufs]);
+        dense_arrive<CG>(&ctl.q_full);
+      }
+      ++uc;
+    }
+    cp_async_wait_all();
+  } else if (warp < kSoftmaxWarps) {
+    // ============================================================ softmax + epilogue
+    const int quad = warp & 3, half = warp >> 2;
+    const int li = quad * 32 + lane;                         // TMEM lane: row of this CTA
+    const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+    const float tau2 = a.scale * 1.4426950408889634f;
+    int64_t gc = 0, uc = 0;
+    // No early exit: the two warps of a quadrant meet at a named barrier per chunk.
+    while (walk.next(t, p, x)) {
+      const int n = p.c1 - p.c0;
+      const int valid = x.nrows - (int)rank * 128;
+      const bool active = li < valid, warp_active = quad * 32 < valid;
+      const int64_t row = x.row0 + rank * 128 + (active ? li : 0);
+      const int32_t pos = t.pos0[x.si] + (int32_t)(row / t.hpg);
+      const int64_t at = ((int64_t)t.q_offset[x.si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg + row % t.hpg;
+      const int32_t first = t.pos0[x.si] + (int32_t)(x.row0 / t.hpg);               // of the unit
+      const int32_t first_cta = t.pos0[x.si] + (int32_t)((x.row0 + rank * 128) / t.hpg);
+      const int32_t kv_len = (int32_t)x.kv_len;
+      mbar_wait_sleep(&ctl.nf_full[uc % kNfBufs], (uint32_t)((uc / kNfBufs) & 1), abort_flag);
+      const uint32_t my_nf = lane < 8 ? ctl.nf[uc % kNfBufs][0][lane] | ctl.nf[uc % kNfBufs][1][lane] : 0u;
+      const bool any_nf = __any_sync(0xffffffffu, my_nf != 0);
+      // bit per run of 16 keys of a chunk: its page is out of range
+      auto bad_runs = [&](int c) -> uint32_t {
+        bool bad = false;
+        if (PAGED && lane < KC / 16) {
+          const int32_t key = c * KC + lane * 16;
+          if (key < kv_len) {
+            const int32_t page = a.kv.table[(int64_t)t.slot[x.si] * a.kv.max_pages + key / a.kv.page_tokens];
+            bad = page < 0 || page >= a.kv.n_pages;
+          }
+        }
+        return PAGED ? __ballot_sync(0xffffffffu, bad) : 0u;
+      };
+      float m = -INFINITY, l = 0.f;
+      for (int c = 0; c < n; ++c, ++gc) {
+        const int b = (int)(gc & 1);
+        const int32_t j0 = (p.c0 + c) * KC;
+        const uint32_t bad = bad_runs(p.c0 + c);
+        mbar_wait_sleep(&ctl.s_full[b], (uint32_t)((gc >> 1) & 1), abort_flag);
+        tc_fence_after();
+        if (j0 + KC > kv_len || bad || (any_nf && j0 + KC - 1 > first)) {
+          // V rows that must not reach the product become zero in shared memory
+          const int64_t it = 2 * (gc - c) + union_item(c, 1, n);
+          mbar_wait_sleep(&ctl.slot_full[it % kSlots], (uint32_t)((it / kSlots) & 1), abort_flag);
+          unsigned char* vs = smem + (it % kSlots) * kSlotBytes;
+          constexpr int kPieces = 2048 / KC;                 // 16-byte pieces of a key's row here: 32 or 16
+          for (int i = threadIdx.x; i < KC * kPieces; i += kSoftmaxWarps * 32) {
+            const int key = i / kPieces, piece = i % kPieces;     // a warp covers one or two keys
+            const int32_t rel = j0 + key - first - 1;
+            const uint32_t w = __shfl_sync(0xffffffffu, my_nf, rel >= 0 ? (rel >> 5) & 7 : 0);
+            const bool zero = j0 + key >= kv_len || ((bad >> (key >> 4)) & 1u) ||
+                              (rel >= 0 && ((w >> (rel & 31)) & 1u));
+            if (zero)
+              *reinterpret_cast<uint4*>(vs + (piece >> 3) * (KC * 128) + key * 128 + ((piece & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (warp_active) {
+          float s[NK];                                       // raw scores
+#pragma unroll
+          for (int k = 0; k < NK; k += 16) {
+            float v[16];
+            tmem_ld16(lane_addr + b * KC + half * NK + k, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[k + i] = v[i];
+          }
+          tmem_wait_ld();
+          if (j0 + KC - 1 > first_cta || bad) {              // keys this row does not attend: -inf
+            const int32_t lim = pos - j0 - half * NK;
+#pragma unroll
+            for (int i = 0; i < NK; ++i)
+              if (i > lim || ((bad >> ((half * NK + i) >> 4)) & 1u)) s[i] = -INFINITY;
+          }
+          float pm = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < NK; ++i) pm = fmaxf(pm, s[i]);
+          ctl.red[half][li] = pm * tau2;
+          named_bar_sync(1 + quad, 64);
+          const float mc = fmaxf(ctl.red[0][li], ctl.red[1][li]);
+          named_bar_sync(1 + quad, 64);
+          float f = 1.f;
+          bool need = false;
+          if (mc > m + 8.f) {                                // false while both are -inf
+            if (m != -INFINITY) {
+              f = exp2f(m - mc);
+              need = true;
+            }
+            m = mc;
+          }
+          l *= f;
+          if (__any_sync(0xffffffffu, need)) {
+            // O holds chunks 0..c-1 (c >= 1 here): wait for the last of their products
+            const int64_t xp = gc - 1;
+            mbar_wait_sleep(&ctl.p_free[xp & 1], (uint32_t)((xp >> 1) & 1), abort_flag);
+            tc_fence_after();
+#pragma unroll 1
+            for (int piece = 0; piece < 8; ++piece) {
+              float o[16];
+              const uint32_t addr = lane_addr + kTmemO + half * 128 + piece * 16;
+              tmem_ld16(addr, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tmem_st16(addr, o);
+            }
+            tmem_wait_st();
+          }
+          const float mb = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int k = 0; k < NK; k += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float p0 = ex2_approx(fmaf(s[k + 2 * i], tau2, -mb));
+              const float p1 = ex2_approx(fmaf(s[k + 2 * i + 1], tau2, -mb));
+              l += p0 + p1;
+              pk[i] = pack_bf16x2(p0, p1);
+            }
+            // P over the first half of the chunk's S columns: both warps of
+            // the row have read S (the exchange above)
+            tmem_st16u(lane_addr + b * KC + half * (NK / 2) + k / 2, pk);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dense_arrive<CG>(&ctl.p_full[b]);
+      }
+      float lt = 0.f;
+      if (warp_active) {                                     // the row's sum: both warps' parts
+        ctl.red[half][li] = l;
+        named_bar_sync(1 + quad, 64);
+        lt = ctl.red[0][li] + ctl.red[1][li];
+        named_bar_sync(1 + quad, 64);
+      }
+      mbar_wait_sleep(&ctl.o_full, (uint32_t)(uc & 1), abort_flag);
+      tc_fence_after();
+      if (warp_active) {
+        const bool whole = p.part < 0;
+        const float inv = !whole ? 1.f : lt != 0.f ? 1.f / lt : 0.f;    // lt = 0: no key at all
+        float* pdst = whole ? nullptr
+                            : a.part + ((int64_t)p.part * t.prows + rank * 128 + li) * dense::kPartFloats + half * 128;
+        __nv_bfloat16* orow = a.o + at * kHeadDim + half * 128;
+#pragma unroll 1
+        for (int piece = 0; piece < 8; ++piece) {
+          float o[16];
+          tmem_ld16(lane_addr + kTmemO + half * 128 + piece * 16, o);
+          tmem_wait_ld();
+          if (any_nf) {                                      // keys kept out of the product
+#pragma unroll 1
+            for (int w = 0; w < 8; ++w) {
+              uint32_t bits = __shfl_sync(0xffffffffu, my_nf, w);
+              while (bits) {
+                const int32_t key = first + 1 + w * 32 + __ffs(bits) - 1;
+                bits &= bits - 1;
+                if (!active || key > pos || key < p.c0 * KC || key >= p.c1 * KC) continue;
+                const int64_t off = kv_row<PAGED>(a.kv, t, x.si, x.grp, key);
+                if (off < 0) continue;
+                const __nv_bfloat16* kr = (const __nv_bfloat16*)a.kv.k + off;
+                const __nv_bfloat16* vr = (const __nv_bfloat16*)a.kv.v + off + half * 128 + piece * 16;
+                float sc = 0.f;
+#pragma unroll 1
+                for (int d = 0; d < kHeadDim; ++d)
+                  sc = fmaf(__bfloat162float(a.q[at * kHeadDim + d]), __bfloat162float(kr[d]), sc);
+                const float pw = ex2_approx(fmaf(sc, tau2, m == -INFINITY ? 0.f : -m));
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = fmaf(pw, __bfloat162float(vr[i]), o[i]);
+              }
+            }
+            __syncwarp();
+          }
+          if (active) {
+            if (whole) {
+              uint4 v0, v1;
+              v0.x = pack_bf16x2(o[0] * inv, o[1] * inv);
+              v0.y = pack_bf16x2(o[2] * inv, o[3] * inv);
+              v0.z = pack_bf16x2(o[4] * inv, o[5] * inv);
+              v0.w = pack_bf16x2(o[6] * inv, o[7] * inv);
+              v1.x = pack_bf16x2(o[8] * inv, o[9] * inv);
+              v1.y = pack_bf16x2(o[10] * inv, o[11] * inv);
+              v1.z = pack_bf16x2(o[12] * inv, o[13] * inv);
+              v1.w = pack_bf16x2(o[14] * inv, o[15] * inv);
+              *reinterpret_cast<uint4*>(orow + piece * 16) = v0;
+              *reinterpret_cast<uint4*>(orow + piece * 16 + 8) = v1;
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(pdst + piece * 16 + 4 * i) =
+                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+          }
+        }
+        if (active && half == 0) {
+          if (!whole) {
+            pdst[kHeadDim] = m;
+            pdst[kHeadDim + 1] = lt;
+          } else if (a.lse) {
+            a.lse[at] = lt != 0.f ? (m + log2f(lt)) * 0.6931471805599453f : -INFINITY;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) dense_arrive<CG>(&ctl.o_free);
+      ++uc;
+    }
+  }
+  tc_fence_before();
+  if constexpr (CG == 2) cluster_sync_all(); else __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_cg<CG>(tmem, kTmemCols);
+  }
+}
+
+}  // namespace qsa
