@@ -12,6 +12,11 @@
 // pieces, each leaving an unnormalised fp32 partial result, which
 // dense_combine_kernel joins in a fixed order.  Units with few rows (decode)
 // are nothing but such a sequence: keys split over the GPU.
+//
+// With by_keys the roles are exchanged (gradients of keys and values): a unit
+// is `rows` consecutive keys of one segment and group, against the group's
+// heads of every token from the unit's first key on, a chunk being `kc` tokens
+// of one head (heads innermost).  A segment's first keys have the most.
 #pragma once
 #include "qsa_internal.cuh"
 
@@ -37,7 +42,7 @@ struct DenseTable {
   int32_t grid;                            // CTAs (or pairs)
   int32_t rounds;                          // whole units per CTA; unit rounds*grid is the first of the tail
   int32_t prows;                           // rows of a partial result
-  int32_t pad_;
+  int32_t by_keys;
   DensePoint cut[dense::kMaxGrid + 1];     // CTA c takes the tail from cut[c] up to cut[c+1]
 };
 
@@ -51,9 +56,9 @@ struct DenseSplits {
 struct DenseUnit {
   int si;                // segment
   int grp;
-  int64_t row0;          // first row of the tile in the segment's rows
+  int64_t row0;          // first row of the tile in the segment's rows (by_keys: first key)
   int nrows;             // valid rows (>= 1)
-  int64_t kv_len;        // keys 0 .. kv_len-1 are those of the tile's last token
+  int64_t kv_len;        // keys 0 .. kv_len-1 are those of the tile's last token (by_keys: the segment's tokens)
   int nchunks;
 };
 
@@ -67,6 +72,14 @@ __host__ __device__ __forceinline__ DenseUnit dense_unit(const DenseTable& t, in
     if (t.item0[mid] <= tile) lo = mid; else hi = mid - 1;
   }
   x.si = lo;
+  if (t.by_keys) {
+    x.row0 = (int64_t)(tile - t.item0[lo]) * t.rows;
+    x.kv_len = t.q_len[lo];
+    const int64_t left = x.kv_len - x.row0;
+    x.nrows = (int)(left < t.rows ? left : t.rows);
+    x.nchunks = (int)((left + t.kc - 1) / t.kc) * t.hpg;
+    return x;
+  }
   const int64_t total = (int64_t)t.q_len[lo] * t.hpg;
   x.row0 = (int64_t)(t.item0[lo + 1] - 1 - tile) * t.rows;     // tiles from the segment's end
   const int64_t left = total - x.row0;
@@ -116,6 +129,13 @@ struct DenseWalk {
   }
 };
 
+// Slot of the partial result that CTA c holds of the cut unit u; -1: none.
+__device__ __forceinline__ int dense_piece_slot(const DenseTable& t, int u, int c) {
+  const DensePoint a = t.cut[c], b = t.cut[c + 1];
+  if (a.unit > u || b.unit < u || (b.unit == u && b.chunk == 0) || (a.unit == b.unit && a.chunk == b.chunk)) return -1;
+  return 2 * c + (a.unit == u ? 0 : 1);
+}
+
 // Joins the pieces of each cut unit: with m the largest of the pieces' maxima
 // (log2 units), l = sum l_p 2^(m_p - m), o = sum o_p 2^(m_p - m) / l.  A piece
 // without a key of a row has m_p = -inf and counts nothing.  One warp per row,
@@ -133,10 +153,8 @@ __global__ void __launch_bounds__(128)
   const int r = blockIdx.y * 4 + warp;
   if (r >= x.nrows) return;
   auto piece = [&](int c) -> const float* {      // null: CTA c has no piece of the unit
-    const DensePoint a = t.cut[c], b = t.cut[c + 1];
-    if (a.unit > u || b.unit < u || (b.unit == u && b.chunk == 0) || (a.unit == b.unit && a.chunk == b.chunk))
-      return nullptr;
-    return part + ((int64_t)(2 * c + (a.unit == u ? 0 : 1)) * t.prows + r) * dense::kPartFloats;
+    const int slot = dense_piece_slot(t, u, c);
+    return slot < 0 ? nullptr : part + ((int64_t)slot * t.prows + r) * dense::kPartFloats;
   };
   float m = -INFINITY;
   for (int c = sp.first[i]; c <= sp.last[i]; ++c)

@@ -6,6 +6,7 @@
 #include "dense.cuh"
 #include "dense_simt.cuh"
 #include "dense_tc.cuh"
+#include "dense_bwd_tc.cuh"
 
 namespace qsa {
 namespace {
@@ -54,6 +55,7 @@ qsa_status_t check_dense_segments(const qsa_segment_t* segs, int32_t n_segs, int
 // Shape of one kind of launch.
 struct DenseKind {
   int rows, kc, grid;
+  bool by_keys;
 };
 // A unit's fixed cost (loading Q, the epilogue) in chunks, for levelling.
 constexpr int64_t kUnitCost = 2;
@@ -166,10 +168,11 @@ qsa_status_t for_each_dense(const Geo& g, std::vector<qsa_segment_t> segs, const
     t.rows = kind.rows;
     t.kc = kind.kc;
     t.grid = kind.grid;
+    t.by_keys = kind.by_keys;
     int64_t tiles = 0, most = 0;
     for (; i < segs.size() && t.n < kMaxSegs; ++i) {
       const qsa_segment_t& s = segs[i];
-      const int64_t rows = (int64_t)s.q_len * g.hpg, it = cdiv(rows, kind.rows);
+      const int64_t rows = (int64_t)s.q_len * (kind.by_keys ? 1 : g.hpg), it = cdiv(rows, kind.rows);
       if (t.n > 0 && (tiles + it) * g.G > INT32_MAX / 4) break;
       if ((tiles + it) * g.G > INT32_MAX / 4) return QSA_ERR_UNSUPPORTED;
       t.q_offset[t.n] = s.q_offset;
@@ -194,11 +197,11 @@ void dense_kinds(const Geo& g, bool tc, const qsa_segment_t* segs, int n, std::v
   if (tc) {
     using N = dense_tc::Shape<1>;
     using W = dense_tc::Shape<2>;
-    kn = {N::kRows, N::kKeys, N::kGrid};
-    kw = {W::kRows, W::kKeys, W::kGrid};
+    kn = {N::kRows, N::kKeys, N::kGrid, false};
+    kw = {W::kRows, W::kKeys, W::kGrid, false};
   } else {
-    kn = {dense_simt::kRowsNarrow, dense_simt::kKeys, kNumSms};
-    kw = {dense_simt::kRowsWide, dense_simt::kKeys, kNumSms};
+    kn = {dense_simt::kRowsNarrow, dense_simt::kKeys, kNumSms, false};
+    kw = {dense_simt::kRowsWide, dense_simt::kKeys, kNumSms, false};
   }
   for (int i = 0; i < n; ++i)
     if (segs[i].q_len > 0) ((int64_t)segs[i].q_len * g.hpg <= kn.rows ? narrow : wide).push_back(segs[i]);
@@ -320,41 +323,166 @@ qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int
 }
 
 // ------------------------------------------------------------------ backward
-size_t dense_bwd_ws(const Geo& g, int32_t n_tokens) { return align_up((size_t)n_tokens * g.H * 4, 256); }
+// Workspace of the gradient: delta by token; for bf16 also the statistics by
+// head (segments padded to whole tiles), the segments' flags and the partial
+// results of the cut units (of one kernel at a time).
+struct DenseBwdPlan {
+  std::vector<qsa_segment_t> segs;       // non-empty; slot: the segment's first statistics tile
+  int64_t stat_rows = 0;
+  size_t off_lse2 = 0, off_delta_h = 0, off_flags = 0, flag_bytes = 0, off_part = 0, bytes = 0;
+};
 
+DenseKind dense_bwd_kind(bool by_keys) {
+  return {dense_bwd::kRows, dense_bwd::kKeys, dense_bwd::kGrid, by_keys};
+}
+
+qsa_status_t plan_dense_bwd(const Geo& g, bool tc, const qsa_segment_t* segs, int n, int32_t n_tokens,
+                            DenseBwdPlan& p) {
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    if (segs[i].q_len <= 0) continue;
+    p.segs.push_back(segs[i]);
+    p.segs.back().slot = (int32_t)tiles;
+    tiles += cdiv(segs[i].q_len, dense_bwd::kStatTile);
+  }
+  size_t at = align_up((size_t)n_tokens * g.H * 4, 256);
+  if (tc) {
+    p.stat_rows = tiles * dense_bwd::kStatTile;
+    const size_t stats = align_up((size_t)p.stat_rows * g.H * 4, 256);
+    p.off_lse2 = at;
+    p.off_delta_h = at + stats;
+    p.off_flags = at + 2 * stats;
+    p.flag_bytes = (size_t)tiles * 4;
+    at = p.off_part = p.off_flags + align_up(p.flag_bytes, 256);
+    size_t part = 0;
+    for (const bool by_keys : {false, true}) {
+      const qsa_status_t r =
+          for_each_dense(g, p.segs, dense_bwd_kind(by_keys), [&](const DenseTable& t, const DenseSplits& sp) {
+            part = std::max(part, partial_bytes(t, sp));
+            return QSA_OK;
+          });
+      if (r != QSA_OK) return r;
+    }
+    at += align_up(part, 256);
+  }
+  p.bytes = at;
+  return QSA_OK;
+}
+
+size_t dense_bwd_ws(const Geo& g, bool tc, const qsa_segment_t* segs, int n, int32_t n_tokens) {
+  DenseBwdPlan p;
+  return plan_dense_bwd(g, tc, segs, n, n_tokens, p) == QSA_OK ? p.bytes : SIZE_MAX;
+}
+
+// The CUDA-core gradient.  With a.flags: of the flagged segments only, on no
+// more blocks than the GPU holds, since there are hardly ever any.
 template <typename T>
-qsa_status_t run_dense_bwd(const Geo& g, const qsa_segment_t* segs, int n, DenseBwdArgs a, const void* o, float* delta,
-                           cudaStream_t st) {
-  qsa_status_t r = for_each_table(
-      segs, n, [&](const qsa_segment_t& s) { return (int64_t)s.q_len; },
-      [&](const SegTable& t) -> cudaError_t {
-        count_launch();
-        return launch_chained(dense_delta_kernel<T>, dim3((unsigned)cdiv((int64_t)t.item0[t.n] * g.H, 8)), dim3(256), 0,
-                              st, t, (const T*)o, (const T*)a.dout, delta, g.H);
-      });
-  if (r != QSA_OK) return r;
+qsa_status_t run_dense_bwd_simt(const Geo& g, const std::vector<qsa_segment_t>& segs, const DenseBwdArgs& a,
+                                cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(dense_dq_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        dense_simt::kBwdSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(dense_dkv_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              dense_simt::kBwdSmem);
   if (e != cudaSuccess) return QSA_ERR_CUDA;
-  r = for_each_dense(g, std::vector<qsa_segment_t>(segs, segs + n), DenseKind{dense_simt::kBRows, dense_simt::kBKeys, 1},
-                     [&](const DenseTable& t, const DenseSplits&) -> qsa_status_t {
-                       count_launch();
-                       return launch_chained(dense_dq_simt_kernel<T>, dim3((unsigned)(t.item0[t.n] * g.G)),
-                                             dim3(dense_simt::kThreads), dense_simt::kBwdSmem, st, t, a) == cudaSuccess
-                                  ? QSA_OK
-                                  : QSA_ERR_CUDA;
-                     });
+  auto blocks = [&](int64_t units) { return dim3((unsigned)(a.flags ? std::min<int64_t>(units, kNumSms) : units)); };
+  const qsa_status_t r = for_each_dense(
+      g, segs, DenseKind{dense_simt::kBRows, dense_simt::kBKeys, 1, false},
+      [&](const DenseTable& t, const DenseSplits&) -> qsa_status_t {
+        count_launch();
+        return launch_chained(dense_dq_simt_kernel<T>, blocks((int64_t)t.item0[t.n] * g.G), dim3(dense_simt::kThreads),
+                              dense_simt::kBwdSmem, st, t, a) == cudaSuccess
+                   ? QSA_OK
+                   : QSA_ERR_CUDA;
+      });
   if (r != QSA_OK) return r;
   return for_each_table(
-      segs, n, [&](const qsa_segment_t& s) { return cdiv(s.q_len, dense_simt::kBKeys); },
+      segs.data(), (int)segs.size(), [&](const qsa_segment_t& s) { return cdiv(s.q_len, dense_simt::kBKeys); },
       [&](const SegTable& t) -> cudaError_t {
         count_launch();
-        return launch_chained(dense_dkv_simt_kernel<T>, dim3((unsigned)(t.item0[t.n] * g.G)), dim3(dense_simt::kThreads),
+        return launch_chained(dense_dkv_simt_kernel<T>, blocks((int64_t)t.item0[t.n] * g.G), dim3(dense_simt::kThreads),
                               dense_simt::kBwdSmem, st, t, g.G, g.hpg, a);
       });
+}
+
+qsa_status_t run_dense_bwd_f32(const Geo& g, const DenseBwdPlan& p, const DenseBwdArgs& a, const void* o, float* delta,
+                               cudaStream_t st) {
+  const qsa_status_t r = for_each_table(
+      p.segs.data(), (int)p.segs.size(), [&](const qsa_segment_t& s) { return (int64_t)s.q_len; },
+      [&](const SegTable& t) -> cudaError_t {
+        count_launch();
+        return launch_chained(dense_delta_kernel<float>, dim3((unsigned)cdiv((int64_t)t.item0[t.n] * g.H, 8)),
+                              dim3(256), 0, st, t, (const float*)o, (const float*)a.dout, delta, g.H);
+      });
+  return r != QSA_OK ? r : run_dense_bwd_simt<float>(g, p.segs, a, st);
+}
+
+// One gradient on the tensor cores: its kernel, then the join of its cut units.
+template <dense_bwd::Grad M>
+qsa_status_t run_dense_grad_tc(const Geo& g, const DenseBwdPlan& p, const CUtensorMap& ms, const CUtensorMap& mp,
+                               const CUtensorMap& md, const DenseBwdTcArgs& a, cudaStream_t st) {
+  auto kernel = dense_bwd_tc_kernel<M>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense_bwd::kSmemBytes) != cudaSuccess)
+    return QSA_ERR_CUDA;
+  return for_each_dense(
+      g, p.segs, dense_bwd_kind(M != dense_bwd::kDq), [&](const DenseTable& t, const DenseSplits& sp) -> qsa_status_t {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(t.grid * 2);
+        cfg.blockDim = dim3(dense_bwd::kThreads);
+        cfg.dynamicSmemBytes = dense_bwd::kSmemBytes;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 2;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        count_launch();
+        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ms, mp, md, t, a);
+        if (e == cudaSuccess && sp.n > 0) {
+          count_launch();
+          e = launch_chained(dense_bwd_combine_kernel, dim3(sp.n, (unsigned)cdiv(t.prows, 4)), dim3(128), 0, st, t, sp,
+                             a.part, a.flags, a.out, g.H, M == dense_bwd::kDv ? 1.f : g.scale);
+        }
+        return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+      });
+}
+
+qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArgs a, const void* o, char* ws,
+                                int32_t n_tokens, cudaStream_t st) {
+  using B = __nv_bfloat16;
+  float* delta = (float*)ws;
+  float* lse2_h = (float*)(ws + p.off_lse2);
+  float* delta_h = (float*)(ws + p.off_delta_h);
+  int32_t* flags = (int32_t*)(ws + p.off_flags);
+  CUtensorMap mq, mo, mk, mv;
+  if (!make_dense_map(&mq, a.q, n_tokens, g.H, 64) || !make_dense_map(&mo, a.dout, n_tokens, g.H, 64) ||
+      !make_dense_map(&mk, a.k, n_tokens, g.G, 64) || !make_dense_map(&mv, a.v, n_tokens, g.G, 64))
+    return QSA_ERR_CUDA;
+  if (cudaMemsetAsync(flags, 0, p.flag_bytes, st) != cudaSuccess) return QSA_ERR_CUDA;
+  qsa_status_t r = for_each_table(
+      p.segs.data(), (int)p.segs.size(),
+      [&](const qsa_segment_t& s) { return cdiv(s.q_len, dense_bwd::kStatTile) * dense_bwd::kStatTile; },
+      [&](const SegTable& t) -> cudaError_t {
+        count_launch();
+        return launch_chained(dense_stats_kernel, dim3((unsigned)cdiv((int64_t)t.item0[t.n] * g.H, 8)), dim3(256), 0,
+                              st, t, (const B*)o, (const B*)a.dout, a.lse, (const B*)a.k, (const B*)a.v, delta, lse2_h,
+                              delta_h, flags, p.stat_rows, g.H, g.G);
+      });
+  if (r != QSA_OK) return r;
+  DenseBwdTcArgs b{(const B*)a.k, (const B*)a.v, lse2_h, delta_h, flags, (B*)a.dv, (float*)(ws + p.off_part),
+                   p.stat_rows, g.H, g.scale};
+  if ((r = run_dense_grad_tc<dense_bwd::kDv>(g, p, mq, mq, mo, b, st)) != QSA_OK) return r;
+  b.out = (B*)a.dk;
+  if ((r = run_dense_grad_tc<dense_bwd::kDk>(g, p, mq, mo, mq, b, st)) != QSA_OK) return r;
+  b.fix0 = (const B*)a.q;
+  b.fix1 = (const B*)a.dout;
+  b.out = (B*)a.dq;
+  if ((r = run_dense_grad_tc<dense_bwd::kDq>(g, p, mk, mv, mk, b, st)) != QSA_OK) return r;
+  a.flags = flags;
+  return run_dense_bwd_simt<B>(g, p.segs, a, st);
 }
 
 // Runs an entry point's body; host memory that runs out is an error code, not
@@ -470,12 +598,14 @@ QSA_API qsa_status_t qsa_prompt_attn_bwd(const qsa_config_t* cfg, const qsa_segm
       if (!p || !aligned16(p)) return QSA_ERR_INVALID_ARG;
     if (!lse || ((uintptr_t)lse & 3u)) return QSA_ERR_INVALID_ARG;
     const Geo g = make_geo(cfg, nullptr);
-    if (!workspace || ws_bytes < dense_bwd_ws(g, n_tokens)) return QSA_ERR_WORKSPACE;
+    const bool tc = cfg->dtype == QSA_DTYPE_BF16;
+    DenseBwdPlan p;
+    if ((s = plan_dense_bwd(g, tc, segs, n_segs, n_tokens, p)) != QSA_OK) return s;
+    if (!workspace || ws_bytes < p.bytes) return QSA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return QSA_ERR_INVALID_ARG;
     float* delta = (float*)workspace;
-    const DenseBwdArgs a{q, k, v, lse, delta, dout, dq, dk, dv, g.H, g.scale};
-    return cfg->dtype == QSA_DTYPE_BF16
-               ? run_dense_bwd<__nv_bfloat16>(g, segs, n_segs, a, o, delta, (cudaStream_t)stream)
-               : run_dense_bwd<float>(g, segs, n_segs, a, o, delta, (cudaStream_t)stream);
+    const DenseBwdArgs a{q, k, v, lse, delta, dout, dq, dk, dv, g.H, g.scale, nullptr};
+    return tc ? run_dense_bwd_bf16(g, p, a, o, (char*)workspace, n_tokens, (cudaStream_t)stream)
+              : run_dense_bwd_f32(g, p, a, o, delta, (cudaStream_t)stream);
   });
 }

@@ -1,0 +1,628 @@
+// dense_bwd_tc.cuh -- gradient of the packed prompts' causal GQA attention,
+// bf16, on tcgen05 tensor cores.
+//
+// With s the softmax scale, lse and delta_i = dout_i . o_i of the forward:
+//   P = exp(s Q K^T - lse),  dP = dO V^T,  dS = P (dP - delta),
+//   dV = P^T dO,  dK = s dS^T Q,  dQ = s dS K.
+// At 256 dims one tile's dK and dV fill tensor memory (2 x 256 columns), so
+// each gradient has a kernel of its own that keeps its sums in 256 columns
+// and S and dP in the other 256:
+//   dV  keys stay (K), rows stream: S^T = K Q^T, dV += P^T dO      2 products
+//   dK  keys stay (K, V), rows stream: S^T, dP^T, dK += dS^T Q     3 products
+//   dQ  rows stay (Q, dO), keys stream: S, dP, dQ += dS K          3 products
+// Eight products where five would do with all sums in one place; none needs
+// atomics, so the same inputs give the same bits.  (Keys on 64-row tiles that
+// hold dK and dV together would stream Q and dO at 64 bytes per cycle and SM,
+// beyond L2; 128 keys per CTA of a pair need 32.)
+//
+// A unit is a tile of 256 stationary rows on a CTA pair (cta_group::2, 128
+// each): for dQ rows (token, head) of a KV group as in the forward, for dK and
+// dV keys, whose chunks are the group's heads x tiles of 128 tokens from the
+// unit's first key on.  Chunks are 128 wide; the streamed operand of S and dP
+// is split between the CTAs by rows, that of the gradient's product by dims.
+// P and dS are rounded to bf16 for the products and written over the columns
+// they were computed from, so no warp waits for another's reads.
+//
+// Roles per CTA (12 warps): eight softmax warps (two per lane quadrant, each
+// thread one lane and 64 of a chunk's columns), one TMA producer, one MMA warp,
+// two loaders of the stationary tiles.  MMA order with three products:
+//   S0 dP0 | S1 D0 dP1 | S2 D1 dP2 | ...
+// so that the exponentials of chunk c+1 run under D(c) and dP(c+1), and dS(c+1)
+// under S(c+2); one buffer each for S and dP is enough.  With two products (dV)
+// S is double-buffered as in the forward.
+//
+// Segments whose lse, delta, K or V hold infinities or NaN are left to the
+// CUDA-core kernels (dense_simt.cuh), which skip masked pairs one by one; here
+// masked pairs are multiplied by zero.  Rows behind a segment's end may be
+// anything: their scores are replaced and their operand rows zeroed in shared
+// memory.  Every mbarrier wait is bounded.
+#pragma once
+#include "dense_tc.cuh"
+
+namespace qsa {
+namespace dense_bwd {
+using dense_tc::kThreads;
+using dense_tc::kSoftmaxWarps;
+using dense_tc::kProducerWarp;
+using dense_tc::kMmaWarp;
+using dense_tc::kQWarp;
+using dense_tc::kQWarps;
+using dense_tc::kSlotBytes;
+using dense_tc::kQBytes;
+enum Grad { kDv, kDk, kDq };
+constexpr int kRows = 256, kKeys = 128, kGrid = 74;
+constexpr int kStatTile = 128;                        // tokens of a row of the statistics
+template <Grad M> struct Ring {
+  static constexpr int kProducts = M == kDv ? 2 : 3;
+  static constexpr int kTiles = M == kDv ? 1 : 2;     // stationary tiles of 64 KiB
+  static constexpr int kSlots = M == kDv ? 5 : 3;
+  static constexpr int kBufs = M == kDv ? 2 : 1;      // S buffers
+};
+constexpr int kOffCtl = 5 * kSlotBytes + kQBytes;     // 229376, also 3 slots + 2 tiles
+static_assert(3 * kSlotBytes + 2 * kQBytes == kOffCtl, "layouts of equal size");
+constexpr int kCtlBytes = 3072;
+constexpr int kSmemBytes = kOffCtl + kCtlBytes;       // 232448: the base itself is 1024-byte aligned
+constexpr uint32_t kTmemP = 128, kTmemD = 256;
+using Pair = dense_tc::Shape<2>;
+}  // namespace dense_bwd
+
+struct DenseBwdTcArgs {
+  const __nv_bfloat16* fix0;  // stationary rows: Q (dQ) or K
+  const __nv_bfloat16* fix1;  // dO (dQ) or V (dK)
+  const float* lse2;          // [H][stat rows] lse * log2 e, +inf behind a segment's end
+  const float* delta;         // [H][stat rows]
+  const int32_t* flags;       // by first statistics tile of a segment: not for these kernels
+  __nv_bfloat16* out;
+  float* part;
+  int64_t stat_rows;
+  int H;
+  float scale;
+};
+
+struct DenseBwdTcCtl {
+  uint64_t slot_full[5], peer_full[5], slot_empty[5];
+  uint64_t fix_full, fix_empty;
+  uint64_t s_full[2], s_free, dp_full, w_full[2];     // w: P (dV) or dS written
+  uint64_t o_full, o_free;
+  uint64_t st_full[2], st_free[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr int kBwdStatOff = 1024;                     // of the control block: two buffers of lse2[128], delta[128]
+static_assert(sizeof(DenseBwdTcCtl) <= kBwdStatOff, "control block");
+static_assert(kBwdStatOff + 2 * 1024 <= dense_bwd::kCtlBytes, "control block");
+
+// Ring position j of a piece of n chunks: which operand (0: S, 1: dP, 2: the
+// gradient's product) of which chunk.
+template <dense_bwd::Grad M>
+__device__ __forceinline__ void bwd_item(int j, int n, int& kind, int& c) {
+  if constexpr (M == dense_bwd::kDv) {
+    kind = (j == 0) ? 0 : (j == 2 * n - 1) ? 2 : (j & 1) ? 0 : 2;
+    c = (j == 0) ? 0 : (j == 2 * n - 1) ? n - 1 : (j & 1) ? (j + 1) / 2 : j / 2 - 1;
+  } else {
+    kind = (j == 0) ? 0 : (j == 3 * n - 1) ? 2 : (j % 3 == 1) ? 1 : (j % 3 == 2) ? 0 : 2;
+    c = (j == 0) ? 0 : (j == 3 * n - 1) ? n - 1 : (j % 3 == 1) ? j / 3 : (j % 3 == 2) ? (j + 1) / 3 : j / 3 - 1;
+  }
+}
+template <dense_bwd::Grad M>
+__device__ __forceinline__ int bwd_pos(int kind, int c, int n) {
+  if constexpr (M == dense_bwd::kDv) return union_item(c, kind == 0 ? 0 : 1, n);
+  if (kind == 0) return c == 0 ? 0 : 3 * c - 1;
+  if (kind == 1) return 3 * c + 1;
+  return c == n - 1 ? 3 * n - 1 : 3 * c + 3;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          sm100::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+
+template <dense_bwd::Grad M>
+__global__ void __launch_bounds__(dense_bwd::kThreads, 1)
+    dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_p,
+                        const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ DenseTable t,
+                        const __grid_constant__ DenseBwdTcArgs a) {
+  using namespace dense_bwd;
+  using namespace sm100;
+  using R = Ring<M>;
+  constexpr bool kByKeys = M != kDq;
+  constexpr int kSlots = R::kSlots, kProducts = R::kProducts, kBufs = R::kBufs;
+  extern __shared__ __align__(1024) unsigned char smem_1k[];
+  unsigned char* const smem = smem_1k;
+  constexpr int kOffFix = kSlots * kSlotBytes;
+  DenseBwdTcCtl& ctl = *reinterpret_cast<DenseBwdTcCtl*>(smem + kOffCtl);
+  float* stats = reinterpret_cast<float*>(smem + kOffCtl + kBwdStatOff);
+  volatile int* abort_flag = &ctl.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int cta = blockIdx.x / 2;
+
+  // ---------------------------------------------------------------- set-up
+  if (smem_u32(smem) & 1023u) {                      // the swizzled tiles need it; the same in both CTAs
+    report_error(kErrWaitTimeout);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&ctl.slot_full[i], 1);
+      mbar_init(&ctl.peer_full[i], 1);
+      mbar_init(&ctl.slot_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.w_full[i], kSoftmaxWarps * 2);
+      mbar_init(&ctl.st_full[i], 1);
+      mbar_init(&ctl.st_free[i], kSoftmaxWarps);
+    }
+    mbar_init(&ctl.s_free, kSoftmaxWarps * 2);
+    mbar_init(&ctl.dp_full, 1);
+    mbar_init(&ctl.fix_full, kQWarps * 2);
+    mbar_init(&ctl.fix_empty, 1);
+    mbar_init(&ctl.o_full, 1);
+    mbar_init(&ctl.o_free, kSoftmaxWarps * 2);
+    mbar_init(&ctl.mma_done, 1);
+    ctl.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc_cg<2>(&ctl.tmem_base, dense_tc::kTmemCols);
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+  pdl_wait();
+  pdl_trigger();
+
+  DenseWalk walk;
+  walk.init(t, cta);
+  DensePiece p;
+  DenseUnit x;
+  // the next piece of a segment that is not flagged (the same in every role and CTA)
+  auto next = [&]() -> bool {
+    while (walk.next(t, p, x))
+      if (!a.flags[t.slot[x.si]]) return true;
+    return false;
+  };
+  if (warp == kProducerWarp) {
+    // ============================================================ TMA producer
+    // A slot is four boxes of 64 lines x 64 dims, one per lane: rows of this
+    // CTA's half x 256 dims (S, dP), or 128 rows x this CTA's half of the dims.
+    int64_t item = 0, gs = 0;
+    bool ok = true;
+    while (ok && next()) {
+      if (warp_aborted(abort_flag)) {
+        ok = false;
+        break;
+      }
+      const int n = p.c1 - p.c0;
+      for (int j = 0; j < kProducts * n && ok; ++j, ++item) {
+        int kind, c;
+        bwd_item<M>(j, n, kind, c);
+        c += p.c0;
+        const int slot = (int)(item % kSlots);
+        const int slab = kind == 2 ? lane & 1 : lane & 3, run = kind == 2 ? (lane >> 1) & 1 : 0;
+        const int off = kind == 2 ? slab * 16384 + run * 8192 : slab * 8192;
+        const int head = kByKeys ? x.grp * t.hpg + c % t.hpg : x.grp;
+        const int64_t r0 = kByKeys ? x.row0 + (int64_t)(c / t.hpg) * kKeys : (int64_t)c * kKeys;   // of the segment
+        const int32_t cx = head * kHeadDim + slab * 64 + (kind == 2 ? (int)rank * 128 : 0);
+        const int32_t cy = t.q_offset[x.si] + (int32_t)r0 + (kind == 2 ? run * 64 : (int)rank * 64);
+        if (!(ok = warp_wait_sleep(&ctl.slot_empty[slot], (uint32_t)(((item / kSlots) & 1) ^ 1), abort_flag))) break;
+        if (lane == 0) mbar_expect_tx(&ctl.slot_full[slot], kSlotBytes);
+        __syncwarp();
+        if (lane < 4)
+          tma_load_2d(smem + slot * kSlotBytes + off, kind == 0 ? &tm_s : kind == 1 ? &tm_p : &tm_d, cx, cy,
+                      &ctl.slot_full[slot]);
+        if (kByKeys && kind == 0) {                  // the chunk's row statistics
+          const int b = (int)(gs & 1);
+          if (!(ok = warp_wait_sleep(&ctl.st_free[b], (uint32_t)(((gs >> 1) & 1) ^ 1), abort_flag))) {
+            ++item;
+            break;
+          }
+          if (lane == 0) {
+            const int64_t at = (int64_t)head * a.stat_rows + (int64_t)t.slot[x.si] * kStatTile + r0;
+            mbar_expect_tx(&ctl.st_full[b], M == kDv ? 512 : 1024);
+            bulk_load(stats + b * 256, a.lse2 + at, 512, &ctl.st_full[b]);
+            if (M != kDv) bulk_load(stats + b * 256 + 128, a.delta + at, 512, &ctl.st_full[b]);
+          }
+          __syncwarp();
+          ++gs;
+        }
+      }
+    }
+    if (!ok) {                                       // no copy outlives the CTA
+      volatile int never = 0;
+      for (int64_t i = item > kSlots ? item - kSlots : 0; i < item; ++i)
+        if (lane == 0) mbar_wait(&ctl.slot_full[i % kSlots], (uint32_t)((i / kSlots) & 1), &never);
+      for (int64_t i = gs > 2 ? gs - 2 : 0; i < gs; ++i)
+        if (lane == 0) mbar_wait(&ctl.st_full[i & 1], (uint32_t)((i >> 1) & 1), &never);
+    }
+  } else if (warp == kMmaWarp && rank == 0) {
+    // ============================================================ MMA issuer
+    int64_t gc = 0, uc = 0;                          // chunks and pieces so far
+    const uint32_t sb = smem_u32(smem);
+    bool ok = true;
+    auto slot_ready = [&](int64_t it) -> bool {
+      const uint32_t ph = (uint32_t)((it / kSlots) & 1);
+      return warp_wait_sleep(&ctl.slot_full[it % kSlots], ph, abort_flag) &&
+             warp_wait_sleep(&ctl.peer_full[it % kSlots], ph, abort_flag);
+    };
+    // S (kind 0) or dP (kind 1) of the piece's chunk c
+    auto scores = [&](int kind, int c, int n) -> bool {
+      const int64_t it = kProducts * gc + bwd_pos<M>(kind, c, n);
+      const int slot = (int)(it % kSlots);
+      const int b = (int)((gc + c) % kBufs);
+      // with one S buffer: the softmax has read the last chunk's.  With two, P of
+      // chunk c-2 was read by a product issued before.
+      if (kBufs == 1 && kind == 0 && !warp_wait_sleep(&ctl.s_free, (uint32_t)(((gc + c) & 1) ^ 1), abort_flag))
+        return false;
+      if (!slot_ready(it)) return false;
+      fence_acquire_cluster();
+      tc_fence_after();
+      if (lane == 0) {
+        fence_proxy_async_smem();
+        const uint32_t b_addr = sb + slot * kSlotBytes, a_addr = sb + kOffFix + kind * kQBytes;
+        const uint32_t d = tmem + (kind == 1 ? kTmemP : (uint32_t)b * 128);
+#pragma unroll
+        for (int kk = 0; kk < 16; ++kk) {            // k-steps of 16 dims
+          const int slab = kk >> 2, sub = kk & 3;
+          const uint64_t da = desc_sw128(a_addr + slab * 16384 + sub * 32, 16, 1024);
+          const uint64_t db = desc_sw128(b_addr + slab * 8192 + sub * 32, 16, 1024);
+          umma_ss<2>(d, da, db, Pair::kIdescS, kk != 0);
+        }
+        umma_commit_cg<2>(&ctl.slot_empty[slot]);
+        umma_commit_cg<2>(kind == 0 ? &ctl.s_full[b] : &ctl.dp_full);
+        if (c == n - 1 && kind == kProducts - 2) umma_commit_cg<2>(&ctl.fix_empty);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto grad = [&](int c, int n) -> bool {
+      const int b = (int)((gc + c) % kBufs);
+      if (!warp_wait_sleep(&ctl.w_full[b], (uint32_t)(((gc + c) / kBufs) & 1), abort_flag)) return false;
+      if (c == 0 && !warp_wait_sleep(&ctl.o_free, (uint32_t)((uc & 1) ^ 1), abort_flag)) return false;
+      const int64_t it = kProducts * gc + bwd_pos<M>(2, c, n);
+      const int slot = (int)(it % kSlots);
+      if (!slot_ready(it)) return false;
+      fence_acquire_cluster();
+      tc_fence_after();
+      if (lane == 0) {
+        fence_proxy_async_smem();
+        const uint32_t b_addr = sb + slot * kSlotBytes;
+        const uint32_t w = tmem + (M == kDv ? (uint32_t)b * 128 : kTmemP);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {             // k-steps of 16 chunk columns; each half's start at its columns
+          const uint64_t db = desc_sw128(b_addr + kk * 2048, 16384, 1024);
+          umma_ts<2>(tmem + kTmemD, w + (kk >> 2) * 64 + (kk & 3) * 8, db, Pair::kIdescPV, (c | kk) != 0);
+        }
+        umma_commit_cg<2>(&ctl.slot_empty[slot]);
+        if (c == n - 1) umma_commit_cg<2>(&ctl.o_full);
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && next()) {
+      if (warp_aborted(abort_flag)) break;
+      if (!(ok = warp_wait_sleep(&ctl.fix_full, (uint32_t)(uc & 1), abort_flag))) break;
+      const int n = p.c1 - p.c0;
+      ok = scores(0, 0, n);
+      if (kProducts == 3) ok = ok && scores(1, 0, n);
+      for (int c = 0; c < n && ok; ++c) {
+        if (c + 1 < n) ok = scores(0, c + 1, n);
+        ok = ok && grad(c, n);
+        if (kProducts == 3 && c + 1 < n) ok = ok && scores(1, c + 1, n);
+      }
+      gc += n;
+      ++uc;
+    }
+    // every MMA issued above has finished before TMEM is freed
+    if (lane == 0) {
+      umma_commit_pair_local(&ctl.mma_done);
+      volatile int never = 0;
+      mbar_wait(&ctl.mma_done, 0, &never);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ============================================================ rank 1: slot full, forwarded to rank 0
+    int64_t item = 0;
+    bool ok = true;
+    while (ok && next()) {
+      if (warp_aborted(abort_flag)) break;
+      for (int j = 0; j < kProducts * (p.c1 - p.c0); ++j, ++item) {
+        const int slot = (int)(item % kSlots);
+        if (!(ok = warp_wait_sleep(&ctl.slot_full[slot], (uint32_t)((item / kSlots) & 1), abort_flag))) break;
+        if (lane == 0) mbar_arrive_cluster(&ctl.peer_full[slot], 0);
+        __syncwarp();
+      }
+    }
+  } else if (warp >= kQWarp) {
+    // ============================================================ stationary tiles of the next unit
+    const int qw = warp - kQWarp;
+    int64_t uc = 0;
+    while (next()) {
+      if (warp_aborted(abort_flag)) break;
+      if (!warp_wait_sleep(&ctl.fix_empty, (uint32_t)((uc & 1) ^ 1), abort_flag)) break;
+      const int valid = x.nrows - (int)rank * 128;   // rows of this CTA (may be <= 0 or > 128)
+      const int64_t row0 = x.row0 + rank * 128;
+#pragma unroll 4
+      for (int i = 0; i < 64; ++i) {
+        const int r = qw * 64 + i;
+        if (r < valid) {
+          const int64_t row = row0 + r;
+          const int64_t at = kByKeys ? ((int64_t)t.q_offset[x.si] + row) * t.G + x.grp
+                                     : ((int64_t)t.q_offset[x.si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg +
+                                           row % t.hpg;
+          const uint32_t dst = smem_u32(smem + kOffFix) + (lane >> 3) * 16384 + r * 128 +
+                               (((lane & 7) ^ (r & 7)) << 4);
+          cp_async16(dst, a.fix0 + at * kHeadDim + lane * 8, 16);
+          if (R::kTiles == 2) cp_async16(dst + kQBytes, a.fix1 + at * kHeadDim + lane * 8, 16);
+        }
+      }
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(&ctl.fix_full, 0);
+      ++uc;
+    }
+    cp_async_wait_all();
+  } else if (warp < kSoftmaxWarps) {
+    // ============================================================ P, dS and the epilogue
+    const int quad = warp & 3, half = warp >> 2;
+    const int li = quad * 32 + lane;                 // TMEM lane: stationary row of this CTA
+    const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+    const float tau2 = a.scale * 1.4426950408889634f;
+    int64_t gc = 0, uc = 0;
+    // No early exit: after an abort every wait returns at once.
+    while (next()) {
+      const int n = p.c1 - p.c0;
+      const int valid = x.nrows - (int)rank * 128;
+      const bool active = li < valid;
+      const int64_t row = x.row0 + (active ? (int)rank * 128 + li : 0);
+      const int32_t seg_n = t.q_len[x.si];
+      const int32_t own = kByKeys ? (int32_t)(x.row0 + rank * 128 + li) : (int32_t)(row / t.hpg);   // position
+      const int64_t at = kByKeys ? ((int64_t)t.q_offset[x.si] + row) * t.G + x.grp
+                                 : ((int64_t)t.q_offset[x.si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg +
+                                       row % t.hpg;
+      float lse2 = 0.f, delta = 0.f;                 // of this thread's row (dQ)
+      if (!kByKeys) {
+        const int64_t sat = ((int64_t)x.grp * t.hpg + row % t.hpg) * a.stat_rows +
+                            (int64_t)t.slot[x.si] * kStatTile + row / t.hpg;
+        lse2 = a.lse2[sat];
+        delta = a.delta[sat];
+      }
+      // first position of this CTA's stationary rows (dQ: below it no key is masked), last one (dK, dV)
+      const int32_t edge = kByKeys ? (int32_t)(x.row0 + rank * 128 + 127)
+                                   : (int32_t)((x.row0 + rank * 128) / t.hpg);
+      // Rows behind the segment's end become zero in the operand of chunk c's
+      // product.  Called once the chunk's last score product is seen done: the
+      // slot's occupant before was consumed by a product issued earlier.
+      auto clear_tail = [&](int c, int32_t j0) {
+        const int64_t it = kProducts * (gc - c) + bwd_pos<M>(2, c, n);
+        mbar_wait_sleep(&ctl.slot_full[it % kSlots], (uint32_t)((it / kSlots) & 1), abort_flag);
+        unsigned char* ds = smem + (it % kSlots) * kSlotBytes;
+        for (int i = threadIdx.x + (seg_n - j0) * 16; i < kKeys * 16; i += kSoftmaxWarps * 32)
+          *reinterpret_cast<uint4*>(ds + ((i >> 3) & 1) * 16384 + (i >> 4) * 128 + ((i & 7) << 4)) =
+              make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      };
+      for (int c = 0; c < n; ++c, ++gc) {
+        const int cc = p.c0 + c;
+        const int b = (int)(gc % kBufs);
+        const int32_t j0 = kByKeys ? (int32_t)x.row0 + (cc / t.hpg) * kKeys : cc * kKeys;   // first position of the columns
+        const float* st_l = stats + (gc & 1) * 256 + half * 64;
+        const float* st_d = st_l + 128;
+        if (kByKeys) mbar_wait_sleep(&ctl.st_full[gc & 1], (uint32_t)((gc >> 1) & 1), abort_flag);
+        mbar_wait_sleep(&ctl.s_full[b], (uint32_t)((gc / kBufs) & 1), abort_flag);
+        tc_fence_after();
+        float w[64];
+#pragma unroll
+        for (int k = 0; k < 64; k += 16) {
+          float v[16];
+          tmem_ld16(lane_addr + b * 128 + half * 64 + k, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[k + i] = v[i];
+        }
+        tmem_wait_ld();
+        if (kBufs == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(&ctl.s_free, 0);
+        }
+        // columns lo .. hi-1 of this thread's 64 count
+        int lo = 0, hi = 64;
+        bool cut = j0 + kKeys > seg_n;
+        if (kByKeys) {
+          cut |= j0 < edge;
+          lo = own - j0 - half * 64;
+          hi = min(64, seg_n - j0 - half * 64);
+        } else {
+          cut |= j0 + kKeys - 1 > edge;
+          hi = own - j0 - half * 64 + 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 64; k += 4) {
+          float4 l = make_float4(lse2, lse2, lse2, lse2);
+          if (kByKeys) l = *reinterpret_cast<const float4*>(st_l + k);
+          w[k] = ex2_approx(fmaf(w[k], tau2, -l.x));
+          w[k + 1] = ex2_approx(fmaf(w[k + 1], tau2, -l.y));
+          w[k + 2] = ex2_approx(fmaf(w[k + 2], tau2, -l.z));
+          w[k + 3] = ex2_approx(fmaf(w[k + 3], tau2, -l.w));
+        }
+        uint32_t dst = lane_addr + b * 128 + half * 64;
+        if (M == kDv) {
+          if (j0 + kKeys > seg_n) clear_tail(c, j0);
+          if (cut) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) w[i] = (i >= lo && i < hi) ? w[i] : 0.f;
+          }
+        } else {
+          dst = lane_addr + kTmemP + half * 64;
+          mbar_wait_sleep(&ctl.dp_full, (uint32_t)(gc & 1), abort_flag);
+          tc_fence_after();
+          if (j0 + kKeys > seg_n) clear_tail(c, j0);
+#pragma unroll
+          for (int k = 0; k < 64; k += 32) {
+            float v[2][16];
+            tmem_ld16(dst + k, v[0]);
+            tmem_ld16(dst + k + 16, v[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              float4 d = make_float4(delta, delta, delta, delta);
+              if (kByKeys) d = *reinterpret_cast<const float4*>(st_d + k + i);
+              w[k + i] *= v[i >> 4][i & 15] - d.x;
+              w[k + i + 1] *= v[i >> 4][(i & 15) + 1] - d.y;
+              w[k + i + 2] *= v[i >> 4][(i & 15) + 2] - d.z;
+              w[k + i + 3] *= v[i >> 4][(i & 15) + 3] - d.w;
+            }
+          }
+          if (cut) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) w[i] = (i >= lo && i < hi) ? w[i] : 0.f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 64; k += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(w[k + 2 * i], w[k + 2 * i + 1]);
+          tmem_st16u(dst + k / 2, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster(&ctl.w_full[b], 0);
+          if (kByKeys) mbar_arrive(&ctl.st_free[gc & 1]);
+        }
+      }
+      mbar_wait_sleep(&ctl.o_full, (uint32_t)(uc & 1), abort_flag);
+      tc_fence_after();
+      const bool whole = p.part < 0;
+      const float f = whole && M != kDv ? a.scale : 1.f;
+      float* pdst = whole ? nullptr
+                          : a.part + ((int64_t)p.part * t.prows + rank * 128 + li) * dense::kPartFloats + half * 128;
+      __nv_bfloat16* orow = a.out + at * kHeadDim + half * 128;
+#pragma unroll 1
+      for (int piece = 0; piece < 8; ++piece) {
+        float o[16];
+        tmem_ld16(lane_addr + kTmemD + half * 128 + piece * 16, o);
+        tmem_wait_ld();
+        if (!active) continue;
+        if (whole) {
+          uint4 v[2];
+          uint32_t* u = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(o[2 * i] * f, o[2 * i + 1] * f);
+          *reinterpret_cast<uint4*>(orow + piece * 16) = v[0];
+          *reinterpret_cast<uint4*>(orow + piece * 16 + 8) = v[1];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(pdst + piece * 16 + 4 * i) =
+                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(&ctl.o_free, 0);
+      ++uc;
+    }
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_cg<2>(tmem, dense_tc::kTmemCols);
+  }
+}
+
+// Adds up the pieces of each cut unit in the order of their chunks, scales and
+// rounds.  One warp per stationary row.
+__global__ void __launch_bounds__(128)
+    dense_bwd_combine_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseSplits sp,
+                             const float* part, const int32_t* flags, __nv_bfloat16* out, int H, float factor) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x;
+  const int u = sp.unit[i];
+  const DenseUnit x = dense_unit(t, u);
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  if (r >= x.nrows || flags[t.slot[x.si]]) return;
+  float acc[8] = {};
+  for (int c = sp.first[i]; c <= sp.last[i]; ++c) {
+    const int part_of = dense_piece_slot(t, u, c);
+    if (part_of < 0) continue;
+    const float4* p = reinterpret_cast<const float4*>(part + ((int64_t)part_of * t.prows + r) * dense::kPartFloats);
+    const float4 v0 = p[2 * lane], v1 = p[2 * lane + 1];
+    acc[0] += v0.x; acc[1] += v0.y; acc[2] += v0.z; acc[3] += v0.w;
+    acc[4] += v1.x; acc[5] += v1.y; acc[6] += v1.z; acc[7] += v1.w;
+  }
+  const int64_t row = x.row0 + r;
+  const int64_t at = t.by_keys ? ((int64_t)t.q_offset[x.si] + row) * t.G + x.grp
+                               : ((int64_t)t.q_offset[x.si] + row / t.hpg) * H + (int64_t)x.grp * t.hpg + row % t.hpg;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] *= factor;
+  Vec8<__nv_bfloat16> v;
+  v.set(acc);
+  v.store(out + at * kHeadDim + lane * 8);
+}
+
+// Row statistics for the gradient kernels, one warp per (token, head): delta =
+// dout . o, by token for the CUDA-core kernels and, with lse in log2 units, by
+// head and statistics row for the tensor-core kernels; rows behind a segment's
+// end get lse +inf (P = 0).  A segment with an lse, delta, key or value that
+// is not finite is flagged.  Items: a segment's tokens rounded up to 128.
+__global__ void __launch_bounds__(256)
+    dense_stats_kernel(const __grid_constant__ SegTable st, const __nv_bfloat16* o, const __nv_bfloat16* dout,
+                       const float* lse, const __nv_bfloat16* k, const __nv_bfloat16* v, float* delta, float* lse2_h,
+                       float* delta_h, int32_t* flags, int64_t stat_rows, int H, int G) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int item = (int)(w / H), h = (int)(w - (int64_t)item * H);
+  if (item >= st.item0[st.n]) return;
+  const int si = find_segment(st, item);
+  const int j = item - st.item0[si];
+  const int64_t sat = (int64_t)h * stat_rows + (int64_t)st.slot[si] * dense_bwd::kStatTile + j;
+  if (j >= st.q_len[si]) {
+    if (lane == 0) {
+      lse2_h[sat] = INFINITY;
+      delta_h[sat] = 0.f;
+    }
+    return;
+  }
+  const int64_t at = (int64_t)(st.q_offset[si] + j) * H + h;
+  Vec8<__nv_bfloat16> a, b;
+  a.load(o + at * kHeadDim + lane * 8);
+  b.load(dout + at * kHeadDim + lane * 8);
+  const float l = lse[at];
+  bool bad = false;
+  if (h < G) {
+    const int64_t kv = ((int64_t)(st.q_offset[si] + j) * G + h) * kHeadDim + lane * 8;
+    const uint4 x = *reinterpret_cast<const uint4*>(k + kv), y = *reinterpret_cast<const uint4*>(v + kv);
+    const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bad |= (u[i] & 0x7f80u) == 0x7f80u || (u[i] & 0x7f800000u) == 0x7f800000u;
+  }
+  float fa[8], fb[8], s = 0.f;
+  a.get(fa);
+  b.get(fb);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaf(fa[i], fb[i], s);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  bad |= !isfinite(s) || !isfinite(l);
+  if (__any_sync(0xffffffffu, bad) && lane == 0) flags[st.slot[si]] = 1;
+  if (lane == 0) {
+    delta[at] = s;
+    lse2_h[sat] = l * 1.4426950408889634f;
+    delta_h[sat] = s;
+  }
+}
+
+}  // namespace qsa

@@ -277,6 +277,7 @@ struct DenseBwdArgs {
   void* dv;
   int H;
   float scale;
+  const int32_t* flags;    // null: every segment; else by SegTable/DenseTable slot, nonzero: this segment
 };
 
 // delta[i][h] = dout[i][h] . o[i][h], one warp per row of the segments.
@@ -330,7 +331,17 @@ __device__ __forceinline__ void simt_p_ds(const float* Qs, const float* Os, cons
   }
 }
 
-// dq of one (64-row tile, group): loops over its keys.
+// True if a segment of the table is these kernels' work: all of them, or (with
+// flags) those whose flag is set.
+template <typename Table>
+__device__ __forceinline__ bool simt_any(const Table& t, const int32_t* flags) {
+  if (!flags) return true;
+  bool any = false;
+  for (int i = threadIdx.x; i < t.n; i += blockDim.x) any |= flags[t.slot[i]] != 0;
+  return __syncthreads_or(any);
+}
+
+// dq of (64-row tile, group): loops over its keys.
 template <typename T>
 __global__ void __launch_bounds__(dense_simt::kThreads)
     dense_dq_simt_kernel(const __grid_constant__ DenseTable t, DenseBwdArgs a) {
@@ -348,62 +359,68 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
   const int tx = threadIdx.x & 15, ra = (threadIdx.x >> 4) * 4;
   pdl_wait();
   pdl_trigger();
-  const DenseUnit x = dense_unit(t, blockIdx.x);
-  const int si = x.si;
-  auto q_at = [&](int r) -> int64_t {
-    const int64_t row = x.row0 + r;
-    return (int64_t)(t.q_offset[si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg + row % t.hpg;
-  };
-  auto rows_of = [&](const void* base) {
-    return [&, base](int r) -> const T* {
-      return r < x.nrows ? (const T*)base + q_at(r) * kHeadDim : nullptr;
-    };
-  };
-  simt_load_rows(Qs, kBRows, (const T*)a.q, rows_of(a.q));
-  simt_load_rows(Os, kBRows, (const T*)a.dout, rows_of(a.dout));
-  if (threadIdx.x < kBRows) {
-    const bool v = threadIdx.x < x.nrows;
-    st_lse[threadIdx.x] = v ? a.lse[q_at(threadIdx.x)] * 1.4426950408889634f : 0.f;
-    st_delta[threadIdx.x] = v ? a.delta[q_at(threadIdx.x)] : 0.f;
-  }
-  float acc[4][16];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int k = 0; k < 16; ++k) acc[i][k] = 0.f;
-  const int64_t first_pos = x.row0 / t.hpg;
-  for (int64_t j0 = 0; j0 < x.kv_len; j0 += kBKeys) {
+  if (!simt_any(t, a.flags)) return;
+  const int n_units = t.item0[t.n] * t.G;
+  for (int unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
+    const DenseUnit x = dense_unit(t, unit);
+    const int si = x.si;
+    if (a.flags && !a.flags[t.slot[si]]) continue;
     __syncthreads();
-    auto keys_of = [&](const void* base) {
+    auto q_at = [&](int r) -> int64_t {
+      const int64_t row = x.row0 + r;
+      return (int64_t)(t.q_offset[si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg + row % t.hpg;
+    };
+    auto rows_of = [&](const void* base) {
       return [&, base](int r) -> const T* {
-        const int64_t j = j0 + r;
-        return j < x.kv_len ? (const T*)base + ((int64_t)(t.q_offset[si] + j) * t.G + x.grp) * kHeadDim : nullptr;
+        return r < x.nrows ? (const T*)base + q_at(r) * kHeadDim : nullptr;
       };
     };
-    simt_load_rows(Ks, kBKeys, (const T*)a.k, keys_of(a.k));
-    simt_load_rows(Vs, kBKeys, (const T*)a.v, keys_of(a.v));
-    sm100::cp_async_wait_all();
-    __syncthreads();
-    simt_p_ds(Qs, Os, Ks, Vs, Ps, Ds, st_lse, st_delta, x.row0, x.nrows, t.hpg, j0, x.kv_len, s2);
-    __syncthreads();
-    int limit[4];
+    simt_load_rows(Qs, kBRows, (const T*)a.q, rows_of(a.q));
+    simt_load_rows(Os, kBRows, (const T*)a.dout, rows_of(a.dout));
+    if (threadIdx.x < kBRows) {
+      const bool v = threadIdx.x < x.nrows;
+      st_lse[threadIdx.x] = v ? a.lse[q_at(threadIdx.x)] * 1.4426950408889634f : 0.f;
+      st_delta[threadIdx.x] = v ? a.delta[q_at(threadIdx.x)] : 0.f;
+    }
+    float acc[4][16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) limit[i] = (int)min((int64_t)kBKeys, (x.row0 + ra + i) / t.hpg - j0 + 1);
-    simt_accumulate<4>(Ds, kBLd, Ks, ra, tx, kBKeys, j0 + kBKeys - 1 > first_pos, limit, acc);
-  }
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (ra + i >= x.nrows) continue;
-    T* dst = (T*)a.dq + q_at(ra + i) * kHeadDim;
+      for (int k = 0; k < 16; ++k) acc[i][k] = 0.f;
+    const int64_t first_pos = x.row0 / t.hpg;
+    for (int64_t j0 = 0; j0 < x.kv_len; j0 += kBKeys) {
+      __syncthreads();
+      auto keys_of = [&](const void* base) {
+        return [&, base](int r) -> const T* {
+          const int64_t j = j0 + r;
+          return j < x.kv_len ? (const T*)base + ((int64_t)(t.q_offset[si] + j) * t.G + x.grp) * kHeadDim : nullptr;
+        };
+      };
+      simt_load_rows(Ks, kBKeys, (const T*)a.k, keys_of(a.k));
+      simt_load_rows(Vs, kBKeys, (const T*)a.v, keys_of(a.v));
+      sm100::cp_async_wait_all();
+      __syncthreads();
+      simt_p_ds(Qs, Os, Ks, Vs, Ps, Ds, st_lse, st_delta, x.row0, x.nrows, t.hpg, j0, x.kv_len, s2);
+      __syncthreads();
+      int limit[4];
 #pragma unroll
-    for (int jj = 0; jj < 4; ++jj)
-      simt_store4(dst + 4 * tx + 64 * jj, acc[i][4 * jj] * a.scale, acc[i][4 * jj + 1] * a.scale,
-                  acc[i][4 * jj + 2] * a.scale, acc[i][4 * jj + 3] * a.scale);
+      for (int i = 0; i < 4; ++i) limit[i] = (int)min((int64_t)kBKeys, (x.row0 + ra + i) / t.hpg - j0 + 1);
+      simt_accumulate<4>(Ds, kBLd, Ks, ra, tx, kBKeys, j0 + kBKeys - 1 > first_pos, limit, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (ra + i >= x.nrows) continue;
+      T* dst = (T*)a.dq + q_at(ra + i) * kHeadDim;
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+        simt_store4(dst + 4 * tx + 64 * jj, acc[i][4 * jj] * a.scale, acc[i][4 * jj + 1] * a.scale,
+                    acc[i][4 * jj + 2] * a.scale, acc[i][4 * jj + 3] * a.scale);
+    }
   }
 }
 
-// dk and dv of one (32-key tile, group): loops over the rows that see it.  The
-// block index counts a segment's key tiles from its start (most rows first);
+// dk and dv of (32-key tile, group): loops over the rows that see it.  The
+// unit counts a segment's key tiles from its start (most rows first);
 // a thread owns 4 keys x 8 dims of both.
 template <typename T>
 __global__ void __launch_bounds__(dense_simt::kThreads)
@@ -422,83 +439,89 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
   const int kq = (threadIdx.x >> 5) * 4, dl = (threadIdx.x & 31) * 4;
   pdl_wait();
   pdl_trigger();
-  const int tile = blockIdx.x / G, grp = blockIdx.x - tile * G;
-  const int si = find_segment(st, tile);
-  const int64_t j0 = (int64_t)(tile - st.item0[si]) * kBKeys;
-  const int64_t n = st.q_len[si], q0 = st.q_offset[si];
-  auto key_at = [&](int r) -> int64_t { return ((q0 + j0 + r) * G + grp) * kHeadDim; };
-  auto keys_of = [&](const void* base) {
-    return [&, base](int r) -> const T* { return j0 + r < n ? (const T*)base + key_at(r) : nullptr; };
-  };
-  simt_load_rows(Ks, kBKeys, (const T*)a.k, keys_of(a.k));
-  simt_load_rows(Vs, kBKeys, (const T*)a.v, keys_of(a.v));
-  float dk[4][8], dv[4][8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) dk[i][k] = dv[i][k] = 0.f;
-  for (int64_t row0 = j0 * hpg; row0 < n * hpg; row0 += kBRows) {
-    const int nrows = (int)min((int64_t)kBRows, n * hpg - row0);
-    auto q_at = [&](int r) -> int64_t {
-      const int64_t row = row0 + r;
-      return (q0 + row / hpg) * a.H + (int64_t)grp * hpg + row % hpg;
+  if (!simt_any(st, a.flags)) return;
+  const int n_units = st.item0[st.n] * G;
+  for (int unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
+    const int tile = unit / G, grp = unit - tile * G;
+    const int si = find_segment(st, tile);
+    if (a.flags && !a.flags[st.slot[si]]) continue;
+    __syncthreads();
+    const int64_t j0 = (int64_t)(tile - st.item0[si]) * kBKeys;
+    const int64_t n = st.q_len[si], q0 = st.q_offset[si];
+    auto key_at = [&](int r) -> int64_t { return ((q0 + j0 + r) * G + grp) * kHeadDim; };
+    auto keys_of = [&](const void* base) {
+      return [&, base](int r) -> const T* { return j0 + r < n ? (const T*)base + key_at(r) : nullptr; };
     };
-    auto rows_of = [&](const void* base) {
-      return [&, base](int r) -> const T* {
-        return r < nrows ? (const T*)base + q_at(r) * kHeadDim : nullptr;
+    simt_load_rows(Ks, kBKeys, (const T*)a.k, keys_of(a.k));
+    simt_load_rows(Vs, kBKeys, (const T*)a.v, keys_of(a.v));
+    float dk[4][8], dv[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) dk[i][k] = dv[i][k] = 0.f;
+    for (int64_t row0 = j0 * hpg; row0 < n * hpg; row0 += kBRows) {
+      const int nrows = (int)min((int64_t)kBRows, n * hpg - row0);
+      auto q_at = [&](int r) -> int64_t {
+        const int64_t row = row0 + r;
+        return (q0 + row / hpg) * a.H + (int64_t)grp * hpg + row % hpg;
       };
-    };
-    __syncthreads();
-    simt_load_rows(Qs, kBRows, (const T*)a.q, rows_of(a.q));
-    simt_load_rows(Os, kBRows, (const T*)a.dout, rows_of(a.dout));
-    if (threadIdx.x < kBRows) {
-      const bool v = threadIdx.x < nrows;
-      st_lse[threadIdx.x] = v ? a.lse[q_at(threadIdx.x)] * 1.4426950408889634f : 0.f;
-      st_delta[threadIdx.x] = v ? a.delta[q_at(threadIdx.x)] : 0.f;
-    }
-    sm100::cp_async_wait_all();
-    __syncthreads();
-    simt_p_ds(Qs, Os, Ks, Vs, Ps, Ds, st_lse, st_delta, row0, nrows, hpg, j0, n, s2);
-    __syncthreads();
-    // keys of the tile after the first row's position: a row before a key does not touch it
-    const bool limited = j0 + kBKeys - 1 > row0 / hpg;
-    for (int r = 0; r < nrows; ++r) {
-      const float4 p = *reinterpret_cast<const float4*>(Ps + r * kBLd + kq);
-      const float4 s = *reinterpret_cast<const float4*>(Ds + r * kBLd + kq);
-      const int64_t pos = limited ? (row0 + r) / hpg : 0;
-      const float pp[4] = {p.x, p.y, p.z, p.w}, ss[4] = {s.x, s.y, s.z, s.w};
-      float4 x[2], y[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        x[h] = *reinterpret_cast<const float4*>(Qs + r * kLd + dl + 128 * h);
-        y[h] = *reinterpret_cast<const float4*>(Os + r * kLd + dl + 128 * h);
+      auto rows_of = [&](const void* base) {
+        return [&, base](int r) -> const T* {
+          return r < nrows ? (const T*)base + q_at(r) * kHeadDim : nullptr;
+        };
+      };
+      __syncthreads();
+      simt_load_rows(Qs, kBRows, (const T*)a.q, rows_of(a.q));
+      simt_load_rows(Os, kBRows, (const T*)a.dout, rows_of(a.dout));
+      if (threadIdx.x < kBRows) {
+        const bool v = threadIdx.x < nrows;
+        st_lse[threadIdx.x] = v ? a.lse[q_at(threadIdx.x)] * 1.4426950408889634f : 0.f;
+        st_delta[threadIdx.x] = v ? a.delta[q_at(threadIdx.x)] : 0.f;
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (limited && j0 + kq + i > pos) continue;
+      sm100::cp_async_wait_all();
+      __syncthreads();
+      simt_p_ds(Qs, Os, Ks, Vs, Ps, Ds, st_lse, st_delta, row0, nrows, hpg, j0, n, s2);
+      __syncthreads();
+      // keys of the tile after the first row's position: a row before a key does not touch it
+      const bool limited = j0 + kBKeys - 1 > row0 / hpg;
+      for (int r = 0; r < nrows; ++r) {
+        const float4 p = *reinterpret_cast<const float4*>(Ps + r * kBLd + kq);
+        const float4 s = *reinterpret_cast<const float4*>(Ds + r * kBLd + kq);
+        const int64_t pos = limited ? (row0 + r) / hpg : 0;
+        const float pp[4] = {p.x, p.y, p.z, p.w}, ss[4] = {s.x, s.y, s.z, s.w};
+        float4 x[2], y[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          dk[i][4 * h] = fmaf(ss[i], x[h].x, dk[i][4 * h]);
-          dk[i][4 * h + 1] = fmaf(ss[i], x[h].y, dk[i][4 * h + 1]);
-          dk[i][4 * h + 2] = fmaf(ss[i], x[h].z, dk[i][4 * h + 2]);
-          dk[i][4 * h + 3] = fmaf(ss[i], x[h].w, dk[i][4 * h + 3]);
-          dv[i][4 * h] = fmaf(pp[i], y[h].x, dv[i][4 * h]);
-          dv[i][4 * h + 1] = fmaf(pp[i], y[h].y, dv[i][4 * h + 1]);
-          dv[i][4 * h + 2] = fmaf(pp[i], y[h].z, dv[i][4 * h + 2]);
-          dv[i][4 * h + 3] = fmaf(pp[i], y[h].w, dv[i][4 * h + 3]);
+          x[h] = *reinterpret_cast<const float4*>(Qs + r * kLd + dl + 128 * h);
+          y[h] = *reinterpret_cast<const float4*>(Os + r * kLd + dl + 128 * h);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (limited && j0 + kq + i > pos) continue;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            dk[i][4 * h] = fmaf(ss[i], x[h].x, dk[i][4 * h]);
+            dk[i][4 * h + 1] = fmaf(ss[i], x[h].y, dk[i][4 * h + 1]);
+            dk[i][4 * h + 2] = fmaf(ss[i], x[h].z, dk[i][4 * h + 2]);
+            dk[i][4 * h + 3] = fmaf(ss[i], x[h].w, dk[i][4 * h + 3]);
+            dv[i][4 * h] = fmaf(pp[i], y[h].x, dv[i][4 * h]);
+            dv[i][4 * h + 1] = fmaf(pp[i], y[h].y, dv[i][4 * h + 1]);
+            dv[i][4 * h + 2] = fmaf(pp[i], y[h].z, dv[i][4 * h + 2]);
+            dv[i][4 * h + 3] = fmaf(pp[i], y[h].w, dv[i][4 * h + 3]);
+          }
         }
       }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (j0 + kq + i >= n) continue;
-    const int64_t at = key_at(kq + i) + dl;
+    for (int i = 0; i < 4; ++i) {
+      if (j0 + kq + i >= n) continue;
+      const int64_t at = key_at(kq + i) + dl;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      simt_store4((T*)a.dk + at + 128 * h, dk[i][4 * h] * a.scale, dk[i][4 * h + 1] * a.scale,
-                  dk[i][4 * h + 2] * a.scale, dk[i][4 * h + 3] * a.scale);
-      simt_store4((T*)a.dv + at + 128 * h, dv[i][4 * h], dv[i][4 * h + 1], dv[i][4 * h + 2], dv[i][4 * h + 3]);
+      for (int h = 0; h < 2; ++h) {
+        simt_store4((T*)a.dk + at + 128 * h, dk[i][4 * h] * a.scale, dk[i][4 * h + 1] * a.scale,
+                    dk[i][4 * h + 2] * a.scale, dk[i][4 * h + 3] * a.scale);
+        simt_store4((T*)a.dv + at + 128 * h, dv[i][4 * h], dv[i][4 * h + 1], dv[i][4 * h + 2], dv[i][4 * h + 3]);
+      }
     }
   }
 }

@@ -1007,7 +1007,15 @@ QSA_API size_t qsa_workspace_size(const qsa_config_t* cfg, const qsa_segment_t* 
         return SIZE_MAX;
       return ws;
     }
-    case QSA_OP_PROMPT_ATTN_BWD: return seg_rows(segs, n_segs) > 0 ? dense_bwd_ws(g, n_tokens) : 0;
+    case QSA_OP_PROMPT_ATTN_BWD: {
+      size_t ws = 0;
+      if (seg_rows(segs, n_segs) > 0 && guarded([&]() -> qsa_status_t {
+            ws = dense_bwd_ws(g, cfg->dtype == QSA_DTYPE_BF16, segs, n_segs, n_tokens);
+            return QSA_OK;
+          }) != QSA_OK)
+        return SIZE_MAX;
+      return ws;
+    }
   }
   return SIZE_MAX;
 }
