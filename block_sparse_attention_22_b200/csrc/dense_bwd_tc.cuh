@@ -24,8 +24,8 @@
 // they were computed from, so no warp waits for another's reads.
 //
 // Roles per CTA (12 warps): eight softmax warps (two per lane quadrant, each
-// thread one lane and 64 of a chunk's columns), one TMA producer, one MMA warp,
-// two loaders of the stationary tiles.  MMA order with three products:
+// thread one lane and 64 of a chunk's columns), one TMA producer, one thread that
+// issues the MMAs (in rank 0), two loaders of the stationary tiles.  MMA order with three products:
 //   S0 dP0 | S1 D0 dP1 | S2 D1 dP2 | ...
 // so that the exponentials of chunk c+1 run under D(c) and dP(c+1), and dS(c+1)
 // under S(c+2); one buffer each for S and dP is enough.  With two products (dV)
@@ -55,7 +55,11 @@ constexpr int kStatTile = 128;                        // tokens of a row of the 
 template <Grad M> struct Ring {
   static constexpr int kProducts = M == kDv ? 2 : 3;
   static constexpr int kTiles = M == kDv ? 1 : 2;     // stationary tiles of 64 KiB
-  static constexpr int kSlots = M == kDv ? 5 : 3;
+  // 32 KiB slots of the three streamed operands
+  static constexpr int kN0 = M == kDv ? 3 : 1, kN1 = M == kDv ? 0 : 1, kN2 = M == kDv ? 2 : 1;
+  static constexpr int kSlots = kN0 + kN1 + kN2;
+  __device__ static constexpr int slots(int kind) { return kind == 0 ? kN0 : kind == 1 ? kN1 : kN2; }
+  __device__ static constexpr int offset(int kind) { return (kind == 0 ? 0 : kind == 1 ? kN0 : kN0 + kN1) * kSlotBytes; }
   static constexpr int kBufs = M == kDv ? 2 : 1;      // S buffers
 };
 constexpr int kOffCtl = 5 * kSlotBytes + kQBytes;     // 229376, also 3 slots + 2 tiles
@@ -80,7 +84,9 @@ struct DenseBwdTcArgs {
 };
 
 struct DenseBwdTcCtl {
-  uint64_t slot_full[5], peer_full[5], slot_empty[5];
+  uint64_t full[2][3];                                // of S's and dP's operand, rank 0's: both CTAs' halves
+  uint64_t d_full[2];                                 // of the gradient's operand: this CTA's half
+  uint64_t empty[3][3];
   uint64_t fix_full, fix_empty;
   uint64_t s_full[2], s_free, dp_full, w_full[2];     // w: P (dV) or dS written
   uint64_t o_full, o_free;
@@ -105,13 +111,6 @@ __device__ __forceinline__ void bwd_item(int j, int n, int& kind, int& c) {
     c = (j == 0) ? 0 : (j == 3 * n - 1) ? n - 1 : (j % 3 == 1) ? j / 3 : (j % 3 == 2) ? (j + 1) / 3 : j / 3 - 1;
   }
 }
-template <dense_bwd::Grad M>
-__device__ __forceinline__ int bwd_pos(int kind, int c, int n) {
-  if constexpr (M == dense_bwd::kDv) return union_item(c, kind == 0 ? 0 : 1, n);
-  if (kind == 0) return c == 0 ? 0 : 3 * c - 1;
-  if (kind == 1) return 3 * c + 1;
-  return c == n - 1 ? 3 * n - 1 : 3 * c + 3;
-}
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -130,10 +129,10 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
   using namespace sm100;
   using R = Ring<M>;
   constexpr bool kByKeys = M != kDq;
-  constexpr int kSlots = R::kSlots, kProducts = R::kProducts, kBufs = R::kBufs;
+  constexpr int kProducts = R::kProducts, kBufs = R::kBufs;
   extern __shared__ __align__(1024) unsigned char smem_1k[];
   unsigned char* const smem = smem_1k;
-  constexpr int kOffFix = kSlots * kSlotBytes;
+  constexpr int kOffFix = R::kSlots * kSlotBytes;
   DenseBwdTcCtl& ctl = *reinterpret_cast<DenseBwdTcCtl*>(smem + kOffCtl);
   float* stats = reinterpret_cast<float*>(smem + kOffCtl + kBwdStatOff);
   volatile int* abort_flag = &ctl.abort;
@@ -147,12 +146,13 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&ctl.slot_full[i], 1);
-      mbar_init(&ctl.peer_full[i], 1);
-      mbar_init(&ctl.slot_empty[i], 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&ctl.full[0][i], 2);
+      mbar_init(&ctl.full[1][i], 2);
+      for (int k = 0; k < 3; ++k) mbar_init(&ctl.empty[k][i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.d_full[i], 1);
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.w_full[i], kSoftmaxWarps * 2);
       mbar_init(&ctl.st_full[i], 1);
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     // ============================================================ TMA producer
     // A slot is four boxes of 64 lines x 64 dims, one per lane: rows of this
     // CTA's half x 256 dims (S, dP), or 128 rows x this CTA's half of the dims.
-    int64_t item = 0, gs = 0;
+    int64_t gc = 0;                                  // chunks of the pieces before
     bool ok = true;
     while (ok && next()) {
       if (warp_aborted(abort_flag)) {
@@ -198,29 +198,33 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         break;
       }
       const int n = p.c1 - p.c0;
-      for (int j = 0; j < kProducts * n && ok; ++j, ++item) {
+      for (int j = 0; j < kProducts * n && ok; ++j) {
         int kind, c;
         bwd_item<M>(j, n, kind, c);
+        const int64_t xg = gc + c;
         c += p.c0;
-        const int slot = (int)(item % kSlots);
+        const int slot = (int)(xg % R::slots(kind));
+        const uint32_t phase = (uint32_t)((xg / R::slots(kind)) & 1);
+        unsigned char* to = smem + R::offset(kind) + slot * kSlotBytes;
         const int slab = kind == 2 ? lane & 1 : lane & 3, run = kind == 2 ? (lane >> 1) & 1 : 0;
         const int off = kind == 2 ? slab * 16384 + run * 8192 : slab * 8192;
         const int head = kByKeys ? x.grp * t.hpg + c % t.hpg : x.grp;
         const int64_t r0 = kByKeys ? x.row0 + (int64_t)(c / t.hpg) * kKeys : (int64_t)c * kKeys;   // of the segment
         const int32_t cx = head * kHeadDim + slab * 64 + (kind == 2 ? (int)rank * 128 : 0);
         const int32_t cy = t.q_offset[x.si] + (int32_t)r0 + (kind == 2 ? run * 64 : (int)rank * 64);
-        if (!(ok = warp_wait_sleep(&ctl.slot_empty[slot], (uint32_t)(((item / kSlots) & 1) ^ 1), abort_flag))) break;
-        if (lane == 0) mbar_expect_tx(&ctl.slot_full[slot], kSlotBytes);
-        __syncwarp();
-        if (lane < 4)
-          tma_load_2d(smem + slot * kSlotBytes + off, kind == 0 ? &tm_s : kind == 1 ? &tm_p : &tm_d, cx, cy,
-                      &ctl.slot_full[slot]);
+        if (!(ok = warp_wait_sleep(&ctl.empty[kind][slot], phase ^ 1, abort_flag))) break;
+        if (kind == 2) {
+          if (lane == 0) mbar_expect_tx(&ctl.d_full[slot], kSlotBytes);
+          __syncwarp();
+          if (lane < 4) tma_load_2d(to + off, &tm_d, cx, cy, &ctl.d_full[slot]);
+        } else {
+          if (lane == 0) mbar_expect_tx_leader<2>(&ctl.full[kind][slot], kSlotBytes);
+          __syncwarp();
+          if (lane < 4) tma_load_2d_leader<2>(to + off, kind == 0 ? &tm_s : &tm_p, cx, cy, &ctl.full[kind][slot]);
+        }
         if (kByKeys && kind == 0) {                  // the chunk's row statistics
-          const int b = (int)(gs & 1);
-          if (!(ok = warp_wait_sleep(&ctl.st_free[b], (uint32_t)(((gs >> 1) & 1) ^ 1), abort_flag))) {
-            ++item;
-            break;
-          }
+          const int b = (int)(xg & 1);
+          if (!(ok = warp_wait_sleep(&ctl.st_free[b], (uint32_t)(((xg >> 1) & 1) ^ 1), abort_flag))) break;
           if (lane == 0) {
             const int64_t at = (int64_t)head * a.stat_rows + (int64_t)t.slot[x.si] * kStatTile + r0;
             mbar_expect_tx(&ctl.st_full[b], M == kDv ? 512 : 1024);
@@ -228,42 +232,27 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
             if (M != kDv) bulk_load(stats + b * 256 + 128, a.delta + at, 512, &ctl.st_full[b]);
           }
           __syncwarp();
-          ++gs;
         }
       }
+      gc += n;
     }
-    if (!ok) {                                       // no copy outlives the CTA
-      volatile int never = 0;
-      for (int64_t i = item > kSlots ? item - kSlots : 0; i < item; ++i)
-        if (lane == 0) mbar_wait(&ctl.slot_full[i % kSlots], (uint32_t)((i / kSlots) & 1), &never);
-      for (int64_t i = gs > 2 ? gs - 2 : 0; i < gs; ++i)
-        if (lane == 0) mbar_wait(&ctl.st_full[i & 1], (uint32_t)((i >> 1) & 1), &never);
-    }
+    if (!ok) drain_copies();                         // no copy outlives the CTA
   } else if (warp == kMmaWarp && rank == 0) {
-    // ============================================================ MMA issuer
-    int64_t gc = 0, uc = 0;                          // chunks and pieces so far
-    const uint32_t sb = smem_u32(smem);
-    bool ok = true;
-    auto slot_ready = [&](int64_t it) -> bool {
-      const uint32_t ph = (uint32_t)((it / kSlots) & 1);
-      return warp_wait_sleep(&ctl.slot_full[it % kSlots], ph, abort_flag) &&
-             warp_wait_sleep(&ctl.peer_full[it % kSlots], ph, abort_flag);
-    };
-    // S (kind 0) or dP (kind 1) of the piece's chunk c
-    auto scores = [&](int kind, int c, int n) -> bool {
-      const int64_t it = kProducts * gc + bwd_pos<M>(kind, c, n);
-      const int slot = (int)(it % kSlots);
-      const int b = (int)((gc + c) % kBufs);
-      // with one S buffer: the softmax has read the last chunk's.  With two, P of
-      // chunk c-2 was read by a product issued before.
-      if (kBufs == 1 && kind == 0 && !warp_wait_sleep(&ctl.s_free, (uint32_t)(((gc + c) & 1) ^ 1), abort_flag))
-        return false;
-      if (!slot_ready(it)) return false;
-      fence_acquire_cluster();
-      tc_fence_after();
-      if (lane == 0) {
-        fence_proxy_async_smem();
-        const uint32_t b_addr = sb + slot * kSlotBytes, a_addr = sb + kOffFix + kind * kQBytes;
+    // ============================================================ MMA issuer (one thread)
+    if (lane == 0) {
+      int64_t gc = 0, uc = 0;                        // chunks and pieces so far
+      const uint32_t sb = smem_u32(smem);
+      auto wait = [&](uint64_t* bar, int64_t phase) { return mbar_wait_fast(bar, (uint32_t)(phase & 1), abort_flag); };
+      // S (kind 0) or dP (kind 1) of the piece's chunk c
+      auto scores = [&](int kind, int c, int n) -> bool {
+        const int64_t xg = gc + c;
+        const int slot = (int)(xg % R::slots(kind)), b = (int)(xg % kBufs);
+        // with one S buffer: the softmax has read the last chunk's.  With two, P of
+        // chunk c-2 was read by a product issued before.
+        if (kBufs == 1 && kind == 0 && !wait(&ctl.s_free, xg ^ 1)) return false;
+        if (!wait(&ctl.full[kind][slot], xg / R::slots(kind))) return false;
+        tc_fence_after();
+        const uint32_t b_addr = sb + R::offset(kind) + slot * kSlotBytes, a_addr = sb + kOffFix + kind * kQBytes;
         const uint32_t d = tmem + (kind == 1 ? kTmemP : (uint32_t)b * 128);
 #pragma unroll
         for (int kk = 0; kk < 16; ++kk) {            // k-steps of 16 dims
@@ -272,71 +261,49 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
           const uint64_t db = desc_sw128(b_addr + slab * 8192 + sub * 32, 16, 1024);
           umma_ss<2>(d, da, db, Pair::kIdescS, kk != 0);
         }
-        umma_commit_cg<2>(&ctl.slot_empty[slot]);
         umma_commit_cg<2>(kind == 0 ? &ctl.s_full[b] : &ctl.dp_full);
+        umma_commit_cg<2>(&ctl.empty[kind][slot]);
         if (c == n - 1 && kind == kProducts - 2) umma_commit_cg<2>(&ctl.fix_empty);
-      }
-      __syncwarp();
-      return true;
-    };
-    auto grad = [&](int c, int n) -> bool {
-      const int b = (int)((gc + c) % kBufs);
-      if (!warp_wait_sleep(&ctl.w_full[b], (uint32_t)(((gc + c) / kBufs) & 1), abort_flag)) return false;
-      if (c == 0 && !warp_wait_sleep(&ctl.o_free, (uint32_t)((uc & 1) ^ 1), abort_flag)) return false;
-      const int64_t it = kProducts * gc + bwd_pos<M>(2, c, n);
-      const int slot = (int)(it % kSlots);
-      if (!slot_ready(it)) return false;
-      fence_acquire_cluster();
-      tc_fence_after();
-      if (lane == 0) {
-        fence_proxy_async_smem();
-        const uint32_t b_addr = sb + slot * kSlotBytes;
+        return true;
+      };
+      auto grad = [&](int c, int n) -> bool {
+        const int64_t xg = gc + c;
+        const int b = (int)(xg % kBufs), slot = (int)(xg % R::kN2);
+        if (!wait(&ctl.w_full[b], xg / kBufs)) return false;      // P or dS, and both halves of the operand
+        if (c == 0 && !wait(&ctl.o_free, uc ^ 1)) return false;
+        tc_fence_after();
+        const uint32_t b_addr = sb + R::offset(2) + slot * kSlotBytes;
         const uint32_t w = tmem + (M == kDv ? (uint32_t)b * 128 : kTmemP);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {             // k-steps of 16 chunk columns; each half's start at its columns
           const uint64_t db = desc_sw128(b_addr + kk * 2048, 16384, 1024);
           umma_ts<2>(tmem + kTmemD, w + (kk >> 2) * 64 + (kk & 3) * 8, db, Pair::kIdescPV, (c | kk) != 0);
         }
-        umma_commit_cg<2>(&ctl.slot_empty[slot]);
+        umma_commit_cg<2>(&ctl.empty[2][slot]);
         if (c == n - 1) umma_commit_cg<2>(&ctl.o_full);
+        return true;
+      };
+      bool ok = true;
+      while (ok && next()) {
+        if (!(ok = wait(&ctl.fix_full, uc))) break;
+        fence_acquire_cluster();                     // the other CTA's stationary rows
+        const int n = p.c1 - p.c0;
+        ok = scores(0, 0, n);
+        if (kProducts == 3) ok = ok && scores(1, 0, n);
+        for (int c = 0; c < n && ok; ++c) {
+          if (c + 1 < n) ok = scores(0, c + 1, n);
+          ok = ok && grad(c, n);
+          if (kProducts == 3 && c + 1 < n) ok = ok && scores(1, c + 1, n);
+        }
+        gc += n;
+        ++uc;
       }
-      __syncwarp();
-      return true;
-    };
-    while (ok && next()) {
-      if (warp_aborted(abort_flag)) break;
-      if (!(ok = warp_wait_sleep(&ctl.fix_full, (uint32_t)(uc & 1), abort_flag))) break;
-      const int n = p.c1 - p.c0;
-      ok = scores(0, 0, n);
-      if (kProducts == 3) ok = ok && scores(1, 0, n);
-      for (int c = 0; c < n && ok; ++c) {
-        if (c + 1 < n) ok = scores(0, c + 1, n);
-        ok = ok && grad(c, n);
-        if (kProducts == 3 && c + 1 < n) ok = ok && scores(1, c + 1, n);
-      }
-      gc += n;
-      ++uc;
-    }
-    // every MMA issued above has finished before TMEM is freed
-    if (lane == 0) {
+      // every MMA issued above has finished before TMEM is freed
       umma_commit_pair_local(&ctl.mma_done);
       volatile int never = 0;
       mbar_wait(&ctl.mma_done, 0, &never);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ============================================================ rank 1: slot full, forwarded to rank 0
-    int64_t item = 0;
-    bool ok = true;
-    while (ok && next()) {
-      if (warp_aborted(abort_flag)) break;
-      for (int j = 0; j < kProducts * (p.c1 - p.c0); ++j, ++item) {
-        const int slot = (int)(item % kSlots);
-        if (!(ok = warp_wait_sleep(&ctl.slot_full[slot], (uint32_t)((item / kSlots) & 1), abort_flag))) break;
-        if (lane == 0) mbar_arrive_cluster(&ctl.peer_full[slot], 0);
-        __syncwarp();
-      }
-    }
   } else if (warp >= kQWarp) {
     // ============================================================ stationary tiles of the next unit
     const int qw = warp - kQWarp;
@@ -395,13 +362,9 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       // first position of this CTA's stationary rows (dQ: below it no key is masked), last one (dK, dV)
       const int32_t edge = kByKeys ? (int32_t)(x.row0 + rank * 128 + 127)
                                    : (int32_t)((x.row0 + rank * 128) / t.hpg);
-      // Rows behind the segment's end become zero in the operand of chunk c's
-      // product.  Called once the chunk's last score product is seen done: the
-      // slot's occupant before was consumed by a product issued earlier.
-      auto clear_tail = [&](int c, int32_t j0) {
-        const int64_t it = kProducts * (gc - c) + bwd_pos<M>(2, c, n);
-        mbar_wait_sleep(&ctl.slot_full[it % kSlots], (uint32_t)((it / kSlots) & 1), abort_flag);
-        unsigned char* ds = smem + (it % kSlots) * kSlotBytes;
+      // Rows behind the segment's end become zero in the operand of the chunk's product.
+      auto clear_tail = [&](int32_t j0) {
+        unsigned char* ds = smem + R::offset(2) + (gc % R::kN2) * kSlotBytes;
         for (int i = threadIdx.x + (seg_n - j0) * 16; i < kKeys * 16; i += kSoftmaxWarps * 32)
           *reinterpret_cast<uint4*>(ds + ((i >> 3) & 1) * 16384 + (i >> 4) * 128 + ((i & 7) << 4)) =
               make_uint4(0, 0, 0, 0);
@@ -413,8 +376,8 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         const int32_t j0 = kByKeys ? (int32_t)x.row0 + (cc / t.hpg) * kKeys : cc * kKeys;   // first position of the columns
         const float* st_l = stats + (gc & 1) * 256 + half * 64;
         const float* st_d = st_l + 128;
-        if (kByKeys) mbar_wait_sleep(&ctl.st_full[gc & 1], (uint32_t)((gc >> 1) & 1), abort_flag);
-        mbar_wait_sleep(&ctl.s_full[b], (uint32_t)((gc / kBufs) & 1), abort_flag);
+        if (kByKeys) mbar_wait_fast(&ctl.st_full[gc & 1], (uint32_t)((gc >> 1) & 1), abort_flag);
+        mbar_wait_fast(&ctl.s_full[b], (uint32_t)((gc / kBufs) & 1), abort_flag);
         tc_fence_after();
         float w[64];
 #pragma unroll
@@ -428,7 +391,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         if (kBufs == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(&ctl.s_free, 0);
+          if (lane == 0) mbar_arrive_leader<2>(&ctl.s_free);
         }
         // columns lo .. hi-1 of this thread's 64 count
         int lo = 0, hi = 64;
@@ -452,16 +415,14 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         }
         uint32_t dst = lane_addr + b * 128 + half * 64;
         if (M == kDv) {
-          if (j0 + kKeys > seg_n) clear_tail(c, j0);
           if (cut) {
 #pragma unroll
             for (int i = 0; i < 64; ++i) w[i] = (i >= lo && i < hi) ? w[i] : 0.f;
           }
         } else {
           dst = lane_addr + kTmemP + half * 64;
-          mbar_wait_sleep(&ctl.dp_full, (uint32_t)(gc & 1), abort_flag);
+          mbar_wait_fast(&ctl.dp_full, (uint32_t)(gc & 1), abort_flag);
           tc_fence_after();
-          if (j0 + kKeys > seg_n) clear_tail(c, j0);
 #pragma unroll
           for (int k = 0; k < 64; k += 32) {
             float v[2][16];
@@ -491,14 +452,17 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
           tmem_st16u(dst + k / 2, pk);
         }
         tmem_wait_st();
+        const bool clear = j0 + kKeys > seg_n;
+        mbar_wait_fast(&ctl.d_full[gc % R::kN2], (uint32_t)((gc / R::kN2) & 1), abort_flag);
+        if (clear) clear_tail(j0);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_cluster(&ctl.w_full[b], 0);
+          if (clear) mbar_arrive_cluster(&ctl.w_full[b], 0); else mbar_arrive_leader<2>(&ctl.w_full[b]);
           if (kByKeys) mbar_arrive(&ctl.st_free[gc & 1]);
         }
       }
-      mbar_wait_sleep(&ctl.o_full, (uint32_t)(uc & 1), abort_flag);
+      mbar_wait_fast(&ctl.o_full, (uint32_t)(uc & 1), abort_flag);
       tc_fence_after();
       const bool whole = p.part < 0;
       const float f = whole && M != kDv ? a.scale : 1.f;
@@ -528,7 +492,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       __syncwarp();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(&ctl.o_free, 0);
+      if (lane == 0) mbar_arrive_leader<2>(&ctl.o_free);
       ++uc;
     }
   }

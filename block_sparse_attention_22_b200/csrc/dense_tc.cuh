@@ -23,10 +23,12 @@
 //
 // Per CTA 12 warps: eight softmax warps (two per TMEM lane quadrant, each
 // thread one row and half of a chunk's keys and dims), one TMA producer that
-// fills a ring of five 32 KiB slots in the order the MMAs consume them (K0,
-// K1, V0, K2, V1, ...), one MMA warp (of rank 0; rank 1's forwards "slot
-// full"), two warps that load Q for the next unit.  TMEM: two S buffers (P
-// overwrites the first half of its S), O in columns 256..511.
+// fills three 32 KiB slots of K and two of V in the order the MMAs consume them
+// (K0, K1, V0, K2, V1, ...), one thread that issues the MMAs (in rank 0), two
+// warps that load Q for the next unit.  K completes on rank 0's barrier, V on
+// each CTA's own, where the softmax warps wait for it before they hand over P,
+// so the MMA thread waits once per product and needs no fence.  TMEM: two S
+// buffers (each half's P overwrites its own S columns), O in columns 256..511.
 //
 // Keys that do not count -- beyond the sequence, on a page out of range, after
 // a row's position -- may hold anything: their scores are replaced by -inf;
@@ -51,13 +53,14 @@ constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 2;
-constexpr int kSlots = 5;
+constexpr int kSlots = 5, kKSlots = 3, kVSlots = 2;
 constexpr int kSlotBytes = 32768;
 constexpr int kQBytes = 65536;                        // 128 rows x 256 dims, 4 slabs of 16 KiB
+constexpr int kOffV = kKSlots * kSlotBytes;
 constexpr int kOffQ = kSlots * kSlotBytes;            // 163840
 constexpr int kOffCtl = kOffQ + kQBytes;              // 229376
-constexpr int kCtlBytes = 2048;
-constexpr int kSmemBytes = kOffCtl + kCtlBytes + 1024;    // + alignment slack: 232448
+constexpr int kCtlBytes = 3072;
+constexpr int kSmemBytes = kOffCtl + kCtlBytes;       // 232448: the base itself is 1024-byte aligned
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
 constexpr int kNfBufs = 4;                            // units whose non-finite lists may be in use at once
 template <int CG> struct Shape {
@@ -81,15 +84,15 @@ struct DenseTcArgs {
 };
 
 struct DenseTcCtl {
-  uint64_t slot_full[dense_tc::kSlots];
-  uint64_t peer_full[dense_tc::kSlots];   // rank 0: rank 1's slot is full
-  uint64_t slot_empty[dense_tc::kSlots];
+  uint64_t k_full[dense_tc::kKSlots];     // rank 0's: both CTAs' halves
+  uint64_t v_full[dense_tc::kVSlots];     // this CTA's half
+  uint64_t k_empty[dense_tc::kKSlots], v_empty[dense_tc::kVSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], p_free[2];
   uint64_t o_full, o_free;
   uint64_t nf_full[dense_tc::kNfBufs];
   uint64_t mma_done;
-  float red[2][128];                      // row maxima / sums of the two warps of a row
+  float red[2][2][128];                   // by chunk parity: row maxima / sums of the two warps of a row
   uint32_t nf[dense_tc::kNfBufs][dense_tc::kQWarps][8];   // keys first_pos+1+i whose V is not finite
   uint32_t tmem_base;
   int abort;
@@ -104,9 +107,18 @@ inline int dense_box(int page_tokens) {
   return b;
 }
 
+// Arrives on rank 0's barrier after shared-memory writes that its MMAs read.
 template <int CG>
-__device__ __forceinline__ void dense_arrive(uint64_t* bar) {   // on rank 0's barrier
+__device__ __forceinline__ void dense_arrive(uint64_t* bar) {
   if constexpr (CG == 1) sm100::mbar_arrive(bar); else sm100::mbar_arrive_cluster(bar, 0);
+}
+
+// After an abort: copies in flight land within microseconds; the CTA stays for
+// about a millisecond.
+__device__ __forceinline__ void drain_copies() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < 2000000) {
+  }
 }
 
 template <int CG, bool PAGED>
@@ -115,9 +127,9 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
                         const __grid_constant__ DenseTable t, const __grid_constant__ DenseTcArgs a) {
   using namespace dense_tc;
   using namespace sm100;
-  constexpr int KC = Shape<CG>::kKeys, NK = KC / 2;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  constexpr int KC = Shape<CG>::kKeys, NK = KC / 2;          // keys of a chunk, of a softmax thread
+  extern __shared__ __align__(1024) unsigned char smem_1k[];
+  unsigned char* const smem = smem_1k;
   DenseTcCtl& ctl = *reinterpret_cast<DenseTcCtl*>(smem + kOffCtl);
   volatile int* abort_flag = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -125,11 +137,18 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
   const int cta = blockIdx.x / CG;
 
   // ---------------------------------------------------------------- set-up
+  if (smem_u32(smem) & 1023u) {                      // the swizzled tiles need it; the same in every CTA
+    report_error(kErrWaitTimeout);
+    return;
+  }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&ctl.slot_full[i], 1);
-      mbar_init(&ctl.peer_full[i], 1);
-      mbar_init(&ctl.slot_empty[i], 1);
+    for (int i = 0; i < kKSlots; ++i) {
+      mbar_init(&ctl.k_full[i], CG);
+      mbar_init(&ctl.k_empty[i], 1);
+    }
+    for (int i = 0; i < kVSlots; ++i) {
+      mbar_init(&ctl.v_full[i], 1);
+      mbar_init(&ctl.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.s_full[i], 1);
@@ -161,7 +180,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
     // ============================================================ TMA producer
     // Lane b < 256 / box issues box b of a slot: `box` keys x 64 dims.
     const int nbox = 256 / a.box;
-    int64_t item = 0;
+    int64_t gc = 0;                                          // chunks of the pieces before
     bool ok = true;
     while (ok && walk.next(t, p, x)) {
       if (warp_aborted(abort_flag)) {
@@ -170,27 +189,26 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       }
       const int n = p.c1 - p.c0;
       // box `lane` of ring position j: its coordinates; y < 0: not loaded
-      auto place = [&](int j, int& kind, int& off, int& cx, int& key) {
+      auto place = [&](int j, int& kind, int& c, int& off, int& cx, int& key) {
         kind = (j == 0) ? 0 : (j == 2 * n - 1) ? 1 : (j & 1) ? 0 : 1;
-        const int c = p.c0 + ((j == 0) ? 0 : (j == 2 * n - 1) ? n - 1 : (j & 1) ? (j + 1) / 2 : j / 2 - 1);
+        c = (j == 0) ? 0 : (j == 2 * n - 1) ? n - 1 : (j & 1) ? (j + 1) / 2 : j / 2 - 1;
         const int slabs = (CG == 2 && kind == 1) ? 2 : 4;
         const int slab = lane % slabs, run = lane / slabs;
         const int lines = 256 / slabs;                       // lines of a slab: 64 or 128
         off = slab * lines * 128 + run * a.box * 128;
         cx = slab * 64 + ((CG == 2 && kind == 1) ? (int)rank * 128 : 0);
-        key = c * KC + run * a.box + ((CG == 2 && kind == 0) ? (int)rank * 64 : 0);
+        key = (p.c0 + c) * KC + run * a.box + ((CG == 2 && kind == 0) ? (int)rank * 64 : 0);
       };
       auto page_of = [&](int j) -> int32_t {                 // page of this lane's box (paged only)
-        int kind, off, cx, key;
-        place(j, kind, off, cx, key);
+        int kind, c, off, cx, key;
+        place(j, kind, c, off, cx, key);
         if (lane >= nbox || key >= x.kv_len) return -1;
         return a.kv.table[(int64_t)t.slot[x.si] * a.kv.max_pages + key / a.kv.page_tokens];
       };
       int32_t page = PAGED ? page_of(0) : 0;
-      for (int j = 0; j < 2 * n; ++j, ++item) {
-        const int slot = (int)(item % kSlots);
-        int kind, off, cx, key;
-        place(j, kind, off, cx, key);
+      for (int j = 0; j < 2 * n; ++j) {
+        int kind, c, off, cx, key;
+        place(j, kind, c, off, cx, key);
         int32_t y = -1;
         if (lane < nbox && key < x.kv_len) {
           if (PAGED) {
@@ -204,68 +222,61 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
           }
         }
         if (PAGED && j + 1 < 2 * n) page = page_of(j + 1);
-        if (!(ok = warp_wait_sleep(&ctl.slot_empty[slot], (uint32_t)(((item / kSlots) & 1) ^ 1), abort_flag))) break;
+        const int64_t xg = gc + c;
         const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
-        if (lane == 0) mbar_expect_tx(&ctl.slot_full[slot], (uint32_t)__popc(live) * (uint32_t)(a.box * 128));
-        __syncwarp();
-        if (y >= 0) tma_load_2d(smem + slot * kSlotBytes + off, kind == 0 ? &tm_k : &tm_v, cx, y, &ctl.slot_full[slot]);
-      }
-    }
-    if (!ok) {                                               // no copy outlives the CTA
-      volatile int never = 0;
-      for (int64_t i = item > kSlots ? item - kSlots : 0; i < item; ++i)
-        if (lane == 0) mbar_wait(&ctl.slot_full[i % kSlots], (uint32_t)((i / kSlots) & 1), &never);
-    }
-  } else if (warp == kMmaWarp && rank == 0) {
-    // ============================================================ MMA issuer
-    int64_t gc = 0, uc = 0;                                  // chunks and pieces so far
-    const uint32_t sb = smem_u32(smem);
-    bool ok = true;
-    auto slot_ready = [&](int64_t it) -> bool {
-      const uint32_t ph = (uint32_t)((it / kSlots) & 1);
-      if (!warp_wait_sleep(&ctl.slot_full[it % kSlots], ph, abort_flag)) return false;
-      if (CG == 2 && !warp_wait_sleep(&ctl.peer_full[it % kSlots], ph, abort_flag)) return false;
-      return true;
-    };
-    auto pv = [&](int64_t base, int cx, int n) -> bool {     // base: chunks before the piece
-      const int64_t xg = base + cx;
-      const int pb = (int)(xg & 1);
-      if (!warp_wait_sleep(&ctl.p_full[pb], (uint32_t)((xg >> 1) & 1), abort_flag)) return false;
-      if (cx == 0 && !warp_wait_sleep(&ctl.o_free, (uint32_t)((uc & 1) ^ 1), abort_flag)) return false;
-      const int64_t it = 2 * base + union_item(cx, 1, n);
-      const int slot = (int)(it % kSlots);
-      if (!slot_ready(it)) return false;
-      if (CG == 2) fence_acquire_cluster();
-      tc_fence_after();
-      if (lane == 0) {
-        fence_proxy_async_smem();
-        const uint32_t v_addr = sb + slot * kSlotBytes;
-#pragma unroll
-        for (int kk = 0; kk < KC / 16; ++kk) {               // k-steps of 16 keys; P: 8 columns of bf16 pairs each
-          const uint64_t db = desc_sw128(v_addr + kk * 2048, KC * 128, 1024);
-          umma_ts<CG>(tmem + kTmemO, tmem + pb * KC + kk * 8, db, Shape<CG>::kIdescPV, (cx | kk) != 0);
+        const uint32_t bytes = (uint32_t)__popc(live) * (uint32_t)(a.box * 128);
+        if (kind == 0) {
+          const int slot = (int)(xg % kKSlots);
+          if (!(ok = warp_wait_sleep(&ctl.k_empty[slot], (uint32_t)(((xg / kKSlots) & 1) ^ 1), abort_flag))) break;
+          if (lane == 0) mbar_expect_tx_leader<CG>(&ctl.k_full[slot], bytes);
+          __syncwarp();
+          if (y >= 0) tma_load_2d_leader<CG>(smem + slot * kSlotBytes + off, &tm_k, cx, y, &ctl.k_full[slot]);
+        } else {
+          const int slot = (int)(xg % kVSlots);
+          if (!(ok = warp_wait_sleep(&ctl.v_empty[slot], (uint32_t)(((xg / kVSlots) & 1) ^ 1), abort_flag))) break;
+          if (lane == 0) mbar_expect_tx(&ctl.v_full[slot], bytes);
+          __syncwarp();
+          if (y >= 0) tma_load_2d(smem + kOffV + slot * kSlotBytes + off, &tm_v, cx, y, &ctl.v_full[slot]);
         }
-        umma_commit_cg<CG>(&ctl.slot_empty[slot]);
+      }
+      gc += n;
+    }
+    if (!ok) drain_copies();                                 // no copy outlives the CTA
+  } else if (warp == kMmaWarp && rank == 0) {
+    // ============================================================ MMA issuer (one thread)
+    if (lane == 0) {
+      int64_t gc = 0, uc = 0;                                // chunks and pieces so far
+      const uint32_t sb = smem_u32(smem);
+      auto wait = [&](uint64_t* bar, int64_t phase) { return mbar_wait_fast(bar, (uint32_t)(phase & 1), abort_flag); };
+      auto pv = [&](int cx, int n) -> bool {
+        const int64_t xg = gc + cx;
+        const int pb = (int)(xg & 1), slot = (int)(xg % kVSlots);
+        if (!wait(&ctl.p_full[pb], xg >> 1)) return false;   // P, and both halves of V
+        if (cx == 0 && !wait(&ctl.o_free, uc ^ 1)) return false;
+        tc_fence_after();
+        const uint32_t v_addr = sb + kOffV + slot * kSlotBytes;
+#pragma unroll
+        for (int kk = 0; kk < KC / 16; ++kk) {               // k-steps of 16 keys; each half's P in its S columns
+          const uint64_t db = desc_sw128(v_addr + kk * 2048, KC * 128, 1024);
+          umma_ts<CG>(tmem + kTmemO, tmem + pb * KC + (kk / (KC / 32)) * NK + (kk % (KC / 32)) * 8, db,
+                      Shape<CG>::kIdescPV, (cx | kk) != 0);
+        }
+        umma_commit_cg<CG>(&ctl.v_empty[slot]);
         umma_commit_cg<CG>(&ctl.p_free[pb]);
         if (cx == n - 1) umma_commit_cg<CG>(&ctl.o_full);
-      }
-      __syncwarp();
-      return true;
-    };
-    while (ok && walk.next(t, p, x)) {
-      if (warp_aborted(abort_flag)) break;
-      if (!(ok = warp_wait_sleep(&ctl.q_full, (uint32_t)(uc & 1), abort_flag))) break;
-      const int n = p.c1 - p.c0;
-      for (int c = 0; c < n && ok; ++c) {
-        const int b = (int)((gc + c) & 1);
-        const int64_t it = 2 * gc + union_item(c, 0, n);
-        const int slot = (int)(it % kSlots);
-        if (!(ok = slot_ready(it))) break;
-        // S buffer b: P of chunk c-2 (of this or the last piece) was read by a product issued before
-        if (CG == 2) fence_acquire_cluster();
-        tc_fence_after();
-        if (lane == 0) {
-          fence_proxy_async_smem();
+        return true;
+      };
+      bool ok = true;
+      while (ok && walk.next(t, p, x)) {
+        if (!(ok = wait(&ctl.q_full, uc))) break;
+        if (CG == 2) fence_acquire_cluster();                // Q of the other CTA
+        const int n = p.c1 - p.c0;
+        for (int c = 0; c < n && ok; ++c) {
+          const int64_t xg = gc + c;
+          const int b = (int)(xg & 1), slot = (int)(xg % kKSlots);
+          // S buffer b: P of chunk c-2 (of this or the last piece) was read by a product issued before
+          if (!(ok = wait(&ctl.k_full[slot], xg / kKSlots))) break;
+          tc_fence_after();
           const uint32_t k_addr = sb + slot * kSlotBytes, q_addr = sb + kOffQ;
 #pragma unroll
           for (int kk = 0; kk < 16; ++kk) {                  // k-steps of 16 dims
@@ -274,38 +285,22 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
             const uint64_t db = desc_sw128(k_addr + slab * 8192 + sub * 32, 16, 1024);
             umma_ss<CG>(tmem + b * KC, da, db, Shape<CG>::kIdescS, kk != 0);
           }
-          umma_commit_cg<CG>(&ctl.slot_empty[slot]);
           umma_commit_cg<CG>(&ctl.s_full[b]);
+          umma_commit_cg<CG>(&ctl.k_empty[slot]);
           if (c == n - 1) umma_commit_cg<CG>(&ctl.q_empty);
+          if (c > 0) ok = pv(c - 1, n);
         }
-        __syncwarp();
-        if (c > 0) ok = pv(gc, c - 1, n);
+        if (!ok) break;
+        ok = pv(n - 1, n);
+        gc += n;
+        ++uc;
       }
-      if (!ok) break;
-      ok = pv(gc, n - 1, n);
-      gc += n;
-      ++uc;
-    }
-    // every MMA issued above has finished before TMEM is freed
-    if (lane == 0) {
+      // every MMA issued above has finished before TMEM is freed
       if constexpr (CG == 1) umma_commit(&ctl.mma_done); else umma_commit_pair_local(&ctl.mma_done);
       volatile int never = 0;
       mbar_wait(&ctl.mma_done, 0, &never);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ============================================================ rank 1: slot full, forwarded to rank 0
-    int64_t item = 0;
-    bool ok = true;
-    while (ok && walk.next(t, p, x)) {
-      if (warp_aborted(abort_flag)) break;
-      for (int j = 0; j < 2 * (p.c1 - p.c0); ++j, ++item) {
-        const int slot = (int)(item % kSlots);
-        if (!(ok = warp_wait_sleep(&ctl.slot_full[slot], (uint32_t)((item / kSlots) & 1), abort_flag))) break;
-        if (lane == 0) mbar_arrive_cluster(&ctl.peer_full[slot], 0);
-        __syncwarp();
-      }
-    }
   } else if (warp >= kQWarp) {
     // ============================================================ Q of the next unit; V of its own tokens checked
     const int qw = warp - kQWarp;
@@ -390,13 +385,13 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
         const int b = (int)(gc & 1);
         const int32_t j0 = (p.c0 + c) * KC;
         const uint32_t bad = bad_runs(p.c0 + c);
-        mbar_wait_sleep(&ctl.s_full[b], (uint32_t)((gc >> 1) & 1), abort_flag);
+        mbar_wait_fast(&ctl.s_full[b], (uint32_t)((gc >> 1) & 1), abort_flag);
         tc_fence_after();
-        if (j0 + KC > kv_len || bad || (any_nf && j0 + KC - 1 > first)) {
+        const bool clear = j0 + KC > kv_len || bad || (any_nf && j0 + KC - 1 > first);
+        if (clear) {
           // V rows that must not reach the product become zero in shared memory
-          const int64_t it = 2 * (gc - c) + union_item(c, 1, n);
-          mbar_wait_sleep(&ctl.slot_full[it % kSlots], (uint32_t)((it / kSlots) & 1), abort_flag);
-          unsigned char* vs = smem + (it % kSlots) * kSlotBytes;
+          mbar_wait_fast(&ctl.v_full[gc % kVSlots], (uint32_t)((gc / kVSlots) & 1), abort_flag);
+          unsigned char* vs = smem + kOffV + (gc % kVSlots) * kSlotBytes;
           constexpr int kPieces = 2048 / KC;                 // 16-byte pieces of a key's row here: 32 or 16
           for (int i = threadIdx.x; i < KC * kPieces; i += kSoftmaxWarps * 32) {
             const int key = i / kPieces, piece = i % kPieces;     // a warp covers one or two keys
@@ -426,13 +421,15 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
             for (int i = 0; i < NK; ++i)
               if (i > lim || ((bad >> ((half * NK + i) >> 4)) & 1u)) s[i] = -INFINITY;
           }
-          float pm = -INFINITY;
+          float pm4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 0; i < NK; ++i) pm = fmaxf(pm, s[i]);
-          ctl.red[half][li] = pm * tau2;
+          for (int i = 4; i < NK; i += 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pm4[k] = fmaxf(pm4[k], s[i + k]);
+          }
+          ctl.red[b][half][li] = fmaxf(fmaxf(pm4[0], pm4[1]), fmaxf(pm4[2], pm4[3])) * tau2;
           named_bar_sync(1 + quad, 64);
-          const float mc = fmaxf(ctl.red[0][li], ctl.red[1][li]);
-          named_bar_sync(1 + quad, 64);
+          const float mc = fmaxf(ctl.red[b][0][li], ctl.red[b][1][li]);
           float f = 1.f;
           bool need = false;
           if (mc > m + 8.f) {                                // false while both are -inf
@@ -446,7 +443,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
           if (__any_sync(0xffffffffu, need)) {
             // O holds chunks 0..c-1 (c >= 1 here): wait for the last of their products
             const int64_t xp = gc - 1;
-            mbar_wait_sleep(&ctl.p_free[xp & 1], (uint32_t)((xp >> 1) & 1), abort_flag);
+            mbar_wait_fast(&ctl.p_free[xp & 1], (uint32_t)((xp >> 1) & 1), abort_flag);
             tc_fence_after();
 #pragma unroll 1
             for (int piece = 0; piece < 8; ++piece) {
@@ -461,6 +458,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
             tmem_wait_st();
           }
           const float mb = m == -INFINITY ? 0.f : m;
+          float l4[4] = {l, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < NK; k += 32) {
             uint32_t pk[16];
@@ -468,27 +466,29 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
             for (int i = 0; i < 16; ++i) {
               const float p0 = ex2_approx(fmaf(s[k + 2 * i], tau2, -mb));
               const float p1 = ex2_approx(fmaf(s[k + 2 * i + 1], tau2, -mb));
-              l += p0 + p1;
+              l4[i & 3] += p0 + p1;
               pk[i] = pack_bf16x2(p0, p1);
             }
-            // P over the first half of the chunk's S columns: both warps of
-            // the row have read S (the exchange above)
-            tmem_st16u(lane_addr + b * KC + half * (NK / 2) + k / 2, pk);
+            tmem_st16u(lane_addr + b * KC + half * NK + k / 2, pk);   // over this thread's own scores
           }
+          l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
           tmem_wait_st();
         }
+        mbar_wait_fast(&ctl.v_full[gc % kVSlots], (uint32_t)((gc / kVSlots) & 1), abort_flag);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) dense_arrive<CG>(&ctl.p_full[b]);
+        if (lane == 0) {
+          if (clear) dense_arrive<CG>(&ctl.p_full[b]); else mbar_arrive_leader<CG>(&ctl.p_full[b]);
+        }
       }
       float lt = 0.f;
       if (warp_active) {                                     // the row's sum: both warps' parts
-        ctl.red[half][li] = l;
+        ctl.red[gc & 1][half][li] = l;                       // the last chunk's buffer is the other one
         named_bar_sync(1 + quad, 64);
-        lt = ctl.red[0][li] + ctl.red[1][li];
-        named_bar_sync(1 + quad, 64);
+        lt = ctl.red[gc & 1][0][li] + ctl.red[gc & 1][1][li];
+        named_bar_sync(1 + quad, 64);                        // the next piece's first chunk writes this buffer
       }
-      mbar_wait_sleep(&ctl.o_full, (uint32_t)(uc & 1), abort_flag);
+      mbar_wait_fast(&ctl.o_full, (uint32_t)(uc & 1), abort_flag);
       tc_fence_after();
       if (warp_active) {
         const bool whole = p.part < 0;
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) dense_arrive<CG>(&ctl.o_free);
+      if (lane == 0) mbar_arrive_leader<CG>(&ctl.o_free);
       ++uc;
     }
   }

@@ -107,6 +107,12 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, 
   }
 }
 
+// mbar_wait_sleep that takes a completed phase without reading the clock.
+__device__ __forceinline__ bool mbar_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_sleep(bar, parity, abort_flag);
+}
+
 // ------------------------------------------------------------------ TMA
 // 2-D tiled load of one box into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
@@ -262,6 +268,46 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank
       "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
       "r"(rank)
       : "memory");
+}
+// Shared-memory address of `bar` in rank 0 of the pair (CG = 1: this CTA), for
+// the operations below that take barriers by address.
+template <int CG>
+__device__ __forceinline__ uint32_t leader_bar(uint64_t* bar) {
+  uint32_t a = smem_u32(bar);
+  if constexpr (CG == 2) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(a));
+  return a;
+}
+// Arrives on rank 0's barrier, expecting `bytes` more.
+template <int CG>
+__device__ __forceinline__ void mbar_expect_tx_leader(uint64_t* bar, uint32_t bytes) {
+  if constexpr (CG == 1)
+    mbar_expect_tx(bar, bytes);
+  else
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(leader_bar<2>(bar)), "r"(bytes)
+                 : "memory");
+}
+// Arrives on rank 0's barrier; orders this CTA's accesses and (after
+// tcgen05.fence::before_thread_sync) tensor memory, not shared memory that the
+// other CTA reads itself: those writers use mbar_arrive_cluster.
+template <int CG>
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
+  if constexpr (CG == 1)
+    mbar_arrive(bar);
+  else
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_bar<2>(bar)) : "memory");
+}
+// 2-D tiled load into this CTA that completes on rank 0's barrier.
+template <int CG>
+__device__ __forceinline__ void tma_load_2d_leader(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                                   uint64_t* bar) {
+  if constexpr (CG == 1)
+    tma_load_2d(dst, map, x, y, bar);
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_bar<2>(bar)), "r"(x), "r"(y)
+        : "memory");
 }
 // Orders what this thread does next after what another CTA released before its
 // arrival on a barrier this thread has seen complete.
