@@ -53,12 +53,14 @@ struct DenseSplits {
   int16_t first[dense::kMaxGrid], last[dense::kMaxGrid];
 };
 
+// Rows and positions of a segment fit 32 bits (checked on the host): 64-bit
+// divisions by the group size cost more than a chunk's products.
 struct DenseUnit {
   int si;                // segment
   int grp;
-  int64_t row0;          // first row of the tile in the segment's rows (by_keys: first key)
+  int32_t row0;          // first row of the tile in the segment's rows (by_keys: first key)
   int nrows;             // valid rows (>= 1)
-  int64_t kv_len;        // keys 0 .. kv_len-1 are those of the tile's last token (by_keys: the segment's tokens)
+  int32_t kv_len;        // keys 0 .. kv_len-1 are those of the tile's last token (by_keys: the segment's tokens)
   int nchunks;
 };
 
@@ -73,21 +75,25 @@ __host__ __device__ __forceinline__ DenseUnit dense_unit(const DenseTable& t, in
   }
   x.si = lo;
   if (t.by_keys) {
-    x.row0 = (int64_t)(tile - t.item0[lo]) * t.rows;
+    x.row0 = (tile - t.item0[lo]) * t.rows;
     x.kv_len = t.q_len[lo];
-    const int64_t left = x.kv_len - x.row0;
-    x.nrows = (int)(left < t.rows ? left : t.rows);
-    x.nchunks = (int)((left + t.kc - 1) / t.kc) * t.hpg;
+    const int32_t left = x.kv_len - x.row0;
+    x.nrows = left < t.rows ? left : t.rows;
+    x.nchunks = (left + t.kc - 1) / t.kc * t.hpg;
     return x;
   }
-  const int64_t total = (int64_t)t.q_len[lo] * t.hpg;
-  x.row0 = (int64_t)(t.item0[lo + 1] - 1 - tile) * t.rows;     // tiles from the segment's end
-  const int64_t left = total - x.row0;
-  x.nrows = (int)(left < t.rows ? left : t.rows);
-  const int64_t last_tok = (x.row0 + x.nrows - 1) / t.hpg;
-  x.kv_len = (int64_t)t.pos0[lo] + last_tok + 1;
-  x.nchunks = (int)((x.kv_len + t.kc - 1) / t.kc);
+  x.row0 = (t.item0[lo + 1] - 1 - tile) * t.rows;     // tiles from the segment's end
+  const int32_t left = t.q_len[lo] * t.hpg - x.row0;
+  x.nrows = left < t.rows ? left : t.rows;
+  x.kv_len = t.pos0[lo] + (x.row0 + x.nrows - 1) / t.hpg + 1;
+  x.nchunks = (x.kv_len + t.kc - 1) / t.kc;
   return x;
+}
+
+// Row `row` of the unit's segment and group in the token-major arrays, in heads.
+__device__ __forceinline__ int64_t dense_q_row(const DenseTable& t, const DenseUnit& x, int32_t row, int H) {
+  const int32_t tok = row / t.hpg;
+  return (int64_t)(t.q_offset[x.si] + tok) * H + x.grp * t.hpg + (row - tok * t.hpg);
 }
 
 // One piece of work of a CTA: chunks c0 .. c1-1 of a unit.  part < 0: the
@@ -175,9 +181,7 @@ __global__ void __launch_bounds__(128)
     }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;     // l = 0: no key at all
-  const int64_t row = x.row0 + r;
-  const int64_t tok = t.q_offset[x.si] + row / t.hpg;
-  const int64_t at = tok * H + (int64_t)x.grp * t.hpg + row % t.hpg;
+  const int64_t at = dense_q_row(t, x, x.row0 + r, H);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     o[at * kHeadDim + lane * 2 + k * 64] = IO<T>::from_f(acc[2 * k] * inv);

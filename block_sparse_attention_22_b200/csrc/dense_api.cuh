@@ -172,6 +172,9 @@ qsa_status_t for_each_dense(const Geo& g, std::vector<qsa_segment_t> segs, const
     int64_t tiles = 0, most = 0;
     for (; i < segs.size() && t.n < kMaxSegs; ++i) {
       const qsa_segment_t& s = segs[i];
+      // a unit's rows, keys and positions are int32, with room for the last tile and chunk
+      if ((int64_t)s.q_len * g.hpg > INT32_MAX - 512 || (int64_t)s.pos0 + s.q_len > INT32_MAX - 512)
+        return QSA_ERR_UNSUPPORTED;
       const int64_t rows = (int64_t)s.q_len * (kind.by_keys ? 1 : g.hpg), it = cdiv(rows, kind.rows);
       if (t.n > 0 && (tiles + it) * g.G > INT32_MAX / 4) break;
       if ((tiles + it) * g.G > INT32_MAX / 4) return QSA_ERR_UNSUPPORTED;
@@ -241,6 +244,7 @@ cudaError_t launch_dense_simt(const Geo& g, const DenseTable& t, const KvSource&
 // Map over rows of 256 dims (paged: every cache row; packed: a token's groups
 // side by side), in boxes of `box` rows x 64 dims, 128-byte swizzled.
 bool make_dense_map(CUtensorMap* m, const void* base, int64_t rows, int groups, int box) {
+  if (rows > INT32_MAX - 512) return false;
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)kHeadDim * groups, (cuuint64_t)rows};
@@ -253,8 +257,7 @@ bool make_dense_map(CUtensorMap* m, const void* base, int64_t rows, int groups, 
 }
 
 template <int CG, bool PAGED>
-cudaError_t launch_dense_tc(const DenseTable& t, const CUtensorMap& mk, const CUtensorMap& mv, const DenseTcArgs& a,
-                            cudaStream_t st) {
+cudaError_t launch_dense_tc(const DenseTable& t, const CUtensorMap (&m)[4], const DenseTcArgs& a, cudaStream_t st) {
   auto kernel = dense_fwd_tc_kernel<CG, PAGED>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense_tc::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -272,7 +275,7 @@ cudaError_t launch_dense_tc(const DenseTable& t, const CUtensorMap& mk, const CU
   cfg.attrs = attr;
   cfg.numAttrs = CG == 1 ? 1 : 2;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, kernel, mk, mv, t, a);
+  return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], t, a);
 }
 
 template <typename T>
@@ -286,8 +289,8 @@ cudaError_t launch_dense_combine(const Geo& g, const DenseTable& t, const DenseS
 // kv_rows, kv_groups: the shape of the tensor map over K and V (make_dense_map).
 template <bool PAGED>
 qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int n, const KvSource& kv,
-                           int64_t kv_rows, int kv_groups, const void* q, void* o, float* lse, void* ws,
-                           size_t ws_bytes, cudaStream_t st) {
+                           int64_t kv_rows, int kv_groups, int32_t n_tokens, const void* q, void* o, float* lse,
+                           void* ws, size_t ws_bytes, cudaStream_t st) {
   const size_t need = dense_fwd_ws(g, tc, segs, n);
   if (need == SIZE_MAX) return QSA_ERR_UNSUPPORTED;
   if (need > 0 && (!ws || ws_bytes < need)) return QSA_ERR_WORKSPACE;
@@ -296,19 +299,21 @@ qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int
   DenseKind kn, kw;
   dense_kinds(g, tc, segs, n, narrow, wide, kn, kw);
   float* part = (float*)ws;
-  CUtensorMap mk, mv;
+  CUtensorMap m[4];                      // K, V, Q by token, Q by row
   DenseTcArgs a;
   if (tc) {
+    if ((int64_t)n_tokens * g.H > INT32_MAX - 512) return QSA_ERR_UNSUPPORTED;      // TMA row coordinates
     a = {kv, (const __nv_bfloat16*)q, (__nv_bfloat16*)o, lse, part, g.H, PAGED ? dense_box(kv.page_tokens) : 64,
          g.scale};
-    if (!make_dense_map(&mk, kv.k, kv_rows, kv_groups, a.box) || !make_dense_map(&mv, kv.v, kv_rows, kv_groups, a.box))
+    if (!make_dense_map(&m[0], kv.k, kv_rows, kv_groups, a.box) || !make_dense_map(&m[1], kv.v, kv_rows, kv_groups, a.box) ||
+        !make_dense_map(&m[2], q, (int64_t)n_tokens * g.H, 1, g.hpg) || !make_dense_map(&m[3], q, (int64_t)n_tokens * g.H, 1, 1))
       return QSA_ERR_CUDA;
   }
   auto run = [&](bool is_wide) {
     return [&, is_wide](const DenseTable& t, const DenseSplits& sp) -> qsa_status_t {
       cudaError_t e;
       if (tc)
-        e = is_wide ? launch_dense_tc<2, PAGED>(t, mk, mv, a, st) : launch_dense_tc<1, PAGED>(t, mk, mv, a, st);
+        e = is_wide ? launch_dense_tc<2, PAGED>(t, m, a, st) : launch_dense_tc<1, PAGED>(t, m, a, st);
       else
         e = is_wide ? launch_dense_simt<dense_simt::kRowsWide, PAGED>(g, t, kv, q, o, lse, part, st)
                     : launch_dense_simt<dense_simt::kRowsNarrow, PAGED>(g, t, kv, q, o, lse, part, st);
@@ -419,8 +424,8 @@ qsa_status_t run_dense_bwd_f32(const Geo& g, const DenseBwdPlan& p, const DenseB
 
 // One gradient on the tensor cores: its kernel, then the join of its cut units.
 template <dense_bwd::Grad M>
-qsa_status_t run_dense_grad_tc(const Geo& g, const DenseBwdPlan& p, const CUtensorMap& ms, const CUtensorMap& mp,
-                               const CUtensorMap& md, const DenseBwdTcArgs& a, cudaStream_t st) {
+qsa_status_t run_dense_grad_tc(const Geo& g, const DenseBwdPlan& p, const DenseBwdMaps& m, const DenseBwdTcArgs& a,
+                               cudaStream_t st) {
   auto kernel = dense_bwd_tc_kernel<M>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense_bwd::kSmemBytes) != cudaSuccess)
     return QSA_ERR_CUDA;
@@ -440,7 +445,7 @@ qsa_status_t run_dense_grad_tc(const Geo& g, const DenseBwdPlan& p, const CUtens
         cfg.attrs = attr;
         cfg.numAttrs = 2;
         count_launch();
-        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ms, mp, md, t, a);
+        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, m, t, a);
         if (e == cudaSuccess && sp.n > 0) {
           count_launch();
           e = launch_chained(dense_bwd_combine_kernel, dim3(sp.n, (unsigned)cdiv(t.prows, 4)), dim3(128), 0, st, t, sp,
@@ -457,9 +462,13 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
   float* lse2_h = (float*)(ws + p.off_lse2);
   float* delta_h = (float*)(ws + p.off_delta_h);
   int32_t* flags = (int32_t*)(ws + p.off_flags);
-  CUtensorMap mq, mo, mk, mv;
+  CUtensorMap mq, mo, mk, mv, tq, to, rq, ro;      // boxes of 64 rows; Q and dO by token and by row
+  const int64_t rows = (int64_t)n_tokens * g.H;
+  if (rows > INT32_MAX - 512) return QSA_ERR_UNSUPPORTED;
   if (!make_dense_map(&mq, a.q, n_tokens, g.H, 64) || !make_dense_map(&mo, a.dout, n_tokens, g.H, 64) ||
-      !make_dense_map(&mk, a.k, n_tokens, g.G, 64) || !make_dense_map(&mv, a.v, n_tokens, g.G, 64))
+      !make_dense_map(&mk, a.k, n_tokens, g.G, 64) || !make_dense_map(&mv, a.v, n_tokens, g.G, 64) ||
+      !make_dense_map(&tq, a.q, rows, 1, g.hpg) || !make_dense_map(&to, a.dout, rows, 1, g.hpg) ||
+      !make_dense_map(&rq, a.q, rows, 1, 1) || !make_dense_map(&ro, a.dout, rows, 1, 1))
     return QSA_ERR_CUDA;
   if (cudaMemsetAsync(flags, 0, p.flag_bytes, st) != cudaSuccess) return QSA_ERR_CUDA;
   qsa_status_t r = for_each_table(
@@ -472,15 +481,13 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
                               delta_h, flags, p.stat_rows, g.H, g.G);
       });
   if (r != QSA_OK) return r;
-  DenseBwdTcArgs b{(const B*)a.k, (const B*)a.v, lse2_h, delta_h, flags, (B*)a.dv, (float*)(ws + p.off_part),
+  DenseBwdTcArgs b{lse2_h, delta_h, flags, (B*)a.dv, (float*)(ws + p.off_part),
                    p.stat_rows, g.H, g.scale};
-  if ((r = run_dense_grad_tc<dense_bwd::kDv>(g, p, mq, mq, mo, b, st)) != QSA_OK) return r;
+  if ((r = run_dense_grad_tc<dense_bwd::kDv>(g, p, {mq, mq, mo, mk, mv, mk, mv}, b, st)) != QSA_OK) return r;
   b.out = (B*)a.dk;
-  if ((r = run_dense_grad_tc<dense_bwd::kDk>(g, p, mq, mo, mq, b, st)) != QSA_OK) return r;
-  b.fix0 = (const B*)a.q;
-  b.fix1 = (const B*)a.dout;
+  if ((r = run_dense_grad_tc<dense_bwd::kDk>(g, p, {mq, mo, mq, mk, mv, mk, mv}, b, st)) != QSA_OK) return r;
   b.out = (B*)a.dq;
-  if ((r = run_dense_grad_tc<dense_bwd::kDq>(g, p, mk, mv, mk, b, st)) != QSA_OK) return r;
+  if ((r = run_dense_grad_tc<dense_bwd::kDq>(g, p, {mk, mv, mk, tq, to, rq, ro}, b, st)) != QSA_OK) return r;
   a.flags = flags;
   return run_dense_bwd_simt<B>(g, p.segs, a, st);
 }
@@ -562,8 +569,8 @@ QSA_API qsa_status_t qsa_paged_attn_fwd(const qsa_config_t* cfg, const qsa_pages
     const Geo g = make_geo(cfg, nullptr);
     const KvSource kv{pages->k, pages->v, pages->table, pages->n_pages, pages->page_tokens, pages->max_pages};
     return run_dense_fwd<true>(g, cfg->dtype == QSA_DTYPE_BF16, segs, n_segs, kv,
-                               (int64_t)pages->n_pages * cfg->n_kv_groups * pages->page_tokens, 1, q, o, lse, workspace,
-                               ws_bytes, (cudaStream_t)stream);
+                               (int64_t)pages->n_pages * cfg->n_kv_groups * pages->page_tokens, 1, n_tokens, q, o, lse,
+                               workspace, ws_bytes, (cudaStream_t)stream);
   });
 }
 
@@ -580,8 +587,8 @@ QSA_API qsa_status_t qsa_prompt_attn_fwd(const qsa_config_t* cfg, const qsa_segm
       return QSA_ERR_INVALID_ARG;
     const Geo g = make_geo(cfg, nullptr);
     const KvSource kv{k, v, nullptr, 0, 0, 0};
-    return run_dense_fwd<false>(g, cfg->dtype == QSA_DTYPE_BF16, segs, n_segs, kv, n_tokens, cfg->n_kv_groups, q, o,
-                                lse, workspace, ws_bytes, (cudaStream_t)stream);
+    return run_dense_fwd<false>(g, cfg->dtype == QSA_DTYPE_BF16, segs, n_segs, kv, n_tokens, cfg->n_kv_groups, n_tokens,
+                                q, o, lse, workspace, ws_bytes, (cudaStream_t)stream);
   });
 }
 

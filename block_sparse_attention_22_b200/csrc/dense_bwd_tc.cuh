@@ -24,8 +24,8 @@
 // they were computed from, so no warp waits for another's reads.
 //
 // Roles per CTA (12 warps): eight softmax warps (two per lane quadrant, each
-// thread one lane and 64 of a chunk's columns), one TMA producer, one thread that
-// issues the MMAs (in rank 0), two loaders of the stationary tiles.  MMA order with three products:
+// thread one lane and 64 of a chunk's columns), one TMA producer, one warp that
+// issues the MMAs (in rank 0), one that loads the stationary tiles.  MMA order with three products:
 //   S0 dP0 | S1 D0 dP1 | S2 D1 dP2 | ...
 // so that the exponentials of chunk c+1 run under D(c) and dP(c+1), and dS(c+1)
 // under S(c+2); one buffer each for S and dP is enough.  With two products (dV)
@@ -46,7 +46,6 @@ using dense_tc::kSoftmaxWarps;
 using dense_tc::kProducerWarp;
 using dense_tc::kMmaWarp;
 using dense_tc::kQWarp;
-using dense_tc::kQWarps;
 using dense_tc::kSlotBytes;
 using dense_tc::kQBytes;
 enum Grad { kDv, kDk, kDq };
@@ -56,23 +55,28 @@ template <Grad M> struct Ring {
   static constexpr int kProducts = M == kDv ? 2 : 3;
   static constexpr int kTiles = M == kDv ? 1 : 2;     // stationary tiles of 64 KiB
   // 32 KiB slots of the three streamed operands
-  static constexpr int kN0 = M == kDv ? 3 : 1, kN1 = M == kDv ? 0 : 1, kN2 = M == kDv ? 2 : 1;
+  static constexpr int kN0 = M == kDv ? 2 : 1, kN1 = M == kDv ? 0 : 1, kN2 = M == kDv ? 3 : 1;
   static constexpr int kSlots = kN0 + kN1 + kN2;
   __device__ static constexpr int slots(int kind) { return kind == 0 ? kN0 : kind == 1 ? kN1 : kN2; }
   __device__ static constexpr int offset(int kind) { return (kind == 0 ? 0 : kind == 1 ? kN0 : kN0 + kN1) * kSlotBytes; }
   static constexpr int kBufs = M == kDv ? 2 : 1;      // S buffers
+  static constexpr int kStats = M == kDv ? 4 : 2;     // buffers of row statistics
 };
-constexpr int kOffCtl = 5 * kSlotBytes + kQBytes;     // 229376, also 3 slots + 2 tiles
-static_assert(3 * kSlotBytes + 2 * kQBytes == kOffCtl, "layouts of equal size");
+constexpr int kOffCtl = 3 * kSlotBytes + 2 * kQBytes; // 229376; dV: 5 slots and one tile
 constexpr int kCtlBytes = 3072;
 constexpr int kSmemBytes = kOffCtl + kCtlBytes;       // 232448: the base itself is 1024-byte aligned
 constexpr uint32_t kTmemP = 128, kTmemD = 256;
 using Pair = dense_tc::Shape<2>;
 }  // namespace dense_bwd
 
+// Tensor maps of one gradient's kernel: streamed operands of S, dP and the
+// gradient's product; the stationary tiles (dQ: Q and dO by token and by row;
+// dK, dV: K and V).
+struct DenseBwdMaps {
+  CUtensorMap s, p, d, fix0, fix1, row0, row1;
+};
+
 struct DenseBwdTcArgs {
-  const __nv_bfloat16* fix0;  // stationary rows: Q (dQ) or K
-  const __nv_bfloat16* fix1;  // dO (dQ) or V (dK)
   const float* lse2;          // [H][stat rows] lse * log2 e, +inf behind a segment's end
   const float* delta;         // [H][stat rows]
   const int32_t* flags;       // by first statistics tile of a segment: not for these kernels
@@ -84,18 +88,18 @@ struct DenseBwdTcArgs {
 };
 
 struct DenseBwdTcCtl {
-  uint64_t full[2][3];                                // of S's and dP's operand, rank 0's: both CTAs' halves
-  uint64_t d_full[2];                                 // of the gradient's operand: this CTA's half
-  uint64_t empty[3][3];
+  uint64_t full[2][2];                                // of S's and dP's operand, rank 0's: both CTAs' halves
+  uint64_t d_full[3];                                 // of the gradient's operand: this CTA's half
+  uint64_t s_done[2], dp_done, d_done[3];             // products: for their readers, and their operand's slot is free
   uint64_t fix_full, fix_empty;
-  uint64_t s_full[2], s_free, dp_full, w_full[2];     // w: P (dV) or dS written
+  uint64_t s_free, w_full[2];                         // S read; P (dV) or dS written
   uint64_t o_full, o_free;
-  uint64_t st_full[2], st_free[2];
+  uint64_t st_full[4], st_free[4];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
 };
-constexpr int kBwdStatOff = 1024;                     // of the control block: two buffers of lse2[128], delta[128]
+constexpr int kBwdStatOff = 1024;                     // of the control block: lse2[128] by buffer, then delta[128] (dK)
 static_assert(sizeof(DenseBwdTcCtl) <= kBwdStatOff, "control block");
 static_assert(kBwdStatOff + 2 * 1024 <= dense_bwd::kCtlBytes, "control block");
 
@@ -122,8 +126,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 template <dense_bwd::Grad M>
 __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
-    dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_p,
-                        const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ DenseTable t,
+    dense_bwd_tc_kernel(const __grid_constant__ DenseBwdMaps tm, const __grid_constant__ DenseTable t,
                         const __grid_constant__ DenseBwdTcArgs a) {
   using namespace dense_bwd;
   using namespace sm100;
@@ -146,21 +149,23 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.full[0][i], 2);
       mbar_init(&ctl.full[1][i], 2);
-      for (int k = 0; k < 3; ++k) mbar_init(&ctl.empty[k][i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.d_full[i], 1);
-      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.s_done[i], 1);
       mbar_init(&ctl.w_full[i], kSoftmaxWarps * 2);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&ctl.d_full[i], 1);
+      mbar_init(&ctl.d_done[i], 1);
+    }
+    for (int i = 0; i < R::kStats; ++i) {
       mbar_init(&ctl.st_full[i], 1);
       mbar_init(&ctl.st_free[i], kSoftmaxWarps);
     }
     mbar_init(&ctl.s_free, kSoftmaxWarps * 2);
-    mbar_init(&ctl.dp_full, 1);
-    mbar_init(&ctl.fix_full, kQWarps * 2);
+    mbar_init(&ctl.dp_done, 1);
+    mbar_init(&ctl.fix_full, 2);
     mbar_init(&ctl.fix_empty, 1);
     mbar_init(&ctl.o_full, 1);
     mbar_init(&ctl.o_free, kSoftmaxWarps * 2);
@@ -186,6 +191,10 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       if (!a.flags[t.slot[x.si]]) return true;
     return false;
   };
+  // a stationary row in its token-major array
+  auto unit_row = [&](int32_t row) -> int64_t {
+    return kByKeys ? (int64_t)(t.q_offset[x.si] + row) * t.G + x.grp : dense_q_row(t, x, row, a.H);
+  };
   if (warp == kProducerWarp) {
     // ============================================================ TMA producer
     // A slot is four boxes of 64 lines x 64 dims, one per lane: rows of this
@@ -209,27 +218,30 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         const int slab = kind == 2 ? lane & 1 : lane & 3, run = kind == 2 ? (lane >> 1) & 1 : 0;
         const int off = kind == 2 ? slab * 16384 + run * 8192 : slab * 8192;
         const int head = kByKeys ? x.grp * t.hpg + c % t.hpg : x.grp;
-        const int64_t r0 = kByKeys ? x.row0 + (int64_t)(c / t.hpg) * kKeys : (int64_t)c * kKeys;   // of the segment
+        const int32_t r0 = kByKeys ? x.row0 + c / t.hpg * kKeys : c * kKeys;   // of the segment
         const int32_t cx = head * kHeadDim + slab * 64 + (kind == 2 ? (int)rank * 128 : 0);
-        const int32_t cy = t.q_offset[x.si] + (int32_t)r0 + (kind == 2 ? run * 64 : (int)rank * 64);
-        if (!(ok = warp_wait_sleep(&ctl.empty[kind][slot], phase ^ 1, abort_flag))) break;
+        const int32_t cy = t.q_offset[x.si] + r0 + (kind == 2 ? run * 64 : (int)rank * 64);
+        uint64_t* const free_bar = kind == 0 ? &ctl.s_done[slot] : kind == 1 ? &ctl.dp_done : &ctl.d_done[slot];
+        if (!(ok = warp_wait_sleep(free_bar, phase ^ 1, abort_flag))) break;
         if (kind == 2) {
           if (lane == 0) mbar_expect_tx(&ctl.d_full[slot], kSlotBytes);
           __syncwarp();
-          if (lane < 4) tma_load_2d(to + off, &tm_d, cx, cy, &ctl.d_full[slot]);
+          if (lane < 4) tma_load_2d(to + off, &tm.d, cx, cy, &ctl.d_full[slot]);
         } else {
           if (lane == 0) mbar_expect_tx_leader<2>(&ctl.full[kind][slot], kSlotBytes);
           __syncwarp();
-          if (lane < 4) tma_load_2d_leader<2>(to + off, kind == 0 ? &tm_s : &tm_p, cx, cy, &ctl.full[kind][slot]);
+          if (lane < 4) tma_load_2d_leader<2>(to + off, kind == 0 ? &tm.s : &tm.p, cx, cy, &ctl.full[kind][slot]);
         }
-        if (kByKeys && kind == 0) {                  // the chunk's row statistics
-          const int b = (int)(xg & 1);
-          if (!(ok = warp_wait_sleep(&ctl.st_free[b], (uint32_t)(((xg >> 1) & 1) ^ 1), abort_flag))) break;
+        // The chunk's row statistics, behind a load whose slot was freed after
+        // the softmax that held the buffer: this wait does not hold up the ring.
+        if (kByKeys && kind == kProducts - 2) {
+          const int b = (int)(xg % R::kStats);
+          if (!(ok = warp_wait_sleep(&ctl.st_free[b], (uint32_t)(((xg / R::kStats) & 1) ^ 1), abort_flag))) break;
           if (lane == 0) {
             const int64_t at = (int64_t)head * a.stat_rows + (int64_t)t.slot[x.si] * kStatTile + r0;
             mbar_expect_tx(&ctl.st_full[b], M == kDv ? 512 : 1024);
-            bulk_load(stats + b * 256, a.lse2 + at, 512, &ctl.st_full[b]);
-            if (M != kDv) bulk_load(stats + b * 256 + 128, a.delta + at, 512, &ctl.st_full[b]);
+            bulk_load(stats + b * 128, a.lse2 + at, 512, &ctl.st_full[b]);
+            if (M != kDv) bulk_load(stats + (R::kStats + b) * 128, a.delta + at, 512, &ctl.st_full[b]);
           }
           __syncwarp();
         }
@@ -238,102 +250,92 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     }
     if (!ok) drain_copies();                         // no copy outlives the CTA
   } else if (warp == kMmaWarp && rank == 0) {
-    // ============================================================ MMA issuer (one thread)
-    if (lane == 0) {
-      int64_t gc = 0, uc = 0;                        // chunks and pieces so far
-      const uint32_t sb = smem_u32(smem);
-      auto wait = [&](uint64_t* bar, int64_t phase) { return mbar_wait_fast(bar, (uint32_t)(phase & 1), abort_flag); };
-      // S (kind 0) or dP (kind 1) of the piece's chunk c
-      auto scores = [&](int kind, int c, int n) -> bool {
-        const int64_t xg = gc + c;
-        const int slot = (int)(xg % R::slots(kind)), b = (int)(xg % kBufs);
-        // with one S buffer: the softmax has read the last chunk's.  With two, P of
-        // chunk c-2 was read by a product issued before.
-        if (kBufs == 1 && kind == 0 && !wait(&ctl.s_free, xg ^ 1)) return false;
-        if (!wait(&ctl.full[kind][slot], xg / R::slots(kind))) return false;
-        tc_fence_after();
-        const uint32_t b_addr = sb + R::offset(kind) + slot * kSlotBytes, a_addr = sb + kOffFix + kind * kQBytes;
-        const uint32_t d = tmem + (kind == 1 ? kTmemP : (uint32_t)b * 128);
+    // ============================================================ MMA issuer
+    int64_t gc = 0, uc = 0;                          // chunks and pieces so far
+    const uint32_t sb = smem_u32(smem), leader = elect_one();
+    auto wait = [&](uint64_t* bar, int64_t phase) { return mbar_wait_fast(bar, (uint32_t)(phase & 1), abort_flag); };
+    // S (kind 0) or dP (kind 1) of the piece's chunk c
+    auto scores = [&](int kind, int c, int n) -> bool {
+      const int64_t xg = gc + c;
+      const int slot = (int)(xg % R::slots(kind));
+      // with one S buffer: the softmax has read the last chunk's.  With two, P of
+      // chunk c-2 was read by a product issued before.
+      if (kBufs == 1 && kind == 0 && !wait(&ctl.s_free, xg ^ 1)) return false;
+      if (!wait(&ctl.full[kind][slot], xg / R::slots(kind))) return false;
+      tc_fence_after();
+      const uint64_t da = desc_sw128(sb + kOffFix + kind * kQBytes, 16, 1024);
+      const uint64_t db = desc_sw128(sb + R::offset(kind) + slot * kSlotBytes, 16, 1024);
+      const uint32_t d = tmem + (kind == 1 ? kTmemP : (uint32_t)slot * 128);
 #pragma unroll
-        for (int kk = 0; kk < 16; ++kk) {            // k-steps of 16 dims
-          const int slab = kk >> 2, sub = kk & 3;
-          const uint64_t da = desc_sw128(a_addr + slab * 16384 + sub * 32, 16, 1024);
-          const uint64_t db = desc_sw128(b_addr + slab * 8192 + sub * 32, 16, 1024);
-          umma_ss<2>(d, da, db, Pair::kIdescS, kk != 0);
-        }
-        umma_commit_cg<2>(kind == 0 ? &ctl.s_full[b] : &ctl.dp_full);
-        umma_commit_cg<2>(&ctl.empty[kind][slot]);
-        if (c == n - 1 && kind == kProducts - 2) umma_commit_cg<2>(&ctl.fix_empty);
-        return true;
-      };
-      auto grad = [&](int c, int n) -> bool {
-        const int64_t xg = gc + c;
-        const int b = (int)(xg % kBufs), slot = (int)(xg % R::kN2);
-        if (!wait(&ctl.w_full[b], xg / kBufs)) return false;      // P or dS, and both halves of the operand
-        if (c == 0 && !wait(&ctl.o_free, uc ^ 1)) return false;
-        tc_fence_after();
-        const uint32_t b_addr = sb + R::offset(2) + slot * kSlotBytes;
-        const uint32_t w = tmem + (M == kDv ? (uint32_t)b * 128 : kTmemP);
+      for (int kk = 0; kk < 16; ++kk)                // k-steps of 16 dims: 32 bytes of a slab's 128-byte lines
+        umma_ss_warp<2>(leader, d, da + (kk >> 2) * 1024 + (kk & 3) * 2, db + (kk >> 2) * 512 + (kk & 3) * 2,
+                        Pair::kIdescS, kk != 0);
+      umma_commit_warp<2>(leader, kind == 0 ? &ctl.s_done[slot] : &ctl.dp_done);
+      if (c == n - 1 && kind == kProducts - 2) umma_commit_warp<2>(leader, &ctl.fix_empty);
+      return true;
+    };
+    auto grad = [&](int c, int n) -> bool {
+      const int64_t xg = gc + c;
+      const int b = (int)(xg % kBufs), slot = (int)(xg % R::kN2);
+      if (!wait(&ctl.w_full[b], xg / kBufs)) return false;        // P or dS, and both halves of the operand
+      if (c == 0 && !wait(&ctl.o_free, uc ^ 1)) return false;
+      tc_fence_after();
+      const uint64_t db = desc_sw128(sb + R::offset(2) + slot * kSlotBytes, 16384, 1024);
+      const uint32_t w = tmem + (M == kDv ? (uint32_t)b * 128 : kTmemP);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {             // k-steps of 16 chunk columns; each half's start at its columns
-          const uint64_t db = desc_sw128(b_addr + kk * 2048, 16384, 1024);
-          umma_ts<2>(tmem + kTmemD, w + (kk >> 2) * 64 + (kk & 3) * 8, db, Pair::kIdescPV, (c | kk) != 0);
-        }
-        umma_commit_cg<2>(&ctl.empty[2][slot]);
-        if (c == n - 1) umma_commit_cg<2>(&ctl.o_full);
-        return true;
-      };
-      bool ok = true;
-      while (ok && next()) {
-        if (!(ok = wait(&ctl.fix_full, uc))) break;
-        fence_acquire_cluster();                     // the other CTA's stationary rows
-        const int n = p.c1 - p.c0;
-        ok = scores(0, 0, n);
-        if (kProducts == 3) ok = ok && scores(1, 0, n);
-        for (int c = 0; c < n && ok; ++c) {
-          if (c + 1 < n) ok = scores(0, c + 1, n);
-          ok = ok && grad(c, n);
-          if (kProducts == 3 && c + 1 < n) ok = ok && scores(1, c + 1, n);
-        }
-        gc += n;
-        ++uc;
+      for (int kk = 0; kk < 8; ++kk)                 // k-steps of 16 chunk columns; each half's start at its columns
+        umma_ts_warp<2>(leader, tmem + kTmemD, w + (kk >> 2) * 64 + (kk & 3) * 8, db + kk * 128, Pair::kIdescPV,
+                        (c | kk) != 0);
+      umma_commit_warp<2>(leader, &ctl.d_done[slot]);
+      if (c == n - 1) umma_commit_warp<2>(leader, &ctl.o_full);
+      return true;
+    };
+    bool ok = true;
+    while (ok && next()) {
+      if (!(ok = wait(&ctl.fix_full, uc))) break;
+      const int n = p.c1 - p.c0;
+      ok = scores(0, 0, n);
+      if (kProducts == 3) ok = ok && scores(1, 0, n);
+      for (int c = 0; c < n && ok; ++c) {
+        if (c + 1 < n) ok = scores(0, c + 1, n);
+        ok = ok && grad(c, n);
+        if (kProducts == 3 && c + 1 < n) ok = ok && scores(1, c + 1, n);
       }
-      // every MMA issued above has finished before TMEM is freed
+      gc += n;
+      ++uc;
+    }
+    // every MMA issued above has finished before TMEM is freed
+    if (leader) {
       umma_commit_pair_local(&ctl.mma_done);
       volatile int never = 0;
       mbar_wait(&ctl.mma_done, 0, &never);
     }
     __syncwarp();
-  } else if (warp >= kQWarp) {
+  } else if (warp == kQWarp) {
     // ============================================================ stationary tiles of the next unit
-    const int qw = warp - kQWarp;
     int64_t uc = 0;
-    while (next()) {
-      if (warp_aborted(abort_flag)) break;
-      if (!warp_wait_sleep(&ctl.fix_empty, (uint32_t)((uc & 1) ^ 1), abort_flag)) break;
-      const int valid = x.nrows - (int)rank * 128;   // rows of this CTA (may be <= 0 or > 128)
-      const int64_t row0 = x.row0 + rank * 128;
-#pragma unroll 4
-      for (int i = 0; i < 64; ++i) {
-        const int r = qw * 64 + i;
-        if (r < valid) {
-          const int64_t row = row0 + r;
-          const int64_t at = kByKeys ? ((int64_t)t.q_offset[x.si] + row) * t.G + x.grp
-                                     : ((int64_t)t.q_offset[x.si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg +
-                                           row % t.hpg;
-          const uint32_t dst = smem_u32(smem + kOffFix) + (lane >> 3) * 16384 + r * 128 +
-                               (((lane & 7) ^ (r & 7)) << 4);
-          cp_async16(dst, a.fix0 + at * kHeadDim + lane * 8, 16);
-          if (R::kTiles == 2) cp_async16(dst + kQBytes, a.fix1 + at * kHeadDim + lane * 8, 16);
-        }
-      }
-      cp_async_wait_all();
-      fence_proxy_async_smem();
+    bool ok = true;
+    while (ok && next()) {
+      if (!(ok = !warp_aborted(abort_flag) &&
+                 warp_wait_sleep(&ctl.fix_empty, (uint32_t)((uc & 1) ^ 1), abort_flag))) break;
+      const int n = kByKeys ? 128 : max(0, min(x.nrows - (int)rank * 128, 128));   // rows of this CTA that are loaded
+      if (lane == 0) mbar_expect_tx_leader<2>(&ctl.fix_full, (uint32_t)(n * kHeadDim * 2 * R::kTiles));
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(&ctl.fix_full, 0);
+      if constexpr (kByKeys) {                       // boxes of 64 keys x 64 dims
+        if (lane < 8 * R::kTiles) {
+          const int tile = lane >> 3, slab = lane & 3, run = (lane >> 2) & 1;
+          tma_load_2d_leader<2>(smem + kOffFix + tile * kQBytes + slab * 16384 + run * 8192,
+                                tile == 0 ? &tm.fix0 : &tm.fix1, x.grp * kHeadDim + slab * 64,
+                                t.q_offset[x.si] + x.row0 + (int)rank * 128 + run * 64, &ctl.fix_full);
+        }
+      } else {
+        const int32_t r0 = x.row0 + (int)rank * 128;
+        load_q_rows<2>(smem + kOffFix, &tm.fix0, &tm.row0, t, x, r0, n, a.H, lane, &ctl.fix_full);
+        load_q_rows<2>(smem + kOffFix + kQBytes, &tm.fix1, &tm.row1, t, x, r0, n, a.H, lane, &ctl.fix_full);
+      }
       ++uc;
     }
-    cp_async_wait_all();
+    if (!ok) drain_copies();
   } else if (warp < kSoftmaxWarps) {
     // ============================================================ P, dS and the epilogue
     const int quad = warp & 3, half = warp >> 2;
@@ -346,22 +348,19 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       const int n = p.c1 - p.c0;
       const int valid = x.nrows - (int)rank * 128;
       const bool active = li < valid;
-      const int64_t row = x.row0 + (active ? (int)rank * 128 + li : 0);
+      const int32_t row = x.row0 + (active ? (int)rank * 128 + li : 0);
       const int32_t seg_n = t.q_len[x.si];
-      const int32_t own = kByKeys ? (int32_t)(x.row0 + rank * 128 + li) : (int32_t)(row / t.hpg);   // position
-      const int64_t at = kByKeys ? ((int64_t)t.q_offset[x.si] + row) * t.G + x.grp
-                                 : ((int64_t)t.q_offset[x.si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg +
-                                       row % t.hpg;
+      const int32_t own = kByKeys ? x.row0 + (int)rank * 128 + li : row / t.hpg;   // position
+      const int64_t at = unit_row(row);
       float lse2 = 0.f, delta = 0.f;                 // of this thread's row (dQ)
       if (!kByKeys) {
-        const int64_t sat = ((int64_t)x.grp * t.hpg + row % t.hpg) * a.stat_rows +
-                            (int64_t)t.slot[x.si] * kStatTile + row / t.hpg;
+        const int64_t sat = (int64_t)(x.grp * t.hpg + row - own * t.hpg) * a.stat_rows +
+                            (int64_t)t.slot[x.si] * kStatTile + own;
         lse2 = a.lse2[sat];
         delta = a.delta[sat];
       }
       // first position of this CTA's stationary rows (dQ: below it no key is masked), last one (dK, dV)
-      const int32_t edge = kByKeys ? (int32_t)(x.row0 + rank * 128 + 127)
-                                   : (int32_t)((x.row0 + rank * 128) / t.hpg);
+      const int32_t edge = kByKeys ? x.row0 + (int)rank * 128 + 127 : (x.row0 + (int)rank * 128) / t.hpg;
       // Rows behind the segment's end become zero in the operand of the chunk's product.
       auto clear_tail = [&](int32_t j0) {
         unsigned char* ds = smem + R::offset(2) + (gc % R::kN2) * kSlotBytes;
@@ -373,11 +372,12 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       for (int c = 0; c < n; ++c, ++gc) {
         const int cc = p.c0 + c;
         const int b = (int)(gc % kBufs);
-        const int32_t j0 = kByKeys ? (int32_t)x.row0 + (cc / t.hpg) * kKeys : cc * kKeys;   // first position of the columns
-        const float* st_l = stats + (gc & 1) * 256 + half * 64;
-        const float* st_d = st_l + 128;
-        if (kByKeys) mbar_wait_fast(&ctl.st_full[gc & 1], (uint32_t)((gc >> 1) & 1), abort_flag);
-        mbar_wait_fast(&ctl.s_full[b], (uint32_t)((gc / kBufs) & 1), abort_flag);
+        const int32_t j0 = kByKeys ? x.row0 + (cc / t.hpg) * kKeys : cc * kKeys;   // first position of the columns
+        const int sbuf = (int)(gc % R::kStats);
+        const float* st_l = stats + sbuf * 128 + half * 64;
+        const float* st_d = st_l + R::kStats * 128;
+        if (kByKeys) mbar_wait_fast(&ctl.st_full[sbuf], (uint32_t)((gc / R::kStats) & 1), abort_flag);
+        mbar_wait_fast(&ctl.s_done[b], (uint32_t)((gc / kBufs) & 1), abort_flag);
         tc_fence_after();
         float w[64];
 #pragma unroll
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
           }
         } else {
           dst = lane_addr + kTmemP + half * 64;
-          mbar_wait_fast(&ctl.dp_full, (uint32_t)(gc & 1), abort_flag);
+          mbar_wait_fast(&ctl.dp_done, (uint32_t)(gc & 1), abort_flag);
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 64; k += 32) {
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if (clear) mbar_arrive_cluster(&ctl.w_full[b], 0); else mbar_arrive_leader<2>(&ctl.w_full[b]);
-          if (kByKeys) mbar_arrive(&ctl.st_free[gc & 1]);
+          if (kByKeys) mbar_arrive(&ctl.st_free[sbuf]);
         }
       }
       mbar_wait_fast(&ctl.o_full, (uint32_t)(uc & 1), abort_flag);
@@ -525,9 +525,9 @@ __global__ void __launch_bounds__(128)
     acc[0] += v0.x; acc[1] += v0.y; acc[2] += v0.z; acc[3] += v0.w;
     acc[4] += v1.x; acc[5] += v1.y; acc[6] += v1.z; acc[7] += v1.w;
   }
-  const int64_t row = x.row0 + r;
-  const int64_t at = t.by_keys ? ((int64_t)t.q_offset[x.si] + row) * t.G + x.grp
-                               : ((int64_t)t.q_offset[x.si] + row / t.hpg) * H + (int64_t)x.grp * t.hpg + row % t.hpg;
+  const int32_t row = x.row0 + r;
+  const int64_t at =
+      t.by_keys ? (int64_t)(t.q_offset[x.si] + row) * t.G + x.grp : dense_q_row(t, x, row, H);
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc[k] *= factor;
   Vec8<__nv_bfloat16> v;

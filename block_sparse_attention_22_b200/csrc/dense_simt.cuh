@@ -43,9 +43,9 @@ struct KvSource {
 
 // Element offset of the row of position j (-1: its page is out of range).
 template <bool PAGED>
-__device__ __forceinline__ int64_t kv_row(const KvSource& s, const DenseTable& t, int si, int grp, int64_t j) {
+__device__ __forceinline__ int64_t kv_row(const KvSource& s, const DenseTable& t, int si, int grp, int32_t j) {
   if (PAGED) {
-    const int64_t pi = j / s.page_tokens;
+    const int32_t pi = j / s.page_tokens;
     const int32_t page = s.table[(int64_t)t.slot[si] * s.max_pages + pi];
     if (page < 0 || page >= s.n_pages) return -1;
     return (((int64_t)page * t.G + grp) * s.page_tokens + (j - pi * s.page_tokens)) * kHeadDim;
@@ -161,19 +161,16 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
   DenseUnit x;
   while (walk.next(t, p, x)) {
     const int si = x.si;
-    auto q_at = [&](int r) -> int64_t {            // row of the token-major arrays, in heads
-      const int64_t row = x.row0 + r;
-      return (int64_t)(t.q_offset[si] + row / t.hpg) * H + (int64_t)x.grp * t.hpg + row % t.hpg;
-    };
+    auto q_at = [&](int r) { return dense_q_row(t, x, x.row0 + r, H); };
     auto load_kv = [&](float* dst, const void* base, int c, bool note) {
       simt_load_rows(dst, kKeys, (const float*)base, [&](int r) -> const float* {
-        const int64_t j = (int64_t)c * kKeys + r;
+        const int32_t j = c * kKeys + r;
         const int64_t off = j < x.kv_len ? kv_row<PAGED>(kv, t, si, x.grp, j) : -1;
         if (PAGED && j < x.kv_len && off < 0) report_error(kErrBadIndex);
         return off < 0 ? nullptr : (const float*)base + off;
       });
       if (note && threadIdx.x < kKeys) {
-        const int64_t j = (int64_t)c * kKeys + threadIdx.x;
+        const int32_t j = c * kKeys + (int)threadIdx.x;
         ok[threadIdx.x] = j < x.kv_len && kv_row<PAGED>(kv, t, si, x.grp, j) >= 0;
       }
       sm100::cp_async_commit();
@@ -310,7 +307,7 @@ __global__ void __launch_bounds__(256)
 // tile's first row, in rows of the segment.
 __device__ __forceinline__ void simt_p_ds(const float* Qs, const float* Os, const float* Ks, const float* Vs,
                                           float* Ps, float* Ds, const float* st_lse, const float* st_delta,
-                                          int64_t row0, int nrows, int hpg, int64_t j0, int64_t n_keys, float s2) {
+                                          int32_t row0, int nrows, int hpg, int32_t j0, int32_t n_keys, float s2) {
   using namespace dense_simt;
   const int tx = threadIdx.x & 15, ra = (threadIdx.x >> 4) * 4;
   float s[4][2], dp[4][2];
@@ -319,7 +316,7 @@ __device__ __forceinline__ void simt_p_ds(const float* Qs, const float* Os, cons
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ra + i;
-    const int64_t pos = (row0 + r) / hpg;
+    const int32_t pos = (row0 + r) / hpg;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int key = tx + 16 * j;
@@ -366,10 +363,7 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
     const int si = x.si;
     if (a.flags && !a.flags[t.slot[si]]) continue;
     __syncthreads();
-    auto q_at = [&](int r) -> int64_t {
-      const int64_t row = x.row0 + r;
-      return (int64_t)(t.q_offset[si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg + row % t.hpg;
-    };
+    auto q_at = [&](int r) { return dense_q_row(t, x, x.row0 + r, a.H); };
     auto rows_of = [&](const void* base) {
       return [&, base](int r) -> const T* {
         return r < x.nrows ? (const T*)base + q_at(r) * kHeadDim : nullptr;
@@ -387,12 +381,12 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][k] = 0.f;
-    const int64_t first_pos = x.row0 / t.hpg;
-    for (int64_t j0 = 0; j0 < x.kv_len; j0 += kBKeys) {
+    const int32_t first_pos = x.row0 / t.hpg;
+    for (int32_t j0 = 0; j0 < x.kv_len; j0 += kBKeys) {
       __syncthreads();
       auto keys_of = [&](const void* base) {
         return [&, base](int r) -> const T* {
-          const int64_t j = j0 + r;
+          const int32_t j = j0 + r;
           return j < x.kv_len ? (const T*)base + ((int64_t)(t.q_offset[si] + j) * t.G + x.grp) * kHeadDim : nullptr;
         };
       };
@@ -404,7 +398,7 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
       __syncthreads();
       int limit[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) limit[i] = (int)min((int64_t)kBKeys, (x.row0 + ra + i) / t.hpg - j0 + 1);
+      for (int i = 0; i < 4; ++i) limit[i] = min(kBKeys, (x.row0 + ra + i) / t.hpg - j0 + 1);
       simt_accumulate<4>(Ds, kBLd, Ks, ra, tx, kBKeys, j0 + kBKeys - 1 > first_pos, limit, acc);
     }
 #pragma unroll
@@ -446,8 +440,8 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
     const int si = find_segment(st, tile);
     if (a.flags && !a.flags[st.slot[si]]) continue;
     __syncthreads();
-    const int64_t j0 = (int64_t)(tile - st.item0[si]) * kBKeys;
-    const int64_t n = st.q_len[si], q0 = st.q_offset[si];
+    const int32_t j0 = (tile - st.item0[si]) * kBKeys, n = st.q_len[si];
+    const int64_t q0 = st.q_offset[si];
     auto key_at = [&](int r) -> int64_t { return ((q0 + j0 + r) * G + grp) * kHeadDim; };
     auto keys_of = [&](const void* base) {
       return [&, base](int r) -> const T* { return j0 + r < n ? (const T*)base + key_at(r) : nullptr; };
@@ -459,11 +453,11 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) dk[i][k] = dv[i][k] = 0.f;
-    for (int64_t row0 = j0 * hpg; row0 < n * hpg; row0 += kBRows) {
-      const int nrows = (int)min((int64_t)kBRows, n * hpg - row0);
+    for (int32_t row0 = j0 * hpg; row0 < n * hpg; row0 += kBRows) {
+      const int nrows = min(kBRows, n * hpg - row0);
       auto q_at = [&](int r) -> int64_t {
-        const int64_t row = row0 + r;
-        return (q0 + row / hpg) * a.H + (int64_t)grp * hpg + row % hpg;
+        const int32_t tok = (row0 + r) / hpg;
+        return (q0 + tok) * a.H + grp * hpg + (row0 + r - tok * hpg);
       };
       auto rows_of = [&](const void* base) {
         return [&, base](int r) -> const T* {
@@ -487,7 +481,7 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
       for (int r = 0; r < nrows; ++r) {
         const float4 p = *reinterpret_cast<const float4*>(Ps + r * kBLd + kq);
         const float4 s = *reinterpret_cast<const float4*>(Ds + r * kBLd + kq);
-        const int64_t pos = limited ? (row0 + r) / hpg : 0;
+        const int32_t pos = limited ? (row0 + r) / hpg : 0;
         const float pp[4] = {p.x, p.y, p.z, p.w}, ss[4] = {s.x, s.y, s.z, s.w};
         float4 x[2], y[2];
 #pragma unroll

@@ -23,12 +23,14 @@
 //
 // Per CTA 12 warps: eight softmax warps (two per TMEM lane quadrant, each
 // thread one row and half of a chunk's keys and dims), one TMA producer that
-// fills three 32 KiB slots of K and two of V in the order the MMAs consume them
-// (K0, K1, V0, K2, V1, ...), one thread that issues the MMAs (in rank 0), two
-// warps that load Q for the next unit.  K completes on rank 0's barrier, V on
+// fills two 32 KiB slots each of K and V in the order the MMAs consume them
+// (K0, K1, V0, K2, V1, ...), one warp that issues the MMAs (in rank 0), one
+// that loads Q of the next unit and one that checks V of the unit's own tokens.  K completes on rank 0's barrier, V on
 // each CTA's own, where the softmax warps wait for it before they hand over P,
-// so the MMA thread waits once per product and needs no fence.  TMEM: two S
-// buffers (each half's P overwrites its own S columns), O in columns 256..511.
+// so the MMA warp waits once per product and needs no fence.  A product is
+// committed to one barrier, which its readers and its slot's producer share.
+// TMEM: two S buffers (each half's P overwrites its own S columns), O in
+// columns 256..511.
 //
 // Keys that do not count -- beyond the sequence, on a page out of range, after
 // a row's position -- may hold anything: their scores are replaced by -inf;
@@ -52,15 +54,15 @@ namespace dense_tc {
 constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kQWarps = 2;
-constexpr int kSlots = 5, kKSlots = 3, kVSlots = 2;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kNfWarp = 11;
+constexpr int kSlots = 4, kKSlots = 2, kVSlots = 2;        // K's as many as S buffers: they share barriers
 constexpr int kSlotBytes = 32768;
 constexpr int kQBytes = 65536;                        // 128 rows x 256 dims, 4 slabs of 16 KiB
 constexpr int kOffV = kKSlots * kSlotBytes;
-constexpr int kOffQ = kSlots * kSlotBytes;            // 163840
-constexpr int kOffCtl = kOffQ + kQBytes;              // 229376
+constexpr int kOffQ = kSlots * kSlotBytes;            // 131072
+constexpr int kOffCtl = kOffQ + kQBytes;              // 196608
 constexpr int kCtlBytes = 3072;
-constexpr int kSmemBytes = kOffCtl + kCtlBytes;       // 232448: the base itself is 1024-byte aligned
+constexpr int kSmemBytes = kOffCtl + kCtlBytes;       // 199680: the base itself is 1024-byte aligned
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
 constexpr int kNfBufs = 4;                            // units whose non-finite lists may be in use at once
 template <int CG> struct Shape {
@@ -86,14 +88,13 @@ struct DenseTcArgs {
 struct DenseTcCtl {
   uint64_t k_full[dense_tc::kKSlots];     // rank 0's: both CTAs' halves
   uint64_t v_full[dense_tc::kVSlots];     // this CTA's half
-  uint64_t k_empty[dense_tc::kKSlots], v_empty[dense_tc::kVSlots];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], p_free[2];
+  uint64_t s_done[2], p_full[2], pv_done[2];          // by chunk parity
   uint64_t o_full, o_free;
   uint64_t nf_full[dense_tc::kNfBufs];
   uint64_t mma_done;
   float red[2][2][128];                   // by chunk parity: row maxima / sums of the two warps of a row
-  uint32_t nf[dense_tc::kNfBufs][dense_tc::kQWarps][8];   // keys first_pos+1+i whose V is not finite
+  uint32_t nf[dense_tc::kNfBufs][8];   // keys first_pos+1+i whose V is not finite
   uint32_t tmem_base;
   int abort;
 };
@@ -113,6 +114,31 @@ __device__ __forceinline__ void dense_arrive(uint64_t* bar) {
   if constexpr (CG == 1) sm100::mbar_arrive(bar); else sm100::mbar_arrive_cluster(bar, 0);
 }
 
+// Loads rows row0 .. row0+n-1 (n <= 128) of a unit's segment and group into a
+// 128-byte swizzled tile, completing n * 512 bytes on rank 0's barrier: a token's
+// heads are consecutive rows of the token-major array, so a whole token is one
+// box per 64 dims, and the rows of tokens cut by the tile's ends are boxes of one
+// row.  By TMA, since the tensor cores' operand reads leave other shared-memory
+// writes little room: cp.async took 25 us for 128 KiB under them.  (The swizzle
+// goes by address bits, so boxes may start at any 128-byte line.)
+template <int CG>
+__device__ __forceinline__ void load_q_rows(unsigned char* tile, const CUtensorMap* tokens, const CUtensorMap* rows,
+                                            const DenseTable& t, const DenseUnit& x, int32_t row0, int n, int H,
+                                            int lane, uint64_t* bar) {
+  const int h0 = row0 % t.hpg;
+  const int lead = h0 == 0 ? 0 : min(t.hpg - h0, n), whole = (n - lead) / t.hpg, tail = n - lead - whole * t.hpg;
+  for (int i = lane; i < 4 * whole; i += 32) {
+    const int r = lead + (i >> 2) * t.hpg;
+    sm100::tma_load_2d_leader<CG>(tile + (i & 3) * 16384 + r * 128, tokens, (i & 3) * 64,
+                                  (int32_t)dense_q_row(t, x, row0 + r, H), bar);
+  }
+  for (int i = lane; i < 4 * (lead + tail); i += 32) {
+    const int e = i >> 2, r = e < lead ? e : n - tail + (e - lead);
+    sm100::tma_load_2d_leader<CG>(tile + (i & 3) * 16384 + r * 128, rows, (i & 3) * 64,
+                                  (int32_t)dense_q_row(t, x, row0 + r, H), bar);
+  }
+}
+
 // After an abort: copies in flight land within microseconds; the CTA stays for
 // about a millisecond.
 __device__ __forceinline__ void drain_copies() {
@@ -124,6 +150,7 @@ __device__ __forceinline__ void drain_copies() {
 template <int CG, bool PAGED>
 __global__ void __launch_bounds__(dense_tc::kThreads, 1)
     dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_tok, const __grid_constant__ CUtensorMap tm_row,
                         const __grid_constant__ DenseTable t, const __grid_constant__ DenseTcArgs a) {
   using namespace dense_tc;
   using namespace sm100;
@@ -142,21 +169,15 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kKSlots; ++i) {
-      mbar_init(&ctl.k_full[i], CG);
-      mbar_init(&ctl.k_empty[i], 1);
-    }
-    for (int i = 0; i < kVSlots; ++i) {
-      mbar_init(&ctl.v_full[i], 1);
-      mbar_init(&ctl.v_empty[i], 1);
-    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.k_full[i], CG);
+      mbar_init(&ctl.v_full[i], 1);
+      mbar_init(&ctl.s_done[i], 1);
       mbar_init(&ctl.p_full[i], kSoftmaxWarps * CG);
-      mbar_init(&ctl.p_free[i], 1);
+      mbar_init(&ctl.pv_done[i], 1);
     }
-    for (int i = 0; i < kNfBufs; ++i) mbar_init(&ctl.nf_full[i], kQWarps);
-    mbar_init(&ctl.q_full, kQWarps * CG);
+    for (int i = 0; i < kNfBufs; ++i) mbar_init(&ctl.nf_full[i], 1);
+    mbar_init(&ctl.q_full, CG);
     mbar_init(&ctl.q_empty, 1);
     mbar_init(&ctl.o_full, 1);
     mbar_init(&ctl.o_free, kSoftmaxWarps * CG);
@@ -227,13 +248,13 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
         const uint32_t bytes = (uint32_t)__popc(live) * (uint32_t)(a.box * 128);
         if (kind == 0) {
           const int slot = (int)(xg % kKSlots);
-          if (!(ok = warp_wait_sleep(&ctl.k_empty[slot], (uint32_t)(((xg / kKSlots) & 1) ^ 1), abort_flag))) break;
+          if (!(ok = warp_wait_sleep(&ctl.s_done[slot], (uint32_t)(((xg / kKSlots) & 1) ^ 1), abort_flag))) break;
           if (lane == 0) mbar_expect_tx_leader<CG>(&ctl.k_full[slot], bytes);
           __syncwarp();
           if (y >= 0) tma_load_2d_leader<CG>(smem + slot * kSlotBytes + off, &tm_k, cx, y, &ctl.k_full[slot]);
         } else {
           const int slot = (int)(xg % kVSlots);
-          if (!(ok = warp_wait_sleep(&ctl.v_empty[slot], (uint32_t)(((xg / kVSlots) & 1) ^ 1), abort_flag))) break;
+          if (!(ok = warp_wait_sleep(&ctl.pv_done[slot], (uint32_t)(((xg / kVSlots) & 1) ^ 1), abort_flag))) break;
           if (lane == 0) mbar_expect_tx(&ctl.v_full[slot], bytes);
           __syncwarp();
           if (y >= 0) tma_load_2d(smem + kOffV + slot * kSlotBytes + off, &tm_v, cx, y, &ctl.v_full[slot]);
@@ -243,110 +264,105 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
     }
     if (!ok) drain_copies();                                 // no copy outlives the CTA
   } else if (warp == kMmaWarp && rank == 0) {
-    // ============================================================ MMA issuer (one thread)
-    if (lane == 0) {
-      int64_t gc = 0, uc = 0;                                // chunks and pieces so far
-      const uint32_t sb = smem_u32(smem);
-      auto wait = [&](uint64_t* bar, int64_t phase) { return mbar_wait_fast(bar, (uint32_t)(phase & 1), abort_flag); };
-      auto pv = [&](int cx, int n) -> bool {
-        const int64_t xg = gc + cx;
-        const int pb = (int)(xg & 1), slot = (int)(xg % kVSlots);
-        if (!wait(&ctl.p_full[pb], xg >> 1)) return false;   // P, and both halves of V
-        if (cx == 0 && !wait(&ctl.o_free, uc ^ 1)) return false;
+    // ============================================================ MMA issuer
+    int64_t gc = 0, uc = 0;                                  // chunks and pieces so far
+    const uint32_t sb = smem_u32(smem), leader = elect_one();
+    auto wait = [&](uint64_t* bar, int64_t phase) { return mbar_wait_fast(bar, (uint32_t)(phase & 1), abort_flag); };
+    auto pv = [&](int cx, int n) -> bool {
+      const int64_t xg = gc + cx;
+      const int b = (int)(xg & 1);
+      if (!wait(&ctl.p_full[b], xg >> 1)) return false;      // P, and both halves of V
+      if (cx == 0 && !wait(&ctl.o_free, uc ^ 1)) return false;
+      tc_fence_after();
+      const uint64_t db = desc_sw128(sb + kOffV + b * kSlotBytes, KC * 128, 1024);
+#pragma unroll
+      for (int kk = 0; kk < KC / 16; ++kk)                   // k-steps of 16 keys; each half's P in its S columns
+        umma_ts_warp<CG>(leader, tmem + kTmemO, tmem + b * KC + (kk / (KC / 32)) * NK + (kk % (KC / 32)) * 8,
+                         db + kk * 128, Shape<CG>::kIdescPV, (cx | kk) != 0);
+      umma_commit_warp<CG>(leader, &ctl.pv_done[b]);
+      if (cx == n - 1) umma_commit_warp<CG>(leader, &ctl.o_full);
+      return true;
+    };
+    const uint64_t da = desc_sw128(sb + kOffQ, 16, 1024);
+    bool ok = true;
+    while (ok && walk.next(t, p, x)) {
+      if (!(ok = wait(&ctl.q_full, uc))) break;
+      const int n = p.c1 - p.c0;
+      for (int c = 0; c < n && ok; ++c) {
+        const int64_t xg = gc + c;
+        const int b = (int)(xg & 1);
+        // S buffer b: P of chunk c-2 (of this or the last piece) was read by a product issued before
+        if (!(ok = wait(&ctl.k_full[b], xg >> 1))) break;
         tc_fence_after();
-        const uint32_t v_addr = sb + kOffV + slot * kSlotBytes;
+        const uint64_t db = desc_sw128(sb + b * kSlotBytes, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < KC / 16; ++kk) {               // k-steps of 16 keys; each half's P in its S columns
-          const uint64_t db = desc_sw128(v_addr + kk * 2048, KC * 128, 1024);
-          umma_ts<CG>(tmem + kTmemO, tmem + pb * KC + (kk / (KC / 32)) * NK + (kk % (KC / 32)) * 8, db,
-                      Shape<CG>::kIdescPV, (cx | kk) != 0);
-        }
-        umma_commit_cg<CG>(&ctl.v_empty[slot]);
-        umma_commit_cg<CG>(&ctl.p_free[pb]);
-        if (cx == n - 1) umma_commit_cg<CG>(&ctl.o_full);
-        return true;
-      };
-      bool ok = true;
-      while (ok && walk.next(t, p, x)) {
-        if (!(ok = wait(&ctl.q_full, uc))) break;
-        if (CG == 2) fence_acquire_cluster();                // Q of the other CTA
-        const int n = p.c1 - p.c0;
-        for (int c = 0; c < n && ok; ++c) {
-          const int64_t xg = gc + c;
-          const int b = (int)(xg & 1), slot = (int)(xg % kKSlots);
-          // S buffer b: P of chunk c-2 (of this or the last piece) was read by a product issued before
-          if (!(ok = wait(&ctl.k_full[slot], xg / kKSlots))) break;
-          tc_fence_after();
-          const uint32_t k_addr = sb + slot * kSlotBytes, q_addr = sb + kOffQ;
-#pragma unroll
-          for (int kk = 0; kk < 16; ++kk) {                  // k-steps of 16 dims
-            const int slab = kk >> 2, sub = kk & 3;
-            const uint64_t da = desc_sw128(q_addr + slab * 16384 + sub * 32, 16, 1024);
-            const uint64_t db = desc_sw128(k_addr + slab * 8192 + sub * 32, 16, 1024);
-            umma_ss<CG>(tmem + b * KC, da, db, Shape<CG>::kIdescS, kk != 0);
-          }
-          umma_commit_cg<CG>(&ctl.s_full[b]);
-          umma_commit_cg<CG>(&ctl.k_empty[slot]);
-          if (c == n - 1) umma_commit_cg<CG>(&ctl.q_empty);
-          if (c > 0) ok = pv(c - 1, n);
-        }
-        if (!ok) break;
-        ok = pv(n - 1, n);
-        gc += n;
-        ++uc;
+        for (int kk = 0; kk < 16; ++kk)                      // k-steps of 16 dims: 32 bytes of a slab's 128-byte lines
+          umma_ss_warp<CG>(leader, tmem + b * KC, da + (kk >> 2) * 1024 + (kk & 3) * 2,
+                           db + (kk >> 2) * 512 + (kk & 3) * 2, Shape<CG>::kIdescS, kk != 0);
+        umma_commit_warp<CG>(leader, &ctl.s_done[b]);
+        if (c == n - 1) umma_commit_warp<CG>(leader, &ctl.q_empty);
+        if (c > 0) ok = pv(c - 1, n);
       }
-      // every MMA issued above has finished before TMEM is freed
+      if (!ok) break;
+      ok = pv(n - 1, n);
+      gc += n;
+      ++uc;
+    }
+    // every MMA issued above has finished before TMEM is freed
+    if (leader) {
       if constexpr (CG == 1) umma_commit(&ctl.mma_done); else umma_commit_pair_local(&ctl.mma_done);
       volatile int never = 0;
       mbar_wait(&ctl.mma_done, 0, &never);
     }
     __syncwarp();
-  } else if (warp >= kQWarp) {
-    // ============================================================ Q of the next unit; V of its own tokens checked
-    const int qw = warp - kQWarp;
+  } else if (warp == kQWarp) {
+    // ============================================================ Q of the next unit
+    int64_t uc = 0;
+    bool ok = true;
+    while (ok && walk.next(t, p, x)) {
+      if (!(ok = !warp_aborted(abort_flag) &&
+                 warp_wait_sleep(&ctl.q_empty, (uint32_t)((uc & 1) ^ 1), abort_flag))) break;
+      const int n = max(0, min(x.nrows - (int)rank * 128, 128));             // rows of this CTA
+      if (lane == 0) mbar_expect_tx_leader<CG>(&ctl.q_full, (uint32_t)n * (kHeadDim * 2));
+      __syncwarp();
+      load_q_rows<CG>(smem + kOffQ, &tm_tok, &tm_row, t, x, x.row0 + (int)rank * 128, n, a.H, lane, &ctl.q_full);
+      ++uc;
+    }
+    if (!ok) drain_copies();
+  } else if (warp == kNfWarp) {
+    // ============================================================ V of the unit's own tokens checked
     int64_t uc = 0;
     while (walk.next(t, p, x)) {
       if (warp_aborted(abort_flag)) break;
+      // not further ahead than Q: the lists of the units before are then no longer read
       if (!warp_wait_sleep(&ctl.q_empty, (uint32_t)((uc & 1) ^ 1), abort_flag)) break;
-      const int valid = x.nrows - (int)rank * 128;           // rows of this CTA (may be <= 0 or > 128)
-      const int64_t row0 = x.row0 + rank * 128;
-      const uint32_t q_addr = smem_u32(smem + kOffQ);
-#pragma unroll 4
-      for (int i = 0; i < 64; ++i) {
-        const int r = qw * 64 + i;
-        if (r < valid) {
-          const int64_t row = row0 + r;
-          const int64_t at = ((int64_t)t.q_offset[x.si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg + row % t.hpg;
-          cp_async16(q_addr + (lane >> 3) * 16384 + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                     a.q + at * kHeadDim + lane * 8, 16);
-        }
-      }
-      const int64_t first = t.pos0[x.si] + x.row0 / t.hpg;   // position of the unit's first row
-      const int own = (int)(x.kv_len - 1 - first);           // keys that only some rows see (<= 255)
+      // keys that only some rows see (at most 255), 32 at a time
+      const int32_t first = t.pos0[x.si] + x.row0 / t.hpg;   // position of the unit's first row
+      const int own = x.kv_len - 1 - first;
       uint32_t word = 0;
-      for (int i = qw; i < own; i += kQWarps) {
-        const int64_t off = kv_row<PAGED>(a.kv, t, x.si, x.grp, first + 1 + i);
-        bool nf = false;
-        if (off >= 0) {
-          const uint4 v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.kv.v + off + lane * 8);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int i0 = 0; i0 < own; i0 += 32) {
+        const int64_t my_off = i0 + lane < own ? kv_row<PAGED>(a.kv, t, x.si, x.grp, first + 1 + i0 + lane) : -1;
+        uint32_t bits = 0;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+          const int64_t off = __shfl_sync(0xffffffffu, my_off, i);
+          bool nf = false;
+          if (off >= 0) {
+            const uint4 v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.kv.v + off + lane * 8);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            nf |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+            for (int k = 0; k < 4; ++k)
+              nf |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+          }
+          bits |= (__any_sync(0xffffffffu, nf) ? 1u : 0u) << i;
         }
-        if (__any_sync(0xffffffffu, nf) && lane == (i >> 5)) word |= 1u << (i & 31);
+        if (lane == (i0 >> 5)) word = bits;
       }
-      if (lane < 8) ctl.nf[uc % kNfBufs][qw][lane] = word;
-      cp_async_wait_all();
-      fence_proxy_async_smem();
+      if (lane < 8) ctl.nf[uc % kNfBufs][lane] = word;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&ctl.nf_full[uc % kNfBufs]);
-        dense_arrive<CG>(&ctl.q_full);
-      }
+      if (lane == 0) mbar_arrive(&ctl.nf_full[uc % kNfBufs]);
       ++uc;
     }
-    cp_async_wait_all();
   } else if (warp < kSoftmaxWarps) {
     // ============================================================ softmax + epilogue
     const int quad = warp & 3, half = warp >> 2;
@@ -359,33 +375,37 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       const int n = p.c1 - p.c0;
       const int valid = x.nrows - (int)rank * 128;
       const bool active = li < valid, warp_active = quad * 32 < valid;
-      const int64_t row = x.row0 + rank * 128 + (active ? li : 0);
-      const int32_t pos = t.pos0[x.si] + (int32_t)(row / t.hpg);
-      const int64_t at = ((int64_t)t.q_offset[x.si] + row / t.hpg) * a.H + (int64_t)x.grp * t.hpg + row % t.hpg;
-      const int32_t first = t.pos0[x.si] + (int32_t)(x.row0 / t.hpg);               // of the unit
-      const int32_t first_cta = t.pos0[x.si] + (int32_t)((x.row0 + rank * 128) / t.hpg);
-      const int32_t kv_len = (int32_t)x.kv_len;
-      mbar_wait_sleep(&ctl.nf_full[uc % kNfBufs], (uint32_t)((uc / kNfBufs) & 1), abort_flag);
-      const uint32_t my_nf = lane < 8 ? ctl.nf[uc % kNfBufs][0][lane] | ctl.nf[uc % kNfBufs][1][lane] : 0u;
-      const bool any_nf = __any_sync(0xffffffffu, my_nf != 0);
-      // bit per run of 16 keys of a chunk: its page is out of range
-      auto bad_runs = [&](int c) -> uint32_t {
-        bool bad = false;
-        if (PAGED && lane < KC / 16) {
-          const int32_t key = c * KC + lane * 16;
-          if (key < kv_len) {
-            const int32_t page = a.kv.table[(int64_t)t.slot[x.si] * a.kv.max_pages + key / a.kv.page_tokens];
-            bad = page < 0 || page >= a.kv.n_pages;
-          }
-        }
-        return PAGED ? __ballot_sync(0xffffffffu, bad) : 0u;
+      const int32_t row = x.row0 + (active ? (int)rank * 128 + li : 0);
+      const int32_t pos = t.pos0[x.si] + row / t.hpg;
+      const int64_t at = dense_q_row(t, x, row, a.H);
+      const int32_t first = t.pos0[x.si] + x.row0 / t.hpg;               // of the unit
+      const int32_t first_cta = t.pos0[x.si] + (x.row0 + (int)rank * 128) / t.hpg;
+      const int32_t kv_len = x.kv_len;
+      // the unit's list of values that are not finite, taken before its first own key
+      bool nf_taken = false, any_nf = false;
+      uint32_t my_nf = 0;
+      // the page of run `lane` of 16 keys of a chunk; 0 where nothing is looked up
+      auto page_of_run = [&](int c) -> int32_t {
+        const int32_t key = c * KC + lane * 16;
+        if (!PAGED || lane >= KC / 16 || c >= p.c1 || key >= kv_len) return 0;
+        return a.kv.table[(int64_t)t.slot[x.si] * a.kv.max_pages + key / a.kv.page_tokens];
       };
+      int32_t next_page = page_of_run(p.c0);
       float m = -INFINITY, l = 0.f;
       for (int c = 0; c < n; ++c, ++gc) {
         const int b = (int)(gc & 1);
         const int32_t j0 = (p.c0 + c) * KC;
-        const uint32_t bad = bad_runs(p.c0 + c);
-        mbar_wait_fast(&ctl.s_full[b], (uint32_t)((gc >> 1) & 1), abort_flag);
+        // bit per run of 16 keys of the chunk: its page is out of range
+        const uint32_t bad =
+            PAGED ? __ballot_sync(0xffffffffu, next_page < 0 || next_page >= a.kv.n_pages) : 0u;
+        next_page = page_of_run(p.c0 + c + 1);
+        if (!nf_taken && j0 + KC - 1 > first) {
+          nf_taken = true;
+          mbar_wait_fast(&ctl.nf_full[uc % kNfBufs], (uint32_t)((uc / kNfBufs) & 1), abort_flag);
+          my_nf = lane < 8 ? ctl.nf[uc % kNfBufs][lane] : 0u;
+          any_nf = __any_sync(0xffffffffu, my_nf != 0);
+        }
+        mbar_wait_fast(&ctl.s_done[b], (uint32_t)((gc >> 1) & 1), abort_flag);
         tc_fence_after();
         const bool clear = j0 + KC > kv_len || bad || (any_nf && j0 + KC - 1 > first);
         if (clear) {
@@ -443,7 +463,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
           if (__any_sync(0xffffffffu, need)) {
             // O holds chunks 0..c-1 (c >= 1 here): wait for the last of their products
             const int64_t xp = gc - 1;
-            mbar_wait_fast(&ctl.p_free[xp & 1], (uint32_t)((xp >> 1) & 1), abort_flag);
+            mbar_wait_fast(&ctl.pv_done[xp & 1], (uint32_t)((xp >> 1) & 1), abort_flag);
             tc_fence_after();
 #pragma unroll 1
             for (int piece = 0; piece < 8; ++piece) {
