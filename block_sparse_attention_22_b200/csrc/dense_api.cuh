@@ -6,6 +6,7 @@
 #include "dense.cuh"
 #include "dense_simt.cuh"
 #include "dense_tc.cuh"
+#include "dense_decode.cuh"
 #include "dense_bwd_tc.cuh"
 
 namespace qsa {
@@ -52,21 +53,20 @@ qsa_status_t check_dense_segments(const qsa_segment_t* segs, int32_t n_segs, int
 }
 
 // ------------------------------------------------------------------ plan
-// Shape of one kind of launch.
+// Shape of one kind of launch.  For levelling: a unit's fixed cost (loading Q,
+// the epilogue) in chunks, and the fewest chunks a CTA takes of the tail, below
+// which a piece's partial result costs more than the chunks it saves.
 struct DenseKind {
   int rows, kc, grid;
   bool by_keys;
+  int cost = 2, min_tail = 4;
 };
-// A unit's fixed cost (loading Q, the epilogue) in chunks, for levelling.
-constexpr int64_t kUnitCost = 2;
-// Fewest chunks a CTA takes of the tail: below it a piece's partial result
-// costs more than the chunks it saves.
-constexpr int64_t kMinTail = 4;
 
 int64_t unit_chunks(const DenseTable& t, int u) { return dense_unit(t, u).nchunks; }
 
 // Fills rounds, cut and the list of cut units of a table whose segments are set.
-void cut_table(DenseTable& t, DenseSplits& sp) {
+void cut_table(DenseTable& t, DenseSplits& sp, const DenseKind& kind) {
+  const int64_t kUnitCost = kind.cost, kMinTail = kind.min_tail;
   const int grid = t.grid;
   const int n_units = t.item0[t.n] * t.G;
   std::vector<int32_t> chunks((size_t)n_units);
@@ -187,27 +187,49 @@ qsa_status_t for_each_dense(const Geo& g, std::vector<qsa_segment_t> segs, const
       most = std::max(most, std::min<int64_t>(rows, kind.rows));
     }
     t.prows = (int32_t)most;
-    cut_table(t, sp);
+    cut_table(t, sp, kind);
     const qsa_status_t r = launch(t, sp);
     if (r != QSA_OK) return r;
   }
   return QSA_OK;
 }
 
-// Segments of few query rows (decode) and the others, with the shape of their launches.
-void dense_kinds(const Geo& g, bool tc, const qsa_segment_t* segs, int n, std::vector<qsa_segment_t>& narrow,
-                 std::vector<qsa_segment_t>& wide, DenseKind& kn, DenseKind& kw) {
+// A forward call's segments by the kernel that takes them, in launch order.
+enum class DenseForm { kWide, kNarrow, kDecode };
+struct DenseGroup {
+  DenseForm form;
+  DenseKind kind;
+  std::vector<qsa_segment_t> segs;
+};
+
+// bf16: single tokens over a cache go to the decode kernel, other segments of
+// at most 128 rows to single CTAs unless larger ones are there, whose pairs then
+// take them too (one launch and its tail, 15 us, for a few half-empty tiles).
+std::vector<DenseGroup> dense_groups(const Geo& g, bool tc, bool paged, const qsa_segment_t* segs, int n) {
+  DenseGroup wide{DenseForm::kWide, {}, {}}, narrow{DenseForm::kNarrow, {}, {}}, decode{DenseForm::kDecode, {}, {}};
   if (tc) {
     using N = dense_tc::Shape<1>;
     using W = dense_tc::Shape<2>;
-    kn = {N::kRows, N::kKeys, N::kGrid, false};
-    kw = {W::kRows, W::kKeys, W::kGrid, false};
+    narrow.kind = {N::kRows, N::kKeys, N::kGrid, false};
+    wide.kind = {W::kRows, W::kKeys, W::kGrid, false};
+    decode.kind = {dense_decode::kRows, dense_decode::kKeys, kNumSms, false, 1, 1};
   } else {
-    kn = {dense_simt::kRowsNarrow, dense_simt::kKeys, kNumSms, false};
-    kw = {dense_simt::kRowsWide, dense_simt::kKeys, kNumSms, false};
+    narrow.kind = {dense_simt::kRowsNarrow, dense_simt::kKeys, kNumSms, false};
+    wide.kind = {dense_simt::kRowsWide, dense_simt::kKeys, kNumSms, false};
   }
-  for (int i = 0; i < n; ++i)
-    if (segs[i].q_len > 0) ((int64_t)segs[i].q_len * g.hpg <= kn.rows ? narrow : wide).push_back(segs[i]);
+  for (int i = 0; i < n; ++i) {
+    if (segs[i].q_len <= 0) continue;
+    const bool few = (int64_t)segs[i].q_len * g.hpg <= narrow.kind.rows;
+    (tc && paged && segs[i].q_len == 1 ? decode : few ? narrow : wide).segs.push_back(segs[i]);
+  }
+  if (tc && !wide.segs.empty()) {
+    wide.segs.insert(wide.segs.end(), narrow.segs.begin(), narrow.segs.end());
+    narrow.segs.clear();
+  }
+  std::vector<DenseGroup> out;
+  for (DenseGroup* d : {&wide, &narrow, &decode})
+    if (!d->segs.empty()) out.push_back(std::move(*d));
+  return out;
 }
 
 // Bytes of a table's partial results.
@@ -215,16 +237,14 @@ size_t partial_bytes(const DenseTable& t, const DenseSplits& sp) {
   return sp.n > 0 ? (size_t)2 * t.grid * t.prows * dense::kPartFloats * 4 : 0;
 }
 
-size_t dense_fwd_ws(const Geo& g, bool tc, const qsa_segment_t* segs, int n) {
-  std::vector<qsa_segment_t> narrow, wide;
-  DenseKind kn, kw;
-  dense_kinds(g, tc, segs, n, narrow, wide, kn, kw);
+size_t dense_fwd_ws(const Geo& g, bool tc, bool paged, const qsa_segment_t* segs, int n) {
   size_t ws = 0;
-  auto note = [&](const DenseTable& t, const DenseSplits& sp) {
-    ws = std::max(ws, partial_bytes(t, sp));
-    return QSA_OK;
-  };
-  if (for_each_dense(g, narrow, kn, note) != QSA_OK || for_each_dense(g, wide, kw, note) != QSA_OK) return SIZE_MAX;
+  for (const DenseGroup& d : dense_groups(g, tc, paged, segs, n))
+    if (for_each_dense(g, d.segs, d.kind, [&](const DenseTable& t, const DenseSplits& sp) {
+          ws = std::max(ws, partial_bytes(t, sp));
+          return QSA_OK;
+        }) != QSA_OK)
+      return SIZE_MAX;
   return align_up(ws, 256);
 }
 
@@ -278,6 +298,15 @@ cudaError_t launch_dense_tc(const DenseTable& t, const CUtensorMap (&m)[4], cons
   return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], t, a);
 }
 
+cudaError_t launch_dense_decode(const DenseTable& t, const DenseTcArgs& a, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(dense_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             dense_decode::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return launch_chained(dense_decode_kernel, dim3(t.grid), dim3(dense_decode::kThreads), dense_decode::kSmemBytes, st,
+                        t, a);
+}
+
 template <typename T>
 cudaError_t launch_dense_combine(const Geo& g, const DenseTable& t, const DenseSplits& sp, const float* part, void* o,
                                  float* lse, cudaStream_t st) {
@@ -291,28 +320,28 @@ template <bool PAGED>
 qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int n, const KvSource& kv,
                            int64_t kv_rows, int kv_groups, int32_t n_tokens, const void* q, void* o, float* lse,
                            void* ws, size_t ws_bytes, cudaStream_t st) {
-  const size_t need = dense_fwd_ws(g, tc, segs, n);
+  const size_t need = dense_fwd_ws(g, tc, PAGED, segs, n);
   if (need == SIZE_MAX) return QSA_ERR_UNSUPPORTED;
   if (need > 0 && (!ws || ws_bytes < need)) return QSA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return QSA_ERR_INVALID_ARG;
-  std::vector<qsa_segment_t> narrow, wide;
-  DenseKind kn, kw;
-  dense_kinds(g, tc, segs, n, narrow, wide, kn, kw);
   float* part = (float*)ws;
-  CUtensorMap m[4];                      // K, V, Q by token, Q by row
+  CUtensorMap m[4];                      // K, V, Q by whole tokens, Q by parts of one
   DenseTcArgs a;
   if (tc) {
     if ((int64_t)n_tokens * g.H > INT32_MAX - 512) return QSA_ERR_UNSUPPORTED;      // TMA row coordinates
     a = {kv, (const __nv_bfloat16*)q, (__nv_bfloat16*)o, lse, part, g.H, PAGED ? dense_box(kv.page_tokens) : 64,
          g.scale};
     if (!make_dense_map(&m[0], kv.k, kv_rows, kv_groups, a.box) || !make_dense_map(&m[1], kv.v, kv_rows, kv_groups, a.box) ||
-        !make_dense_map(&m[2], q, (int64_t)n_tokens * g.H, 1, g.hpg) || !make_dense_map(&m[3], q, (int64_t)n_tokens * g.H, 1, 1))
+        !make_dense_map(&m[2], q, (int64_t)n_tokens * g.H, 1, g.hpg) || !make_dense_map(&m[3], q, (int64_t)n_tokens * g.H, 1, g.hpg & -g.hpg))
       return QSA_ERR_CUDA;
   }
-  auto run = [&](bool is_wide) {
-    return [&, is_wide](const DenseTable& t, const DenseSplits& sp) -> qsa_status_t {
+  for (const DenseGroup& d : dense_groups(g, tc, PAGED, segs, n)) {
+    const bool is_wide = d.form == DenseForm::kWide;
+    const qsa_status_t r = for_each_dense(g, d.segs, d.kind, [&](const DenseTable& t, const DenseSplits& sp) -> qsa_status_t {
       cudaError_t e;
-      if (tc)
+      if (d.form == DenseForm::kDecode)
+        e = launch_dense_decode(t, a, st);
+      else if (tc)
         e = is_wide ? launch_dense_tc<2, PAGED>(t, m, a, st) : launch_dense_tc<1, PAGED>(t, m, a, st);
       else
         e = is_wide ? launch_dense_simt<dense_simt::kRowsWide, PAGED>(g, t, kv, q, o, lse, part, st)
@@ -321,10 +350,10 @@ qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int
         e = tc ? launch_dense_combine<__nv_bfloat16>(g, t, sp, part, o, lse, st)
                : launch_dense_combine<float>(g, t, sp, part, o, lse, st);
       return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
-    };
-  };
-  const qsa_status_t r = for_each_dense(g, wide, kw, run(true));
-  return r != QSA_OK ? r : for_each_dense(g, narrow, kn, run(false));
+    });
+    if (r != QSA_OK) return r;
+  }
+  return QSA_OK;
 }
 
 // ------------------------------------------------------------------ backward
@@ -462,13 +491,13 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
   float* lse2_h = (float*)(ws + p.off_lse2);
   float* delta_h = (float*)(ws + p.off_delta_h);
   int32_t* flags = (int32_t*)(ws + p.off_flags);
-  CUtensorMap mq, mo, mk, mv, tq, to, rq, ro;      // boxes of 64 rows; Q and dO by token and by row
+  CUtensorMap mq, mo, mk, mv, tq, to, rq, ro;      // boxes of 64 rows; Q and dO by whole tokens and parts of one
   const int64_t rows = (int64_t)n_tokens * g.H;
   if (rows > INT32_MAX - 512) return QSA_ERR_UNSUPPORTED;
   if (!make_dense_map(&mq, a.q, n_tokens, g.H, 64) || !make_dense_map(&mo, a.dout, n_tokens, g.H, 64) ||
       !make_dense_map(&mk, a.k, n_tokens, g.G, 64) || !make_dense_map(&mv, a.v, n_tokens, g.G, 64) ||
       !make_dense_map(&tq, a.q, rows, 1, g.hpg) || !make_dense_map(&to, a.dout, rows, 1, g.hpg) ||
-      !make_dense_map(&rq, a.q, rows, 1, 1) || !make_dense_map(&ro, a.dout, rows, 1, 1))
+      !make_dense_map(&rq, a.q, rows, 1, g.hpg & -g.hpg) || !make_dense_map(&ro, a.dout, rows, 1, g.hpg & -g.hpg))
     return QSA_ERR_CUDA;
   if (cudaMemsetAsync(flags, 0, p.flag_bytes, st) != cudaSuccess) return QSA_ERR_CUDA;
   qsa_status_t r = for_each_table(

@@ -466,30 +466,24 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       tc_fence_after();
       const bool whole = p.part < 0;
       const float f = whole && M != kDv ? a.scale : 1.f;
-      float* pdst = whole ? nullptr
-                          : a.part + ((int64_t)p.part * t.prows + rank * 128 + li) * dense::kPartFloats + half * 128;
-      __nv_bfloat16* orow = a.out + at * kHeadDim + half * 128;
+      const int row_q = (int)rank * 128 + quad * 32 + (lane & ~3);   // first row of this lane's quad
+      float* part_q = whole ? nullptr : a.part + ((int64_t)p.part * t.prows + row_q) * dense::kPartFloats;
+      int64_t at_q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) at_q[j] = __shfl_sync(0xffffffffu, active ? at : -1, (lane & ~3) + j);
 #pragma unroll 1
-      for (int piece = 0; piece < 8; ++piece) {
-        float o[16];
-        tmem_ld16(lane_addr + kTmemD + half * 128 + piece * 16, o);
-        tmem_wait_ld();
-        if (!active) continue;
-        if (whole) {
-          uint4 v[2];
-          uint32_t* u = reinterpret_cast<uint32_t*>(v);
+      for (int piece = 0; piece < 4; ++piece) {
+        float o[32];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(o[2 * i] * f, o[2 * i + 1] * f);
-          *reinterpret_cast<uint4*>(orow + piece * 16) = v[0];
-          *reinterpret_cast<uint4*>(orow + piece * 16 + 8) = v[1];
-        } else {
+        for (int k = 0; k < 32; k += 16) {
+          float v[16];
+          tmem_ld16(lane_addr + kTmemD + half * 128 + piece * 32 + k, v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(pdst + piece * 16 + 4 * i) =
-                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 16; ++i) o[k + i] = v[i];
         }
+        tmem_wait_ld();
+        store_cols32(o, f, whole ? a.out : nullptr, part_q, at_q, half * 128 + piece * 32, lane);
       }
-      __syncwarp();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_leader<2>(&ctl.o_free);

@@ -1,0 +1,270 @@
+// dense_decode.cuh -- dense attention of single new tokens over a paged cache,
+// bf16: one token's heads of a KV group against all its keys.
+//
+// The work is the HBM read of K and V once: 12 heads make 12 flop per byte and
+// operand, beyond what CUDA cores add up at HBM rate, a fifth of what
+// mma.sync gives.  tcgen05 tiles would be a tenth full and tie the SM's loads
+// to one chain of barriers (a chunk's products, softmax and the slots' reuse took
+// 1.8 us for 64 KiB on them: 2.9 TB/s); here eight warps each stream keys of
+// their own, 16 at a time, through three 8 KiB slots, with no barrier between
+// them, so that 128 KiB are in flight per SM all the time:
+//   S[16 heads, 16 keys] = Q K^T   32 mma.m16n8k16, K by ldmatrix
+//   O[16 heads, 256]    += P V     32 mma.m16n8k16, V by ldmatrix.trans
+// A warp keeps its own maximum (moved only when a tile exceeds it by more than 8 in
+// log2 units), sum and O (128 registers); at the end of a piece the warps join
+// through shared memory.  P is rounded to bf16 for its product, the row sum
+// adds the unrounded values.  Tables, pieces and their join: dense.cuh, rows =
+// 16 and a chunk of 128 keys, 16 for each warp.
+//
+// A token's keys are all visible to it, so nothing is masked but keys beyond
+// the sequence and of pages out of range: neither is read (zeros are filled
+// in), their scores are -inf.
+#pragma once
+#include "dense.cuh"
+#include "dense_simt.cuh"
+#include "dense_tc.cuh"
+
+namespace qsa {
+namespace dense_decode {
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kTile = 16;                             // keys of a warp's step
+constexpr int kRows = 16, kKeys = kWarps * kTile;     // of a unit, of a chunk
+constexpr int kSlotBytes = kTile * kHeadDim * 2, kSlots = 3;
+constexpr int kOffQ = kWarps * kSlots * kSlotBytes;
+constexpr int kOffStat = kOffQ + kRows * kHeadDim * 2;       // maxima and sums of the warps' rows
+constexpr int kSmemBytes = kOffStat + 2 * kWarps * kRows * 4;
+constexpr int kOLd = kHeadDim + 8;                    // floats between a warp's O rows in shared memory
+static_assert(kRows * kOLd * 4 <= kSlots * kSlotBytes, "O of a warp over its slots");
+}  // namespace dense_decode
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__global__ void __launch_bounds__(dense_decode::kThreads, 1)
+    dense_decode_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseTcArgs a) {
+  using namespace dense_decode;
+  using namespace sm100;
+  extern __shared__ __align__(1024) unsigned char smem_1k[];
+  unsigned char* const smem = smem_1k;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = smem_u32(smem) + warp * kSlots * kSlotBytes, q_addr = smem_u32(smem + kOffQ);
+  float* const o_s = reinterpret_cast<float*>(smem + warp * kSlots * kSlotBytes);
+  float* const m_s = reinterpret_cast<float*>(smem + kOffStat);        // [warp][row]
+  float* const l_s = m_s + kWarps * kRows;
+  const float tau2 = a.scale * 1.4426950408889634f;
+  // 16-byte piece `piece` of line r of a tile, swizzled so that eight lines of one piece hit all banks
+  auto at = [](int r, int piece) { return (uint32_t)(r * (kHeadDim * 2) + ((piece ^ (r & 7)) << 4)); };
+  const int mi = lane >> 3, ml = lane & 7;              // this lane's matrix and line of an ldmatrix.x4
+  pdl_wait();
+  pdl_trigger();
+  DenseWalk walk;
+  walk.init(t, blockIdx.x);
+  DensePiece p;
+  DenseUnit x;
+  while (walk.next(t, p, x)) {
+    const int64_t head0 = (int64_t)t.q_offset[x.si] * a.H + x.grp * t.hpg;
+    // Q, rows beyond the group's heads zero
+    for (int i = threadIdx.x; i < kRows * 32; i += kThreads) {
+      const int r = i >> 5, c = i & 31;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < x.nrows) v = *reinterpret_cast<const uint4*>(a.q + (head0 + r) * kHeadDim + c * 8);
+      *reinterpret_cast<uint4*>(smem + kOffQ + at(r, c)) = v;
+    }
+    // this warp's tiles: keys (p.c0 + i) * 128 + 16 warp, of those that hold a key
+    const int32_t key0 = p.c0 * kKeys + warp * kTile;
+    const int n = min(p.c1 - p.c0, max(0, (x.kv_len - key0 + kKeys - 1) / kKeys));
+    // rows of the tiles, looked up for 32 tiles at a time (-1: page out of range)
+    int32_t look0 = -32;
+    int64_t my_row = -1;
+    auto tile_row = [&](int i) -> int64_t {               // first cache row of tile i (lanes agree)
+      if (i - look0 >= 32) {
+        look0 = i;
+        const int32_t key = key0 + (i + lane) * kKeys;
+        my_row = -1;
+        if (i + lane < n) {
+          const int32_t pi = key / a.kv.page_tokens;
+          const int32_t page = a.kv.table[(int64_t)t.slot[x.si] * a.kv.max_pages + pi];
+          if (page >= 0 && page < a.kv.n_pages)
+            my_row = ((int64_t)page * t.G + x.grp) * a.kv.page_tokens + (key - pi * a.kv.page_tokens);
+          else
+            report_error(kErrBadIndex);
+        }
+      }
+      return __shfl_sync(0xffffffffu, my_row, i - look0);
+    };
+    // item 2 i: K of tile i, 2 i + 1: V; slot = item % 3.  The row of a tile
+    // is kept for its V and (below) its scores.
+    int64_t row_k = -1, row_v = -1;                       // of the last K / V issued
+    auto load = [&](int item) {
+      const int i = item >> 1;
+      if (i < n) {
+        const bool is_v = item & 1;
+        const int64_t row = is_v ? row_v : tile_row(i);
+        if (!is_v) row_k = row;
+        const __nv_bfloat16* base = (const __nv_bfloat16*)(is_v ? a.kv.v : a.kv.k);
+        const int valid = row < 0 ? 0 : min(kTile, x.kv_len - (key0 + i * kKeys));
+        const __nv_bfloat16* src = base + (valid > 0 ? row : 0) * kHeadDim + lane * 8;
+        const uint32_t dst = ring + (item % kSlots) * kSlotBytes;
+#pragma unroll
+        for (int r = 0; r < kTile; ++r)
+          cp_async16(dst + at(r, lane), r < valid ? src + r * kHeadDim : src, r < valid ? 16u : 0u);
+      }
+      cp_async_commit();
+    };
+    float o[32][4];
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};      // rows lane/4 and lane/4 + 8
+    load(0);
+    row_v = row_k;
+    load(1);
+    int64_t row_now = row_k;
+    load(2);
+    __syncthreads();                                      // Q written
+    for (int i = 0; i < n; ++i) {
+      // ---- S of tile i
+      cp_async_wait<2>();
+      __syncwarp();
+      float s[2][2][4] = {};                              // [k-step parity][keys 0-7, 8-15]
+      const uint32_t ks = ring + ((2 * i) % kSlots) * kSlotBytes;
+#pragma unroll
+      for (int kk = 0; kk < 16; ++kk) {
+        uint32_t qa[4], kb[4];
+        ldmatrix_x4(q_addr + at((mi & 1) * 8 + ml, 2 * kk + (mi >> 1)), qa);
+        ldmatrix_x4(ks + at((mi >> 1) * 8 + ml, 2 * kk + (mi & 1)), kb);
+        mma_m16n8k16(s[kk & 1][0], qa, kb[0], kb[1]);
+        mma_m16n8k16(s[kk & 1][1], qa, kb[2], kb[3]);
+      }
+      __syncwarp();
+      row_v = row_k;                                      // of tile i + 1
+      const bool bad = row_now < 0;
+      row_now = row_k;
+      load(2 * i + 3);                                    // V of tile i + 1 over K of tile i
+      // ---- softmax: this thread's keys are 8 j + 2 (lane % 4), + 1
+      const int left = bad ? 0 : x.kv_len - (key0 + i * kKeys);
+      uint32_t pa[4];
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float v = s[0][j][k] + s[1][j][k];
+          s[0][j][k] = 8 * j + 2 * (lane & 3) + (k & 1) < left ? v * tau2 : -INFINITY;
+          mx[k >> 1] = fmaxf(mx[k >> 1], s[0][j][k]);
+        }
+      float f[2] = {1.f, 1.f};
+      bool need = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        if (mx[r] > m[r] + 8.f) {                         // false while both are -inf
+          if (m[r] != -INFINITY) {
+            f[r] = exp2f(m[r] - mx[r]);
+            need = true;
+          }
+          m[r] = mx[r];
+        }
+      }
+      if (__any_sync(0xffffffffu, need)) {
+        l[0] *= f[0];
+        l[1] *= f[1];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          o[j][0] *= f[0];
+          o[j][1] *= f[0];
+          o[j][2] *= f[1];
+          o[j][3] *= f[1];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float mb = m[k >> 1] == -INFINITY ? 0.f : m[k >> 1];
+          e[k] = ex2_approx(s[0][j][k] - mb);
+          l[k >> 1] += e[k];
+        }
+        pa[2 * j] = pack_bf16x2(e[0], e[1]);
+        pa[2 * j + 1] = pack_bf16x2(e[2], e[3]);
+      }
+      // ---- O += P V of tile i
+      cp_async_wait<2>();
+      __syncwarp();
+      const uint32_t vs = ring + ((2 * i + 1) % kSlots) * kSlotBytes;
+#pragma unroll
+      for (int jj = 0; jj < 16; ++jj) {
+        uint32_t vb[4];
+        ldmatrix_x4_trans(vs + at((mi & 1) * 8 + ml, 2 * jj + (mi >> 1)), vb);
+        mma_m16n8k16(o[2 * jj], pa, vb[0], vb[1]);
+        mma_m16n8k16(o[2 * jj + 1], pa, vb[2], vb[3]);
+      }
+      __syncwarp();
+      load(2 * i + 4);                                    // K of tile i + 2 over V of tile i
+    }
+    // ---- join the warps
+    cp_async_wait_all();
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if ((lane & 3) == 0) {
+        m_s[warp * kRows + 8 * r + (lane >> 2)] = m[r];
+        l_s[warp * kRows + 8 * r + (lane >> 2)] = l[r];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      float* dst = o_s + (lane >> 2) * kOLd + 8 * j + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(dst) = make_float2(o[j][0], o[j][1]);
+      *reinterpret_cast<float2*>(dst + 8 * kOLd) = make_float2(o[j][2], o[j][3]);
+    }
+    __syncthreads();
+    const int d = threadIdx.x;                            // dim
+    for (int r = 0; r < x.nrows; ++r) {
+      float mr = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, m_s[w * kRows + r]);
+      float lr = 0.f, v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = m_s[w * kRows + r];
+        const float f = mw == -INFINITY ? 0.f : exp2f(mw - mr);
+        lr = fmaf(f, l_s[w * kRows + r], lr);
+        v = fmaf(f, reinterpret_cast<const float*>(smem + w * kSlots * kSlotBytes)[r * kOLd + d], v);
+      }
+      if (p.part < 0) {
+        a.o[(head0 + r) * kHeadDim + d] = __float2bfloat16_rn(lr != 0.f ? v / lr : 0.f);
+        if (d == 0 && a.lse) a.lse[head0 + r] = lr != 0.f ? (mr + log2f(lr)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        float* dst = a.part + ((int64_t)p.part * t.prows + r) * dense::kPartFloats;
+        dst[d] = v;
+        if (d == 0) {
+          dst[kHeadDim] = mr;
+          dst[kHeadDim + 1] = lr;
+        }
+      }
+    }
+    __syncthreads();                                      // shared memory free for the next piece
+  }
+}
+
+}  // namespace qsa

@@ -117,8 +117,8 @@ __device__ __forceinline__ void dense_arrive(uint64_t* bar) {
 // Loads rows row0 .. row0+n-1 (n <= 128) of a unit's segment and group into a
 // 128-byte swizzled tile, completing n * 512 bytes on rank 0's barrier: a token's
 // heads are consecutive rows of the token-major array, so a whole token is one
-// box per 64 dims, and the rows of tokens cut by the tile's ends are boxes of one
-// row.  By TMA, since the tensor cores' operand reads leave other shared-memory
+// box per 64 dims; tokens cut by the tile's ends come in boxes of as many rows as
+// divide both 128 and the group's heads.  By TMA, since the tensor cores' operand reads leave other shared-memory
 // writes little room: cp.async took 25 us for 128 KiB under them.  (The swizzle
 // goes by address bits, so boxes may start at any 128-byte line.)
 template <int CG>
@@ -132,10 +132,63 @@ __device__ __forceinline__ void load_q_rows(unsigned char* tile, const CUtensorM
     sm100::tma_load_2d_leader<CG>(tile + (i & 3) * 16384 + r * 128, tokens, (i & 3) * 64,
                                   (int32_t)dense_q_row(t, x, row0 + r, H), bar);
   }
-  for (int i = lane; i < 4 * (lead + tail); i += 32) {
-    const int e = i >> 2, r = e < lead ? e : n - tail + (e - lead);
+  const int step = t.hpg & -t.hpg;
+  for (int i = lane; i < 4 * (lead + tail) / step; i += 32) {
+    const int e = (i >> 2) * step, r = e < lead ? e : n - tail + (e - lead);
     sm100::tma_load_2d_leader<CG>(tile + (i & 3) * 16384 + r * 128, rows, (i & 3) * 64,
                                   (int32_t)dense_q_row(t, x, row0 + r, H), bar);
+  }
+}
+
+// Four lanes' 4 x 4 blocks of 16 bytes transposed: lane k of a quad then holds
+// piece k of the four lanes' rows.
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4], int lane) {
+  auto swap = [&](uint4& lo, uint4& hi, int bit) {
+    const bool up = lane & bit;
+    uint4 s = up ? lo : hi;
+    s.x = __shfl_xor_sync(0xffffffffu, s.x, bit);
+    s.y = __shfl_xor_sync(0xffffffffu, s.y, bit);
+    s.z = __shfl_xor_sync(0xffffffffu, s.z, bit);
+    s.w = __shfl_xor_sync(0xffffffffu, s.w, bit);
+    if (up) lo = s; else hi = s;
+  };
+  swap(v[0], v[1], 1);
+  swap(v[2], v[3], 1);
+  swap(v[0], v[2], 2);
+  swap(v[1], v[3], 2);
+}
+
+// Stores 32 result columns (from `col` on) of the warp's 32 rows: out != null:
+// times f, rounded, to the rows at[] (of this lane's quad, in heads; < 0: not
+// stored); else as they are to the partial rows from `part` (the quad's first).
+// Transposed first, so that a store instruction touches 8 rows, not 32: the
+// epilogue's stores took 10 cycles per row and instruction under the MMAs.
+__device__ __forceinline__ void store_cols32(const float (&o)[32], float f, __nv_bfloat16* out, float* part,
+                                             const int64_t (&at)[4], int col, int lane) {
+  uint4 v[4];
+  if (out) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      v[c] = make_uint4(pack_bf16x2(o[8 * c] * f, o[8 * c + 1] * f), pack_bf16x2(o[8 * c + 2] * f, o[8 * c + 3] * f),
+                        pack_bf16x2(o[8 * c + 4] * f, o[8 * c + 5] * f),
+                        pack_bf16x2(o[8 * c + 6] * f, o[8 * c + 7] * f));
+    quad_transpose(v, lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (at[j] >= 0) *reinterpret_cast<uint4*>(out + at[j] * kHeadDim + col + 8 * (lane & 3)) = v[j];
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        v[c] = make_uint4(__float_as_uint(o[16 * h + 4 * c]), __float_as_uint(o[16 * h + 4 * c + 1]),
+                          __float_as_uint(o[16 * h + 4 * c + 2]), __float_as_uint(o[16 * h + 4 * c + 3]));
+      quad_transpose(v, lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (at[j] >= 0)
+          *reinterpret_cast<uint4*>(part + j * dense::kPartFloats + col + 16 * h + 4 * (lane & 3)) = v[j];
+    }
   }
 }
 
@@ -513,13 +566,21 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       if (warp_active) {
         const bool whole = p.part < 0;
         const float inv = !whole ? 1.f : lt != 0.f ? 1.f / lt : 0.f;    // lt = 0: no key at all
-        float* pdst = whole ? nullptr
-                            : a.part + ((int64_t)p.part * t.prows + rank * 128 + li) * dense::kPartFloats + half * 128;
-        __nv_bfloat16* orow = a.o + at * kHeadDim + half * 128;
+        const int row_q = (int)rank * 128 + quad * 32 + (lane & ~3);   // first row of this lane's quad
+        float* part_q = whole ? nullptr : a.part + ((int64_t)p.part * t.prows + row_q) * dense::kPartFloats;
+        int64_t at_q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) at_q[j] = __shfl_sync(0xffffffffu, active ? at : -1, (lane & ~3) + j);
 #pragma unroll 1
-        for (int piece = 0; piece < 8; ++piece) {
-          float o[16];
-          tmem_ld16(lane_addr + kTmemO + half * 128 + piece * 16, o);
+        for (int piece = 0; piece < 4; ++piece) {
+          float o[32];
+#pragma unroll
+          for (int k = 0; k < 32; k += 16) {
+            float v[16];
+            tmem_ld16(lane_addr + kTmemO + half * 128 + piece * 32 + k, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[k + i] = v[i];
+          }
           tmem_wait_ld();
           if (any_nf) {                                      // keys kept out of the product
 #pragma unroll 1
@@ -532,43 +593,25 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
                 const int64_t off = kv_row<PAGED>(a.kv, t, x.si, x.grp, key);
                 if (off < 0) continue;
                 const __nv_bfloat16* kr = (const __nv_bfloat16*)a.kv.k + off;
-                const __nv_bfloat16* vr = (const __nv_bfloat16*)a.kv.v + off + half * 128 + piece * 16;
+                const __nv_bfloat16* vr = (const __nv_bfloat16*)a.kv.v + off + half * 128 + piece * 32;
                 float sc = 0.f;
 #pragma unroll 1
                 for (int d = 0; d < kHeadDim; ++d)
                   sc = fmaf(__bfloat162float(a.q[at * kHeadDim + d]), __bfloat162float(kr[d]), sc);
                 const float pw = ex2_approx(fmaf(sc, tau2, m == -INFINITY ? 0.f : -m));
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = fmaf(pw, __bfloat162float(vr[i]), o[i]);
+                for (int i = 0; i < 32; ++i) o[i] = fmaf(pw, __bfloat162float(vr[i]), o[i]);
               }
             }
             __syncwarp();
           }
-          if (active) {
-            if (whole) {
-              uint4 v0, v1;
-              v0.x = pack_bf16x2(o[0] * inv, o[1] * inv);
-              v0.y = pack_bf16x2(o[2] * inv, o[3] * inv);
-              v0.z = pack_bf16x2(o[4] * inv, o[5] * inv);
-              v0.w = pack_bf16x2(o[6] * inv, o[7] * inv);
-              v1.x = pack_bf16x2(o[8] * inv, o[9] * inv);
-              v1.y = pack_bf16x2(o[10] * inv, o[11] * inv);
-              v1.z = pack_bf16x2(o[12] * inv, o[13] * inv);
-              v1.w = pack_bf16x2(o[14] * inv, o[15] * inv);
-              *reinterpret_cast<uint4*>(orow + piece * 16) = v0;
-              *reinterpret_cast<uint4*>(orow + piece * 16 + 8) = v1;
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(pdst + piece * 16 + 4 * i) =
-                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            }
-          }
+          store_cols32(o, inv, whole ? a.o : nullptr, part_q, at_q, half * 128 + piece * 32, lane);
         }
         if (active && half == 0) {
           if (!whole) {
-            pdst[kHeadDim] = m;
-            pdst[kHeadDim + 1] = lt;
+            float* st = part_q + (lane & 3) * dense::kPartFloats + kHeadDim;
+            st[0] = m;
+            st[1] = lt;
           } else if (a.lse) {
             a.lse[at] = lt != 0.f ? (m + log2f(lt)) * 0.6931471805599453f : -INFINITY;
           }

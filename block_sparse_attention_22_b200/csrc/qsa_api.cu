@@ -1001,7 +1001,7 @@ QSA_API size_t qsa_workspace_size(const qsa_config_t* cfg, const qsa_segment_t* 
     case QSA_OP_PROMPT_ATTN: {
       size_t ws = SIZE_MAX;
       if (guarded([&]() -> qsa_status_t {
-            ws = dense_fwd_ws(g, cfg->dtype == QSA_DTYPE_BF16, segs, n_segs);
+            ws = dense_fwd_ws(g, cfg->dtype == QSA_DTYPE_BF16, op == QSA_OP_PAGED_ATTN, segs, n_segs);
             return QSA_OK;
           }) != QSA_OK)
         return SIZE_MAX;
