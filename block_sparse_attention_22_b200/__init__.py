@@ -279,9 +279,10 @@ def _one_device(where, *tensors):
             continue
         if not t.is_contiguous():
             raise ValueError(f"{where}: a tensor is not contiguous")
-        if dev is not None and t.device != dev:
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
             raise ValueError(f"{where}: tensors on {dev} and {t.device}")
-        dev = t.device
     if dev is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
         raise ValueError(f"{where}: tensors on {dev}, but the current device is {torch.cuda.current_device()}")
     return dev
@@ -290,27 +291,31 @@ def _one_device(where, *tensors):
 def _shaped(where, cfg, n_tokens, pages=None, **tensors):
     """Checks the dtype and shape of token-major tensors: q-like names hold
     n_q_heads rows per token, k/v-like names n_kv_groups; lse is fp32."""
-    want = "torch.bfloat16" if cfg.dtype == QSA_DTYPE_BF16 else "torch.float32"
+    import torch
+    want = torch.bfloat16 if cfg.dtype == QSA_DTYPE_BF16 else torch.float32
+    groups, dim = cfg.n_kv_groups, cfg.head_dim
     if pages is not None:
         pk = pages.tensors[0]
-        if str(pk.dtype) != want or pk.shape[1] != cfg.n_kv_groups or pk.shape[3] != cfg.head_dim:
-            raise ValueError(f"{where}: pages are {tuple(pk.shape)} {pk.dtype}, not {want} with "
-                             f"{cfg.n_kv_groups} groups of {cfg.head_dim}")
+        if pk.dtype != want or pk.shape[1] != groups or pk.shape[3] != dim:
+            raise ValueError(f"{where}: pages are {tuple(pk.shape)} {pk.dtype}, not {want} with {groups} groups "
+                             f"of {dim}")
+    kv, qo, stat = (n_tokens, groups, dim), (n_tokens, cfg.n_q_heads, dim), (n_tokens, cfg.n_q_heads)
     for name, t in tensors.items():
         if t is None:
             continue
-        heads = cfg.n_kv_groups if name in ("k", "v", "dk", "dv") else cfg.n_q_heads
-        shape = (n_tokens, heads) if name == "lse" else (n_tokens, heads, cfg.head_dim)
-        dtype = "torch.float32" if name == "lse" else want
-        if tuple(t.shape) != shape or str(t.dtype) != dtype:
+        shape = kv if name in ("k", "v", "dk", "dv") else stat if name == "lse" else qo
+        dtype = torch.float32 if name == "lse" else want
+        if t.shape != shape or t.dtype != dtype:
             raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype}, not {shape} {dtype}")
 
 
 def _token_stride(where, name, t) -> int:
     """Elements between a [T, heads, D] tensor's tokens; its heads are dense."""
-    if t.shape[0] and (t.stride(2) != 1 or t.stride(1) != t.shape[2]):
+    n, heads, dim = t.shape
+    ld, sh, sd = t.stride()
+    if n and (sd != 1 or sh != dim):
         raise ValueError(f"{where}: the heads of a token of {name} are not contiguous")
-    return max(t.stride(0), t.shape[1] * t.shape[2]) if t.shape[0] <= 1 else t.stride(0)
+    return max(ld, heads * dim) if n <= 1 else ld
 
 
 def qsa_append_kv(cfg, pages, segs, n_tokens, k, v, q=None, q_out=None, stream=None):

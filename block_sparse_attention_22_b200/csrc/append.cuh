@@ -15,6 +15,7 @@ namespace append {
 constexpr int kThreads = 256;
 constexpr int kMaxHalf = kHeadDim / 2;      // rotated pairs at rope_fraction 1
 constexpr int kUnroll = 4;                  // vectors a warp loads before it stores the first
+constexpr int kTokens = 8;                  // tokens of a block, when there are enough for every SM
 }  // namespace append
 
 struct AppendArgs {
@@ -72,81 +73,109 @@ template <> struct Vec8<float> {
   }
 };
 
-// One block per token.  A token's G keys, H queries (when given) and G values
-// are vectors of 256 dims, one warp each, 8 dims per lane; warp w takes
-// vectors w, w + 8, ...  The first loads are in flight while the block's first
-// `half` threads form the token's cosines and sines.
-template <typename T>
+// A block takes TPB tokens.  A token's G keys, H queries (when given) and G
+// values are vectors of 256 dims, one warp each, 8 dims per lane.  The kernel
+// is a copy, bound by HBM; what it waits for is the fp64 sine and cosine, so with
+// eight tokens at 32 rotated pairs every thread forms one of them while the
+// warps' first loads are in flight.  (One token per block left seven of eight warps
+// idle meanwhile: 44 us for a 4096-token chunk of 24 + 2 + 2 heads, 117 MB.)  Few
+// tokens take a block each, for the latency.  A pair's halves are `half` / 8 lanes
+// apart; where that is no whole number they meet in shared memory.
+template <typename T, int TPB>
 __global__ void __launch_bounds__(append::kThreads)
-    append_kernel(Geo g, SegTable st, AppendArgs a) {
+    append_kernel(Geo g, const __grid_constant__ SegTable st, const __grid_constant__ AppendArgs a) {
   using namespace append;
-  __shared__ float cs[kMaxHalf], sn[kMaxHalf];
-  __shared__ float row[kThreads / 32][kHeadDim];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kWarps = kThreads / 32;
-  const int si = find_segment(st, (int)blockIdx.x);
-  const int j = (int)blockIdx.x - st.item0[si];
-  const int64_t tok = (int64_t)st.q_offset[si] + j;
-  const int64_t pos = (int64_t)st.pos0[si] + j;
+  __shared__ float cs[TPB][kMaxHalf], sn[TPB][kMaxHalf];
+  __shared__ float row[kWarps][kHeadDim];
+  __shared__ int64_t tok_s[TPB], pos_s[TPB], cache_s[TPB];      // cache row of group 0; -1: not stored
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = (int)blockIdx.x * TPB, ntok = min(TPB, st.item0[st.n] - first);
   pdl_wait();
   pdl_trigger();
+  if (threadIdx.x < ntok) {
+    const int item = first + (int)threadIdx.x;
+    const int si = find_segment(st, item);
+    const int j = item - st.item0[si];
+    const int32_t pos = st.pos0[si] + j, pi = pos / a.page_tokens;
+    const int32_t page = a.table[(int64_t)st.slot[si] * a.max_pages + pi];
+    const bool ok = page >= 0 && page < a.n_pages;
+    if (!ok) report_error(kErrBadIndex);
+    tok_s[threadIdx.x] = (int64_t)st.q_offset[si] + j;
+    pos_s[threadIdx.x] = pos;
+    cache_s[threadIdx.x] = ok ? (int64_t)page * g.G * a.page_tokens + (pos - pi * a.page_tokens) : -1;
+  }
+  __syncthreads();
   const int nq = a.q ? g.H : 0;
-  const int n_rot = g.G + nq, n_vec = n_rot + g.G;
-  const int32_t page = a.table[(int64_t)st.slot[si] * a.max_pages + pos / a.page_tokens];
-  const bool stored = page >= 0 && page < a.n_pages;
-  if (!stored && threadIdx.x == 0) report_error(kErrBadIndex);
-  const int64_t cache_row = (int64_t)page * g.G * a.page_tokens + pos % a.page_tokens;   // of group 0
-  auto src = [&](int v) -> const T* {
+  const int n_rot = g.G + nq, n_vec = n_rot + g.G, total = ntok * n_vec;
+  auto src = [&](int i, int v) -> const T* {
+    const int64_t tok = tok_s[i];
     if (v < g.G) return (const T*)a.k + tok * a.ld_k + (int64_t)v * kHeadDim;
     if (v < n_rot) return (const T*)a.q + tok * a.ld_q + (int64_t)(v - g.G) * kHeadDim;
     return (const T*)a.v + tok * a.ld_v + (int64_t)(v - n_rot) * kHeadDim;
   };
-  auto dst = [&](int v) -> T* {          // null: not stored
-    if (v >= g.G && v < n_rot) return (T*)a.q_out + (tok * g.H + (v - g.G)) * kHeadDim;
-    if (!stored) return nullptr;
+  auto dst = [&](int i, int v) -> T* {   // null: not stored
+    if (v >= g.G && v < n_rot) return (T*)a.q_out + (tok_s[i] * g.H + (v - g.G)) * kHeadDim;
+    if (cache_s[i] < 0) return nullptr;
     const bool is_k = v < g.G;
-    const int64_t r = cache_row + (int64_t)(is_k ? v : v - n_rot) * a.page_tokens;
+    const int64_t r = cache_s[i] + (int64_t)(is_k ? v : v - n_rot) * a.page_tokens;
     return (T*)(is_k ? a.kp : a.vp) + r * kHeadDim;
   };
+  const bool by_lane = (a.half & 7) == 0;
+  const int apart = a.half >> 3;         // lanes between a pair's halves
   bool angles = false;
-  for (int v0 = warp; v0 < n_vec || !angles; v0 += kWarps * kUnroll) {
+  for (int w0 = warp; w0 < total || !angles; w0 += kWarps * kUnroll) {
     Vec8<T> x[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (v0 + u * kWarps < n_vec) x[u].load(src(v0 + u * kWarps) + lane * 8);
+    for (int u = 0; u < kUnroll; ++u) {
+      const int w = w0 + u * kWarps, i = w / n_vec;
+      if (w < total) x[u].load(src(i, w - i * n_vec) + lane * 8);
+    }
     if (!angles) {
-      if (threadIdx.x < a.half) {
+      for (int k = threadIdx.x; k < ntok * a.half; k += kThreads) {
+        const int i = k / a.half, p = k - i * a.half;
         double s, c;
-        sincos((double)pos * a.theta[threadIdx.x], &s, &c);
-        cs[threadIdx.x] = (float)c;
-        sn[threadIdx.x] = (float)s;
+        sincos((double)pos_s[i] * a.theta[p], &s, &c);
+        cs[i][p] = (float)c;
+        sn[i][p] = (float)s;
       }
       __syncthreads();
       angles = true;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int v = v0 + u * kWarps;
-      if (v >= n_vec) break;
-      T* out = dst(v);
-      if (v < n_rot) {                   // rotate: a pair's halves may sit in different lanes
-        float f[8];
+      const int w = w0 + u * kWarps;
+      if (w >= total) break;
+      const int i = w / n_vec, v = w - i * n_vec;
+      T* out = dst(i, v);
+      if (v < n_rot) {
+        float f[8], y[8];                // this lane's dims and their partners
         x[u].get(f);
-        __syncwarp();
+        if (by_lane) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) row[warp][lane * 8 + i] = f[i];
-        __syncwarp();
+          for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, f[k], lane < apart ? lane + apart : lane - apart);
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) row[warp][lane * 8 + k] = f[k];
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int d = lane * 8 + k;
+            y[k] = d < a.half ? row[warp][d + a.half] : d < 2 * a.half ? row[warp][d - a.half] : 0.f;
+          }
+        }
         if (lane * 8 < 2 * a.half) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int d = lane * 8 + i;
+          for (int k = 0; k < 8; ++k) {
+            const int d = lane * 8 + k;
             float oa, ob;
             if (d < a.half) {
-              rope_pair(f[i], row[warp][d + a.half], cs[d], sn[d], oa, ob);
-              f[i] = oa;
+              rope_pair(f[k], y[k], cs[i][d], sn[i][d], oa, ob);
+              f[k] = oa;
             } else if (d < 2 * a.half) {
-              rope_pair(row[warp][d - a.half], f[i], cs[d - a.half], sn[d - a.half], oa, ob);
-              f[i] = ob;
+              rope_pair(y[k], f[k], cs[i][d - a.half], sn[i][d - a.half], oa, ob);
+              f[k] = ob;
             }
           }
           x[u].set(f);

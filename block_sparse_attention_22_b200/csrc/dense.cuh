@@ -190,4 +190,75 @@ __global__ void __launch_bounds__(128)
   if (lse && lane == 0) lse[at] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// The same by a block of eight warps per row, for units in many pieces (decode
+// of a long sequence: 74 of them): the pieces' statistics are read at once, the
+// warps add up every eighth piece and then join in order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    dense_combine_many_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseSplits sp,
+                              const float* part, T* o, float* lse, int H) {
+  __shared__ float w_s[dense::kMaxGrid], red[8], acc_s[8][kHeadDim];
+  __shared__ int64_t at_s[dense::kMaxGrid];
+  pdl_wait();
+  pdl_trigger();
+  const int u = sp.unit[blockIdx.x], c0 = sp.first[blockIdx.x], n = sp.last[blockIdx.x] - c0 + 1;
+  const DenseUnit x = dense_unit(t, u);
+  const int r = blockIdx.y;
+  if (r >= x.nrows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto block_reduce = [&](float v, bool is_max) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, v, off);
+      v = is_max ? fmaxf(v, y) : v + y;
+    }
+    __syncthreads();
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v = is_max ? fmaxf(v, red[k]) : v + red[k];
+    return v;
+  };
+  float mp = -INFINITY, lp = 0.f;
+  if (threadIdx.x < n) {
+    const int slot = dense_piece_slot(t, u, c0 + (int)threadIdx.x);
+    const int64_t at = ((int64_t)slot * t.prows + r) * dense::kPartFloats;
+    at_s[threadIdx.x] = at;
+    if (slot >= 0) {
+      mp = part[at + kHeadDim];
+      lp = part[at + kHeadDim + 1];
+    }
+  }
+  const float m = block_reduce(mp, true);
+  const float w = mp == -INFINITY ? 0.f : exp2f(mp - m);
+  if (threadIdx.x < n) w_s[threadIdx.x] = w;
+  const float l = block_reduce(w * lp, false);          // its barriers also order w_s, at_s
+  float acc[8] = {};
+#pragma unroll 4
+  for (int k = warp; k < n; k += 8) {
+    const float f = w_s[k];
+    if (f == 0.f) continue;
+    const float4* p = reinterpret_cast<const float4*>(part + at_s[k]);
+    const float4 v0 = p[lane], v1 = p[lane + 32];
+    acc[0] = fmaf(f, v0.x, acc[0]);
+    acc[1] = fmaf(f, v0.y, acc[1]);
+    acc[2] = fmaf(f, v0.z, acc[2]);
+    acc[3] = fmaf(f, v0.w, acc[3]);
+    acc[4] = fmaf(f, v1.x, acc[4]);
+    acc[5] = fmaf(f, v1.y, acc[5]);
+    acc[6] = fmaf(f, v1.z, acc[6]);
+    acc[7] = fmaf(f, v1.w, acc[7]);
+  }
+  reinterpret_cast<float4*>(acc_s[warp])[lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  reinterpret_cast<float4*>(acc_s[warp])[lane + 32] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  __syncthreads();
+  float v = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v += acc_s[k][threadIdx.x];
+  const int64_t at = dense_q_row(t, x, x.row0 + r, H);
+  o[at * kHeadDim + threadIdx.x] = IO<T>::from_f(l != 0.f ? v / l : 0.f);      // l = 0: no key at all
+  if (lse && threadIdx.x == 0) lse[at] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
 }  // namespace qsa

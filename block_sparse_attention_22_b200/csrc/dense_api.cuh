@@ -60,19 +60,25 @@ struct DenseKind {
   int rows, kc, grid;
   bool by_keys;
   int cost = 2, min_tail = 4;
+  int part_rows = 0;                     // rows of a partial result, where they are not the unit's rows
+  bool level = true;                     // false: whole units in turn, for launches that hardly ever have work
 };
-
-int64_t unit_chunks(const DenseTable& t, int u) { return dense_unit(t, u).nchunks; }
 
 // Fills rounds, cut and the list of cut units of a table whose segments are set.
 void cut_table(DenseTable& t, DenseSplits& sp, const DenseKind& kind) {
   const int64_t kUnitCost = kind.cost, kMinTail = kind.min_tail;
   const int grid = t.grid;
   const int n_units = t.item0[t.n] * t.G;
+  sp.n = 0;
+  if (!kind.level) {
+    t.rounds = n_units / grid;
+    for (int c = 0; c <= grid; ++c) t.cut[c] = {std::min(t.rounds * grid + c, n_units), 0};
+    return;
+  }
   std::vector<int32_t> chunks((size_t)n_units);
   int64_t total = 0;
   for (int u = 0; u < n_units; ++u) {
-    chunks[u] = (int32_t)unit_chunks(t, u);
+    chunks[u] = dense_unit(t, u).nchunks;
     total += chunks[u] + kUnitCost;
   }
   // the most whole rounds after which no CTA has more than its share of everything
@@ -131,7 +137,6 @@ void cut_table(DenseTable& t, DenseSplits& sp, const DenseKind& kind) {
   }
   lay(hi);
   t.cut[grid] = {n_units, 0};
-  sp.n = 0;
   // a unit is cut iff some CTA's stretch starts inside it
   for (int c = 1; c < grid; ++c) {
     if (t.cut[c].chunk == 0) continue;
@@ -186,12 +191,33 @@ qsa_status_t for_each_dense(const Geo& g, std::vector<qsa_segment_t> segs, const
       t.item0[++t.n] = (int32_t)tiles;
       most = std::max(most, std::min<int64_t>(rows, kind.rows));
     }
-    t.prows = (int32_t)most;
+    t.prows = kind.part_rows > 0 ? kind.part_rows : (int32_t)most;
     cut_table(t, sp, kind);
     const qsa_status_t r = launch(t, sp);
     if (r != QSA_OK) return r;
   }
   return QSA_OK;
+}
+
+// One launch's table with its cut units.
+struct DenseLaunch {
+  DenseTable t;
+  DenseSplits sp;
+};
+
+// Bytes of a table's partial results.
+size_t partial_bytes(const DenseTable& t, const DenseSplits& sp) {
+  return sp.n > 0 ? (size_t)2 * t.grid * t.prows * dense::kPartFloats * 4 : 0;
+}
+
+// The launches of one kind for the segments; `part` grows to the largest's partial results.
+qsa_status_t plan_launches(const Geo& g, const std::vector<qsa_segment_t>& segs, const DenseKind& kind,
+                           std::vector<DenseLaunch>& out, size_t& part) {
+  return for_each_dense(g, segs, kind, [&](const DenseTable& t, const DenseSplits& sp) {
+    out.push_back({t, sp});
+    part = std::max(part, partial_bytes(t, sp));
+    return QSA_OK;
+  });
 }
 
 // A forward call's segments by the kernel that takes them, in launch order.
@@ -200,13 +226,15 @@ struct DenseGroup {
   DenseForm form;
   DenseKind kind;
   std::vector<qsa_segment_t> segs;
+  std::vector<DenseLaunch> launches;
 };
 
 // bf16: single tokens over a cache go to the decode kernel, other segments of
 // at most 128 rows to single CTAs unless larger ones are there, whose pairs then
 // take them too (one launch and its tail, 15 us, for a few half-empty tiles).
 std::vector<DenseGroup> dense_groups(const Geo& g, bool tc, bool paged, const qsa_segment_t* segs, int n) {
-  DenseGroup wide{DenseForm::kWide, {}, {}}, narrow{DenseForm::kNarrow, {}, {}}, decode{DenseForm::kDecode, {}, {}};
+  DenseGroup wide{DenseForm::kWide, {}, {}, {}}, narrow{DenseForm::kNarrow, {}, {}, {}},
+      decode{DenseForm::kDecode, {}, {}, {}};
   if (tc) {
     using N = dense_tc::Shape<1>;
     using W = dense_tc::Shape<2>;
@@ -232,20 +260,23 @@ std::vector<DenseGroup> dense_groups(const Geo& g, bool tc, bool paged, const qs
   return out;
 }
 
-// Bytes of a table's partial results.
-size_t partial_bytes(const DenseTable& t, const DenseSplits& sp) {
-  return sp.n > 0 ? (size_t)2 * t.grid * t.prows * dense::kPartFloats * 4 : 0;
+// The groups with their launches, and the bytes of workspace they need.
+qsa_status_t plan_dense_fwd(const Geo& g, bool tc, bool paged, const qsa_segment_t* segs, int n,
+                            std::vector<DenseGroup>& out, size_t& ws) {
+  out = dense_groups(g, tc, paged, segs, n);
+  ws = 0;
+  for (DenseGroup& d : out) {
+    const qsa_status_t r = plan_launches(g, d.segs, d.kind, d.launches, ws);
+    if (r != QSA_OK) return r;
+  }
+  ws = align_up(ws, 256);
+  return QSA_OK;
 }
 
 size_t dense_fwd_ws(const Geo& g, bool tc, bool paged, const qsa_segment_t* segs, int n) {
+  std::vector<DenseGroup> groups;
   size_t ws = 0;
-  for (const DenseGroup& d : dense_groups(g, tc, paged, segs, n))
-    if (for_each_dense(g, d.segs, d.kind, [&](const DenseTable& t, const DenseSplits& sp) {
-          ws = std::max(ws, partial_bytes(t, sp));
-          return QSA_OK;
-        }) != QSA_OK)
-      return SIZE_MAX;
-  return align_up(ws, 256);
+  return plan_dense_fwd(g, tc, paged, segs, n, groups, ws) == QSA_OK ? ws : SIZE_MAX;
 }
 
 // ------------------------------------------------------------------ forward
@@ -311,6 +342,11 @@ template <typename T>
 cudaError_t launch_dense_combine(const Geo& g, const DenseTable& t, const DenseSplits& sp, const float* part, void* o,
                                  float* lse, cudaStream_t st) {
   count_launch();
+  int most = 0;
+  for (int i = 0; i < sp.n; ++i) most = std::max(most, sp.last[i] - sp.first[i] + 1);
+  if (most > 4)                          // a warp per row adds four pieces in the time of a barrier or two
+    return launch_chained(dense_combine_many_kernel<T>, dim3(sp.n, (unsigned)t.prows), dim3(256), 0, st, t, sp, part,
+                          (T*)o, lse, g.H);
   return launch_chained(dense_combine_kernel<T>, dim3(sp.n, (unsigned)cdiv(t.prows, 4)), dim3(128), 0, st, t, sp,
                         part, (T*)o, lse, g.H);
 }
@@ -320,8 +356,10 @@ template <bool PAGED>
 qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int n, const KvSource& kv,
                            int64_t kv_rows, int kv_groups, int32_t n_tokens, const void* q, void* o, float* lse,
                            void* ws, size_t ws_bytes, cudaStream_t st) {
-  const size_t need = dense_fwd_ws(g, tc, PAGED, segs, n);
-  if (need == SIZE_MAX) return QSA_ERR_UNSUPPORTED;
+  std::vector<DenseGroup> groups;
+  size_t need = 0;
+  const qsa_status_t r = plan_dense_fwd(g, tc, PAGED, segs, n, groups, need);
+  if (r != QSA_OK) return r;
   if (need > 0 && (!ws || ws_bytes < need)) return QSA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return QSA_ERR_INVALID_ARG;
   float* part = (float*)ws;
@@ -331,43 +369,48 @@ qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int
     if ((int64_t)n_tokens * g.H > INT32_MAX - 512) return QSA_ERR_UNSUPPORTED;      // TMA row coordinates
     a = {kv, (const __nv_bfloat16*)q, (__nv_bfloat16*)o, lse, part, g.H, PAGED ? dense_box(kv.page_tokens) : 64,
          g.scale};
-    if (!make_dense_map(&m[0], kv.k, kv_rows, kv_groups, a.box) || !make_dense_map(&m[1], kv.v, kv_rows, kv_groups, a.box) ||
-        !make_dense_map(&m[2], q, (int64_t)n_tokens * g.H, 1, g.hpg) || !make_dense_map(&m[3], q, (int64_t)n_tokens * g.H, 1, g.hpg & -g.hpg))
+    if ((groups.size() > 1 || groups[0].form != DenseForm::kDecode) &&      // decode takes no maps
+        (!make_dense_map(&m[0], kv.k, kv_rows, kv_groups, a.box) ||
+         !make_dense_map(&m[1], kv.v, kv_rows, kv_groups, a.box) ||
+         !make_dense_map(&m[2], q, (int64_t)n_tokens * g.H, 1, g.hpg) ||
+         !make_dense_map(&m[3], q, (int64_t)n_tokens * g.H, 1, g.hpg & -g.hpg)))
       return QSA_ERR_CUDA;
   }
-  for (const DenseGroup& d : dense_groups(g, tc, PAGED, segs, n)) {
-    const bool is_wide = d.form == DenseForm::kWide;
-    const qsa_status_t r = for_each_dense(g, d.segs, d.kind, [&](const DenseTable& t, const DenseSplits& sp) -> qsa_status_t {
+  for (const DenseGroup& d : groups)
+    for (const DenseLaunch& x : d.launches) {
+      const bool is_wide = d.form == DenseForm::kWide;
       cudaError_t e;
       if (d.form == DenseForm::kDecode)
-        e = launch_dense_decode(t, a, st);
+        e = launch_dense_decode(x.t, a, st);
       else if (tc)
-        e = is_wide ? launch_dense_tc<2, PAGED>(t, m, a, st) : launch_dense_tc<1, PAGED>(t, m, a, st);
+        e = is_wide ? launch_dense_tc<2, PAGED>(x.t, m, a, st) : launch_dense_tc<1, PAGED>(x.t, m, a, st);
       else
-        e = is_wide ? launch_dense_simt<dense_simt::kRowsWide, PAGED>(g, t, kv, q, o, lse, part, st)
-                    : launch_dense_simt<dense_simt::kRowsNarrow, PAGED>(g, t, kv, q, o, lse, part, st);
-      if (e == cudaSuccess && sp.n > 0)
-        e = tc ? launch_dense_combine<__nv_bfloat16>(g, t, sp, part, o, lse, st)
-               : launch_dense_combine<float>(g, t, sp, part, o, lse, st);
-      return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
-    });
-    if (r != QSA_OK) return r;
-  }
+        e = is_wide ? launch_dense_simt<dense_simt::kRowsWide, PAGED>(g, x.t, kv, q, o, lse, part, st)
+                    : launch_dense_simt<dense_simt::kRowsNarrow, PAGED>(g, x.t, kv, q, o, lse, part, st);
+      if (e == cudaSuccess && x.sp.n > 0)
+        e = tc ? launch_dense_combine<__nv_bfloat16>(g, x.t, x.sp, part, o, lse, st)
+               : launch_dense_combine<float>(g, x.t, x.sp, part, o, lse, st);
+      if (e != cudaSuccess) return QSA_ERR_CUDA;
+    }
   return QSA_OK;
 }
 
 // ------------------------------------------------------------------ backward
 // Workspace of the gradient: delta by token; for bf16 also the statistics by
-// head (segments padded to whole tiles), the segments' flags and the partial
+// head (segments padded to whole tiles) and the segments' flags; the partial
 // results of the cut units (of one kernel at a time).
 struct DenseBwdPlan {
   std::vector<qsa_segment_t> segs;       // non-empty; slot: the segment's first statistics tile
+  std::vector<DenseLaunch> rows, keys;   // launches by rows (dq) and by keys (dk, dv)
   int64_t stat_rows = 0;
   size_t off_lse2 = 0, off_delta_h = 0, off_flags = 0, flag_bytes = 0, off_part = 0, bytes = 0;
 };
 
-DenseKind dense_bwd_kind(bool by_keys) {
-  return {dense_bwd::kRows, dense_bwd::kKeys, dense_bwd::kGrid, by_keys};
+DenseKind dense_bwd_kind(bool tc, bool by_keys) {
+  if (tc) return {dense_bwd::kRows, dense_bwd::kKeys, dense_bwd::kGrid, by_keys};
+  using namespace dense_simt;
+  return by_keys ? DenseKind{kBKeys, kBRows, kNumSms, true, 1, 1, 2 * kBKeys}
+                 : DenseKind{kBRows, kBKeys, kNumSms, false, 1, 1};
 }
 
 qsa_status_t plan_dense_bwd(const Geo& g, bool tc, const qsa_segment_t* segs, int n, int32_t n_tokens,
@@ -387,20 +430,14 @@ qsa_status_t plan_dense_bwd(const Geo& g, bool tc, const qsa_segment_t* segs, in
     p.off_delta_h = at + stats;
     p.off_flags = at + 2 * stats;
     p.flag_bytes = (size_t)tiles * 4;
-    at = p.off_part = p.off_flags + align_up(p.flag_bytes, 256);
-    size_t part = 0;
-    for (const bool by_keys : {false, true}) {
-      const qsa_status_t r =
-          for_each_dense(g, p.segs, dense_bwd_kind(by_keys), [&](const DenseTable& t, const DenseSplits& sp) {
-            part = std::max(part, partial_bytes(t, sp));
-            return QSA_OK;
-          });
-      if (r != QSA_OK) return r;
-    }
-    at += align_up(part, 256);
+    at = p.off_flags + align_up(p.flag_bytes, 256);
   }
-  p.bytes = at;
-  return QSA_OK;
+  p.off_part = at;
+  size_t part = 0;
+  qsa_status_t r = plan_launches(g, p.segs, dense_bwd_kind(tc, false), p.rows, part);
+  if (r == QSA_OK) r = plan_launches(g, p.segs, dense_bwd_kind(tc, true), p.keys, part);
+  p.bytes = at + align_up(part, 256);
+  return r;
 }
 
 size_t dense_bwd_ws(const Geo& g, bool tc, const qsa_segment_t* segs, int n, int32_t n_tokens) {
@@ -408,47 +445,53 @@ size_t dense_bwd_ws(const Geo& g, bool tc, const qsa_segment_t* segs, int n, int
   return plan_dense_bwd(g, tc, segs, n, n_tokens, p) == QSA_OK ? p.bytes : SIZE_MAX;
 }
 
-// The CUDA-core gradient.  With a.flags: of the flagged segments only, on no
-// more blocks than the GPU holds, since there are hardly ever any.
+// Joins the cut units of a gradient launch.
 template <typename T>
-qsa_status_t run_dense_bwd_simt(const Geo& g, const std::vector<qsa_segment_t>& segs, const DenseBwdArgs& a,
+cudaError_t launch_bwd_combine(const Geo& g, const DenseLaunch& x, const float* part, const int32_t* flags, void* out,
+                               float factor, void* out2, cudaStream_t st) {
+  if (x.sp.n == 0) return cudaSuccess;
+  count_launch();
+  return launch_chained(dense_bwd_combine_kernel<T>,
+                        dim3(x.sp.n, (unsigned)cdiv(std::min(x.t.prows, x.t.rows), 4)), dim3(128), 0, st, x.t, x.sp,
+                        part, flags, (T*)out, factor, (T*)out2, dense_simt::kBKeys, g.H);
+}
+
+// The CUDA-core gradient over the given launches.
+template <typename T>
+qsa_status_t run_dense_bwd_simt(const Geo& g, const std::vector<DenseLaunch>& rows,
+                                const std::vector<DenseLaunch>& keys, const DenseBwdArgs& a, float* part,
                                 cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(dense_dq_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        dense_simt::kBwdSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(dense_dkv_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              dense_simt::kBwdSmem);
-  if (e != cudaSuccess) return QSA_ERR_CUDA;
-  auto blocks = [&](int64_t units) { return dim3((unsigned)(a.flags ? std::min<int64_t>(units, kNumSms) : units)); };
-  const qsa_status_t r = for_each_dense(
-      g, segs, DenseKind{dense_simt::kBRows, dense_simt::kBKeys, 1, false},
-      [&](const DenseTable& t, const DenseSplits&) -> qsa_status_t {
-        count_launch();
-        return launch_chained(dense_dq_simt_kernel<T>, blocks((int64_t)t.item0[t.n] * g.G), dim3(dense_simt::kThreads),
-                              dense_simt::kBwdSmem, st, t, a) == cudaSuccess
-                   ? QSA_OK
-                   : QSA_ERR_CUDA;
-      });
-  if (r != QSA_OK) return r;
-  return for_each_table(
-      segs.data(), (int)segs.size(), [&](const qsa_segment_t& s) { return cdiv(s.q_len, dense_simt::kBKeys); },
-      [&](const SegTable& t) -> cudaError_t {
-        count_launch();
-        return launch_chained(dense_dkv_simt_kernel<T>, blocks((int64_t)t.item0[t.n] * g.G), dim3(dense_simt::kThreads),
-                              dense_simt::kBwdSmem, st, t, g.G, g.hpg, a);
-      });
+  const dim3 block(dense_simt::kThreads);
+  for (const DenseLaunch& x : rows) {
+    if (e != cudaSuccess) break;
+    count_launch();
+    e = launch_chained(dense_dq_simt_kernel<T>, dim3(x.t.grid), block, dense_simt::kBwdSmem, st, x.t, a, part);
+    if (e == cudaSuccess) e = launch_bwd_combine<T>(g, x, part, nullptr, a.dq, g.scale, nullptr, st);
+  }
+  for (const DenseLaunch& x : keys) {
+    if (e != cudaSuccess) break;
+    count_launch();
+    e = launch_chained(dense_dkv_simt_kernel<T>, dim3(x.t.grid), block, dense_simt::kBwdSmem, st, x.t, a, part);
+    if (e == cudaSuccess) e = launch_bwd_combine<T>(g, x, part, nullptr, a.dk, g.scale, a.dv, st);
+  }
+  return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 
-qsa_status_t run_dense_bwd_f32(const Geo& g, const DenseBwdPlan& p, const DenseBwdArgs& a, const void* o, float* delta,
+qsa_status_t run_dense_bwd_f32(const Geo& g, const DenseBwdPlan& p, const DenseBwdArgs& a, const void* o, char* ws,
                                cudaStream_t st) {
   const qsa_status_t r = for_each_table(
       p.segs.data(), (int)p.segs.size(), [&](const qsa_segment_t& s) { return (int64_t)s.q_len; },
       [&](const SegTable& t) -> cudaError_t {
         count_launch();
         return launch_chained(dense_delta_kernel<float>, dim3((unsigned)cdiv((int64_t)t.item0[t.n] * g.H, 8)),
-                              dim3(256), 0, st, t, (const float*)o, (const float*)a.dout, delta, g.H);
+                              dim3(256), 0, st, t, (const float*)o, (const float*)a.dout, (float*)ws, g.H);
       });
-  return r != QSA_OK ? r : run_dense_bwd_simt<float>(g, p.segs, a, st);
+  return r != QSA_OK ? r : run_dense_bwd_simt<float>(g, p.rows, p.keys, a, (float*)(ws + p.off_part), st);
 }
 
 // One gradient on the tensor cores: its kernel, then the join of its cut units.
@@ -456,32 +499,29 @@ template <dense_bwd::Grad M>
 qsa_status_t run_dense_grad_tc(const Geo& g, const DenseBwdPlan& p, const DenseBwdMaps& m, const DenseBwdTcArgs& a,
                                cudaStream_t st) {
   auto kernel = dense_bwd_tc_kernel<M>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense_bwd::kSmemBytes) != cudaSuccess)
-    return QSA_ERR_CUDA;
-  return for_each_dense(
-      g, p.segs, dense_bwd_kind(M != dense_bwd::kDq), [&](const DenseTable& t, const DenseSplits& sp) -> qsa_status_t {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(t.grid * 2);
-        cfg.blockDim = dim3(dense_bwd::kThreads);
-        cfg.dynamicSmemBytes = dense_bwd::kSmemBytes;
-        cfg.stream = st;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = 2;
-        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        count_launch();
-        cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, m, t, a);
-        if (e == cudaSuccess && sp.n > 0) {
-          count_launch();
-          e = launch_chained(dense_bwd_combine_kernel, dim3(sp.n, (unsigned)cdiv(t.prows, 4)), dim3(128), 0, st, t, sp,
-                             a.part, a.flags, a.out, g.H, M == dense_bwd::kDv ? 1.f : g.scale);
-        }
-        return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
-      });
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense_bwd::kSmemBytes);
+  for (const DenseLaunch& x : M == dense_bwd::kDq ? p.rows : p.keys) {
+    if (e != cudaSuccess) break;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(x.t.grid * 2);
+    cfg.blockDim = dim3(dense_bwd::kThreads);
+    cfg.dynamicSmemBytes = dense_bwd::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    count_launch();
+    e = cudaLaunchKernelEx(&cfg, kernel, m, x.t, a);
+    if (e == cudaSuccess)
+      e = launch_bwd_combine<__nv_bfloat16>(g, x, a.part, a.flags, a.out, M == dense_bwd::kDv ? 1.f : g.scale, nullptr,
+                                            st);
+  }
+  return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 
 qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArgs a, const void* o, char* ws,
@@ -517,8 +557,15 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
   if ((r = run_dense_grad_tc<dense_bwd::kDk>(g, p, {mq, mo, mq, mk, mv, mk, mv}, b, st)) != QSA_OK) return r;
   b.out = (B*)a.dq;
   if ((r = run_dense_grad_tc<dense_bwd::kDq>(g, p, {mk, mv, mk, tq, to, rq, ro}, b, st)) != QSA_OK) return r;
+  // the flagged segments; their launches are not levelled (there are hardly ever any)
   a.flags = flags;
-  return run_dense_bwd_simt<B>(g, p.segs, a, st);
+  std::vector<DenseLaunch> by_rows, by_keys;
+  size_t part = 0;
+  DenseKind kr = dense_bwd_kind(false, false), kk = dense_bwd_kind(false, true);
+  kr.level = kk.level = false;
+  if ((r = plan_launches(g, p.segs, kr, by_rows, part)) != QSA_OK) return r;
+  if ((r = plan_launches(g, p.segs, kk, by_keys, part)) != QSA_OK) return r;
+  return run_dense_bwd_simt<B>(g, by_rows, by_keys, a, nullptr, st);
 }
 
 // Runs an entry point's body; host memory that runs out is an error code, not
@@ -577,10 +624,14 @@ QSA_API qsa_status_t qsa_append_kv(const qsa_config_t* cfg, const qsa_pages_t* p
         segs, n_segs, [&](const qsa_segment_t& sg) { return (int64_t)sg.q_len; },
         [&](const SegTable& t) -> cudaError_t {
           count_launch();
-          const dim3 grid((unsigned)t.item0[t.n]), block(append::kThreads);
-          return cfg->dtype == QSA_DTYPE_BF16
-                     ? launch_chained(append_kernel<__nv_bfloat16>, grid, block, 0, (cudaStream_t)stream, g, t, a)
-                     : launch_chained(append_kernel<float>, grid, block, 0, (cudaStream_t)stream, g, t, a);
+          const int n = t.item0[t.n], per = n <= 4 * kNumSms ? 1 : append::kTokens;
+          const dim3 grid((unsigned)cdiv(n, per)), block(append::kThreads);
+          const cudaStream_t s0 = (cudaStream_t)stream;
+          if (cfg->dtype == QSA_DTYPE_BF16)
+            return per == 1 ? launch_chained(append_kernel<__nv_bfloat16, 1>, grid, block, 0, s0, g, t, a)
+                            : launch_chained(append_kernel<__nv_bfloat16, append::kTokens>, grid, block, 0, s0, g, t, a);
+          return per == 1 ? launch_chained(append_kernel<float, 1>, grid, block, 0, s0, g, t, a)
+                          : launch_chained(append_kernel<float, append::kTokens>, grid, block, 0, s0, g, t, a);
         });
   });
 }
@@ -639,9 +690,8 @@ QSA_API qsa_status_t qsa_prompt_attn_bwd(const qsa_config_t* cfg, const qsa_segm
     if ((s = plan_dense_bwd(g, tc, segs, n_segs, n_tokens, p)) != QSA_OK) return s;
     if (!workspace || ws_bytes < p.bytes) return QSA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return QSA_ERR_INVALID_ARG;
-    float* delta = (float*)workspace;
-    const DenseBwdArgs a{q, k, v, lse, delta, dout, dq, dk, dv, g.H, g.scale, nullptr};
+    const DenseBwdArgs a{q, k, v, lse, (const float*)workspace, dout, dq, dk, dv, g.H, g.scale, nullptr};
     return tc ? run_dense_bwd_bf16(g, p, a, o, (char*)workspace, n_tokens, (cudaStream_t)stream)
-              : run_dense_bwd_f32(g, p, a, o, delta, (cudaStream_t)stream);
+              : run_dense_bwd_f32(g, p, a, o, (char*)workspace, (cudaStream_t)stream);
   });
 }

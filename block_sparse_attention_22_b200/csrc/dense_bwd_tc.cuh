@@ -498,37 +498,6 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
   }
 }
 
-// Adds up the pieces of each cut unit in the order of their chunks, scales and
-// rounds.  One warp per stationary row.
-__global__ void __launch_bounds__(128)
-    dense_bwd_combine_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseSplits sp,
-                             const float* part, const int32_t* flags, __nv_bfloat16* out, int H, float factor) {
-  pdl_wait();
-  pdl_trigger();
-  const int i = blockIdx.x;
-  const int u = sp.unit[i];
-  const DenseUnit x = dense_unit(t, u);
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (r >= x.nrows || flags[t.slot[x.si]]) return;
-  float acc[8] = {};
-  for (int c = sp.first[i]; c <= sp.last[i]; ++c) {
-    const int part_of = dense_piece_slot(t, u, c);
-    if (part_of < 0) continue;
-    const float4* p = reinterpret_cast<const float4*>(part + ((int64_t)part_of * t.prows + r) * dense::kPartFloats);
-    const float4 v0 = p[2 * lane], v1 = p[2 * lane + 1];
-    acc[0] += v0.x; acc[1] += v0.y; acc[2] += v0.z; acc[3] += v0.w;
-    acc[4] += v1.x; acc[5] += v1.y; acc[6] += v1.z; acc[7] += v1.w;
-  }
-  const int32_t row = x.row0 + r;
-  const int64_t at =
-      t.by_keys ? (int64_t)(t.q_offset[x.si] + row) * t.G + x.grp : dense_q_row(t, x, row, H);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) acc[k] *= factor;
-  Vec8<__nv_bfloat16> v;
-  v.set(acc);
-  v.store(out + at * kHeadDim + lane * 8);
-}
-
 // Row statistics for the gradient kernels, one warp per (token, head): delta =
 // dout . o, by token for the CUDA-core kernels and, with lse in log2 units, by
 // head and statistics row for the tensor-core kernels; rows behind a segment's

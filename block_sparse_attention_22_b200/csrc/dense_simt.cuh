@@ -338,10 +338,11 @@ __device__ __forceinline__ bool simt_any(const Table& t, const int32_t* flags) {
   return __syncthreads_or(any);
 }
 
-// dq of (64-row tile, group): loops over its keys.
+// dq of tiles of 64 rows, in chunks of 32 keys (dense.cuh); a piece of a cut
+// unit leaves its unscaled sum.
 template <typename T>
 __global__ void __launch_bounds__(dense_simt::kThreads)
-    dense_dq_simt_kernel(const __grid_constant__ DenseTable t, DenseBwdArgs a) {
+    dense_dq_simt_kernel(const __grid_constant__ DenseTable t, DenseBwdArgs a, float* part) {
   using namespace dense_simt;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
@@ -357,9 +358,11 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
   pdl_wait();
   pdl_trigger();
   if (!simt_any(t, a.flags)) return;
-  const int n_units = t.item0[t.n] * t.G;
-  for (int unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
-    const DenseUnit x = dense_unit(t, unit);
+  DenseWalk walk;
+  walk.init(t, blockIdx.x);
+  DensePiece p;
+  DenseUnit x;
+  while (walk.next(t, p, x)) {
     const int si = x.si;
     if (a.flags && !a.flags[t.slot[si]]) continue;
     __syncthreads();
@@ -382,7 +385,8 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][k] = 0.f;
     const int32_t first_pos = x.row0 / t.hpg;
-    for (int32_t j0 = 0; j0 < x.kv_len; j0 += kBKeys) {
+    for (int c = p.c0; c < p.c1; ++c) {
+      const int32_t j0 = c * kBKeys;
       __syncthreads();
       auto keys_of = [&](const void* base) {
         return [&, base](int r) -> const T* {
@@ -404,21 +408,30 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (ra + i >= x.nrows) continue;
-      T* dst = (T*)a.dq + q_at(ra + i) * kHeadDim;
+      if (p.part < 0) {
+        T* dst = (T*)a.dq + q_at(ra + i) * kHeadDim;
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj)
-        simt_store4(dst + 4 * tx + 64 * jj, acc[i][4 * jj] * a.scale, acc[i][4 * jj + 1] * a.scale,
-                    acc[i][4 * jj + 2] * a.scale, acc[i][4 * jj + 3] * a.scale);
+        for (int jj = 0; jj < 4; ++jj)
+          simt_store4(dst + 4 * tx + 64 * jj, acc[i][4 * jj] * a.scale, acc[i][4 * jj + 1] * a.scale,
+                      acc[i][4 * jj + 2] * a.scale, acc[i][4 * jj + 3] * a.scale);
+      } else {
+        float* dst = part + ((int64_t)p.part * t.prows + ra + i) * dense::kPartFloats;
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+          simt_store4(dst + 4 * tx + 64 * jj, acc[i][4 * jj], acc[i][4 * jj + 1], acc[i][4 * jj + 2],
+                      acc[i][4 * jj + 3]);
+      }
     }
   }
 }
 
-// dk and dv of (32-key tile, group): loops over the rows that see it.  The
-// unit counts a segment's key tiles from its start (most rows first);
-// a thread owns 4 keys x 8 dims of both.
+// dk and dv of tiles of 32 keys, by keys (dense.cuh): a chunk is 64 tokens of
+// one head.  A thread owns 4 keys x 8 dims of both.  A piece of a cut unit leaves
+// its unscaled sums, dv's rows kBKeys behind dk's.  (One block per unit held 64 of
+// 148 SMs at 989 tokens x 2 groups, and the longest of them 3.5 ms.)
 template <typename T>
 __global__ void __launch_bounds__(dense_simt::kThreads)
-    dense_dkv_simt_kernel(const __grid_constant__ SegTable st, int G, int hpg, DenseBwdArgs a) {
+    dense_dkv_simt_kernel(const __grid_constant__ DenseTable t, DenseBwdArgs a, float* part) {
   using namespace dense_simt;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
@@ -433,16 +446,17 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
   const int kq = (threadIdx.x >> 5) * 4, dl = (threadIdx.x & 31) * 4;
   pdl_wait();
   pdl_trigger();
-  if (!simt_any(st, a.flags)) return;
-  const int n_units = st.item0[st.n] * G;
-  for (int unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
-    const int tile = unit / G, grp = unit - tile * G;
-    const int si = find_segment(st, tile);
-    if (a.flags && !a.flags[st.slot[si]]) continue;
+  if (!simt_any(t, a.flags)) return;
+  DenseWalk walk;
+  walk.init(t, blockIdx.x);
+  DensePiece p;
+  DenseUnit x;
+  while (walk.next(t, p, x)) {
+    if (a.flags && !a.flags[t.slot[x.si]]) continue;
     __syncthreads();
-    const int32_t j0 = (tile - st.item0[si]) * kBKeys, n = st.q_len[si];
-    const int64_t q0 = st.q_offset[si];
-    auto key_at = [&](int r) -> int64_t { return ((q0 + j0 + r) * G + grp) * kHeadDim; };
+    const int32_t j0 = x.row0, n = x.kv_len;
+    const int64_t q0 = t.q_offset[x.si];
+    auto key_at = [&](int r) -> int64_t { return ((q0 + j0 + r) * t.G + x.grp) * kHeadDim; };
     auto keys_of = [&](const void* base) {
       return [&, base](int r) -> const T* { return j0 + r < n ? (const T*)base + key_at(r) : nullptr; };
     };
@@ -453,12 +467,11 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) dk[i][k] = dv[i][k] = 0.f;
-    for (int32_t row0 = j0 * hpg; row0 < n * hpg; row0 += kBRows) {
-      const int nrows = min(kBRows, n * hpg - row0);
-      auto q_at = [&](int r) -> int64_t {
-        const int32_t tok = (row0 + r) / hpg;
-        return (q0 + tok) * a.H + grp * hpg + (row0 + r - tok * hpg);
-      };
+    for (int c = p.c0; c < p.c1; ++c) {
+      const int32_t i0 = j0 + c / t.hpg * kBRows;                     // first token of the chunk
+      const int nrows = min(kBRows, n - i0);
+      const int64_t head = x.grp * t.hpg + c % t.hpg;
+      auto q_at = [&](int r) { return (q0 + i0 + r) * a.H + head; };
       auto rows_of = [&](const void* base) {
         return [&, base](int r) -> const T* {
           return r < nrows ? (const T*)base + q_at(r) * kHeadDim : nullptr;
@@ -474,49 +487,93 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
       }
       sm100::cp_async_wait_all();
       __syncthreads();
-      simt_p_ds(Qs, Os, Ks, Vs, Ps, Ds, st_lse, st_delta, row0, nrows, hpg, j0, n, s2);
+      simt_p_ds(Qs, Os, Ks, Vs, Ps, Ds, st_lse, st_delta, i0, nrows, 1, j0, n, s2);
       __syncthreads();
-      // keys of the tile after the first row's position: a row before a key does not touch it
-      const bool limited = j0 + kBKeys - 1 > row0 / hpg;
+      // a row before a key does not touch it
+      const bool limited = j0 + kBKeys - 1 > i0;
       for (int r = 0; r < nrows; ++r) {
-        const float4 p = *reinterpret_cast<const float4*>(Ps + r * kBLd + kq);
-        const float4 s = *reinterpret_cast<const float4*>(Ds + r * kBLd + kq);
-        const int32_t pos = limited ? (row0 + r) / hpg : 0;
-        const float pp[4] = {p.x, p.y, p.z, p.w}, ss[4] = {s.x, s.y, s.z, s.w};
-        float4 x[2], y[2];
+        const float4 pr = *reinterpret_cast<const float4*>(Ps + r * kBLd + kq);
+        const float4 sr = *reinterpret_cast<const float4*>(Ds + r * kBLd + kq);
+        const float pp[4] = {pr.x, pr.y, pr.z, pr.w}, ss[4] = {sr.x, sr.y, sr.z, sr.w};
+        float4 xq[2], xo[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          x[h] = *reinterpret_cast<const float4*>(Qs + r * kLd + dl + 128 * h);
-          y[h] = *reinterpret_cast<const float4*>(Os + r * kLd + dl + 128 * h);
+          xq[h] = *reinterpret_cast<const float4*>(Qs + r * kLd + dl + 128 * h);
+          xo[h] = *reinterpret_cast<const float4*>(Os + r * kLd + dl + 128 * h);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (limited && j0 + kq + i > pos) continue;
+          if (limited && j0 + kq + i > i0 + r) continue;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            dk[i][4 * h] = fmaf(ss[i], x[h].x, dk[i][4 * h]);
-            dk[i][4 * h + 1] = fmaf(ss[i], x[h].y, dk[i][4 * h + 1]);
-            dk[i][4 * h + 2] = fmaf(ss[i], x[h].z, dk[i][4 * h + 2]);
-            dk[i][4 * h + 3] = fmaf(ss[i], x[h].w, dk[i][4 * h + 3]);
-            dv[i][4 * h] = fmaf(pp[i], y[h].x, dv[i][4 * h]);
-            dv[i][4 * h + 1] = fmaf(pp[i], y[h].y, dv[i][4 * h + 1]);
-            dv[i][4 * h + 2] = fmaf(pp[i], y[h].z, dv[i][4 * h + 2]);
-            dv[i][4 * h + 3] = fmaf(pp[i], y[h].w, dv[i][4 * h + 3]);
+            dk[i][4 * h] = fmaf(ss[i], xq[h].x, dk[i][4 * h]);
+            dk[i][4 * h + 1] = fmaf(ss[i], xq[h].y, dk[i][4 * h + 1]);
+            dk[i][4 * h + 2] = fmaf(ss[i], xq[h].z, dk[i][4 * h + 2]);
+            dk[i][4 * h + 3] = fmaf(ss[i], xq[h].w, dk[i][4 * h + 3]);
+            dv[i][4 * h] = fmaf(pp[i], xo[h].x, dv[i][4 * h]);
+            dv[i][4 * h + 1] = fmaf(pp[i], xo[h].y, dv[i][4 * h + 1]);
+            dv[i][4 * h + 2] = fmaf(pp[i], xo[h].z, dv[i][4 * h + 2]);
+            dv[i][4 * h + 3] = fmaf(pp[i], xo[h].w, dv[i][4 * h + 3]);
           }
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (j0 + kq + i >= n) continue;
+      if (kq + i >= x.nrows) continue;
       const int64_t at = key_at(kq + i) + dl;
+      float* pk = part + ((int64_t)p.part * t.prows + kq + i) * dense::kPartFloats + dl;
+      float* pv = pk + kBKeys * dense::kPartFloats;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        simt_store4((T*)a.dk + at + 128 * h, dk[i][4 * h] * a.scale, dk[i][4 * h + 1] * a.scale,
-                    dk[i][4 * h + 2] * a.scale, dk[i][4 * h + 3] * a.scale);
-        simt_store4((T*)a.dv + at + 128 * h, dv[i][4 * h], dv[i][4 * h + 1], dv[i][4 * h + 2], dv[i][4 * h + 3]);
+        if (p.part < 0) {
+          simt_store4((T*)a.dk + at + 128 * h, dk[i][4 * h] * a.scale, dk[i][4 * h + 1] * a.scale,
+                      dk[i][4 * h + 2] * a.scale, dk[i][4 * h + 3] * a.scale);
+          simt_store4((T*)a.dv + at + 128 * h, dv[i][4 * h], dv[i][4 * h + 1], dv[i][4 * h + 2], dv[i][4 * h + 3]);
+        } else {
+          simt_store4(pk + 128 * h, dk[i][4 * h], dk[i][4 * h + 1], dk[i][4 * h + 2], dk[i][4 * h + 3]);
+          simt_store4(pv + 128 * h, dv[i][4 * h], dv[i][4 * h + 1], dv[i][4 * h + 2], dv[i][4 * h + 3]);
+        }
       }
     }
+  }
+}
+
+// Adds up the pieces of each cut unit in the order of their chunks, scales and
+// rounds: out, then (if given) out2 from the partial rows `rows2` behind.  One
+// warp per stationary row.  With flags: not the units of flagged segments.
+template <typename T>
+__global__ void __launch_bounds__(128)
+    dense_bwd_combine_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseSplits sp,
+                             const float* part, const int32_t* flags, T* out, float factor, T* out2,
+                             int rows2, int H) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x;
+  const int u = sp.unit[i];
+  const DenseUnit x = dense_unit(t, u);
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  if (r >= x.nrows || (flags && flags[t.slot[x.si]])) return;
+  const int32_t row = x.row0 + r;
+  const int64_t at =
+      t.by_keys ? (int64_t)(t.q_offset[x.si] + row) * t.G + x.grp : dense_q_row(t, x, row, H);
+  for (int k = 0; k < (out2 ? 2 : 1); ++k) {
+    float acc[8] = {};
+    for (int c = sp.first[i]; c <= sp.last[i]; ++c) {
+      const int slot = dense_piece_slot(t, u, c);
+      if (slot < 0) continue;
+      const float4* p =
+          reinterpret_cast<const float4*>(part + ((int64_t)slot * t.prows + r + k * rows2) * dense::kPartFloats);
+      const float4 v0 = p[2 * lane], v1 = p[2 * lane + 1];
+      acc[0] += v0.x; acc[1] += v0.y; acc[2] += v0.z; acc[3] += v0.w;
+      acc[4] += v1.x; acc[5] += v1.y; acc[6] += v1.z; acc[7] += v1.w;
+    }
+    const float f = k == 0 ? factor : 1.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] *= f;
+    Vec8<T> v;
+    v.set(acc);
+    v.store((k == 0 ? out : out2) + at * kHeadDim + lane * 8);
   }
 }
 
