@@ -14,8 +14,7 @@ namespace qsa {
 namespace append {
 constexpr int kThreads = 256;
 constexpr int kMaxHalf = kHeadDim / 2;      // rotated pairs at rope_fraction 1
-constexpr int kUnroll = 4;                  // vectors a warp loads before it stores the first
-constexpr int kTokens = 8;                  // tokens of a block, when there are enough for every SM
+constexpr int kWarps = kThreads / 32;
 }  // namespace append
 
 struct AppendArgs {
@@ -73,115 +72,124 @@ template <> struct Vec8<float> {
   }
 };
 
-// A block takes TPB tokens.  A token's G keys, H queries (when given) and G
-// values are vectors of 256 dims, one warp each, 8 dims per lane.  The kernel
-// is a copy, bound by HBM; what it waits for is the fp64 sine and cosine, so with
-// eight tokens at 32 rotated pairs every thread forms one of them while the
-// warps' first loads are in flight.  (One token per block left seven of eight warps
-// idle meanwhile: 44 us for a 4096-token chunk of 24 + 2 + 2 heads, 117 MB.)  Few
-// tokens take a block each, for the latency.  A pair's halves are `half` / 8 lanes
-// apart; where that is no whole number they meet in shared memory.
-template <typename T, int TPB>
+// WPT warps take a token (one, or the block's eight when there are too few
+// tokens to fill the GPU).  A token's G keys, H queries (when given) and G values
+// are vectors of 256 dims; the rotated dims are a part of the first 16-byte pieces
+// of each.  The kernel is a copy, bound by HBM as long as it stays short of
+// instructions: pieces that are only copied go lane by lane down the vectors, and
+// the rotated ones are taken pairwise, a lane holding eight dims and their eight
+// partners, so no lane converts what it does not rotate.  A warp forms its own
+// token's sines and cosines while its first loads are in flight.  (With a vector
+// per warp and step, partners by shuffle, and the pointers formed per vector, a
+// 4096-token chunk of 24 + 2 + 2 heads took 44 us, bound by instruction issue.)
+template <typename T, int WPT>
 __global__ void __launch_bounds__(append::kThreads)
     append_kernel(Geo g, const __grid_constant__ SegTable st, const __grid_constant__ AppendArgs a) {
   using namespace append;
-  constexpr int kWarps = kThreads / 32;
-  __shared__ float cs[TPB][kMaxHalf], sn[TPB][kMaxHalf];
-  __shared__ float row[kWarps][kHeadDim];
-  __shared__ int64_t tok_s[TPB], pos_s[TPB], cache_s[TPB];      // cache row of group 0; -1: not stored
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int first = (int)blockIdx.x * TPB, ntok = min(TPB, st.item0[st.n] - first);
+  __shared__ float cs_s[kWarps][kMaxHalf], sn_s[kWarps][kMaxHalf];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPT;
+  const int item = (int)blockIdx.x * (kWarps / WPT) + warp / WPT;
+  float* const cs = cs_s[warp];
+  float* const sn = sn_s[warp];
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x < ntok) {
-    const int item = first + (int)threadIdx.x;
-    const int si = find_segment(st, item);
-    const int j = item - st.item0[si];
-    const int32_t pos = st.pos0[si] + j, pi = pos / a.page_tokens;
-    const int32_t page = a.table[(int64_t)st.slot[si] * a.max_pages + pi];
-    const bool ok = page >= 0 && page < a.n_pages;
-    if (!ok) report_error(kErrBadIndex);
-    tok_s[threadIdx.x] = (int64_t)st.q_offset[si] + j;
-    pos_s[threadIdx.x] = pos;
-    cache_s[threadIdx.x] = ok ? (int64_t)page * g.G * a.page_tokens + (pos - pi * a.page_tokens) : -1;
-  }
-  __syncthreads();
-  const int nq = a.q ? g.H : 0;
-  const int n_rot = g.G + nq, n_vec = n_rot + g.G, total = ntok * n_vec;
-  auto src = [&](int i, int v) -> const T* {
-    const int64_t tok = tok_s[i];
-    if (v < g.G) return (const T*)a.k + tok * a.ld_k + (int64_t)v * kHeadDim;
-    if (v < n_rot) return (const T*)a.q + tok * a.ld_q + (int64_t)(v - g.G) * kHeadDim;
-    return (const T*)a.v + tok * a.ld_v + (int64_t)(v - n_rot) * kHeadDim;
+  if (item >= st.item0[st.n]) return;
+  const int si = find_segment(st, item);
+  const int j = item - st.item0[si];
+  const int64_t tok = (int64_t)st.q_offset[si] + j;
+  const int32_t pos = st.pos0[si] + j, pi = pos / a.page_tokens;
+  const int32_t page = a.table[(int64_t)st.slot[si] * a.max_pages + pi];
+  const bool stored = page >= 0 && page < a.n_pages;
+  if (!stored && lane == 0 && sub == 0) report_error(kErrBadIndex);
+  const T* const k = (const T*)a.k + tok * a.ld_k;
+  const T* const v = (const T*)a.v + tok * a.ld_v;
+  const T* const q = (const T*)a.q + tok * a.ld_q;
+  T* const qo = (T*)a.q_out + tok * g.H * kHeadDim;
+  const int64_t at = stored ? ((int64_t)page * g.G * a.page_tokens + (pos - pi * a.page_tokens)) * kHeadDim : 0;
+  T* const kp = (T*)a.kp + at;
+  T* const vp = (T*)a.vp + at;
+  const int64_t ld_p = (int64_t)a.page_tokens * kHeadDim;      // between a page's groups
+  const int half = a.half, nq = a.q ? g.H : 0, n_rot = g.G + nq;
+  // vector w: keys, then queries, then values (which are not rotated)
+  auto from = [&](int w) { return w < g.G ? k + w * kHeadDim : w < n_rot ? q + (w - g.G) * kHeadDim : v + (w - n_rot) * kHeadDim; };
+  auto to = [&](int w) { return w < g.G ? kp + w * ld_p : w < n_rot ? qo + (w - g.G) * kHeadDim : vp + (w - n_rot) * ld_p; };
+  auto wanted = [&](int w) { return stored || (w >= g.G && w < n_rot); };
+  // values, and the pieces of the rotated vectors behind the rotation; kUnroll
+  // loads before the first store, which may alias them (q in place)
+  constexpr int kUnroll = sizeof(T) == 2 ? 8 : 4;
+  const int mixed = (2 * half + 7) >> 3;                        // pieces with rotated dims
+  auto form_angles = [&]() {
+    for (int p = lane; p < half; p += 32) {
+      double s, c;
+      sincos((double)pos * a.theta[p], &s, &c);
+      cs[p] = (float)c;
+      sn[p] = (float)s;
+    }
   };
-  auto dst = [&](int i, int v) -> T* {   // null: not stored
-    if (v >= g.G && v < n_rot) return (T*)a.q_out + (tok_s[i] * g.H + (v - g.G)) * kHeadDim;
-    if (cache_s[i] < 0) return nullptr;
-    const bool is_k = v < g.G;
-    const int64_t r = cache_s[i] + (int64_t)(is_k ? v : v - n_rot) * a.page_tokens;
-    return (T*)(is_k ? a.kp : a.vp) + r * kHeadDim;
-  };
-  const bool by_lane = (a.half & 7) == 0;
-  const int apart = a.half >> 3;         // lanes between a pair's halves
   bool angles = false;
-  for (int w0 = warp; w0 < total || !angles; w0 += kWarps * kUnroll) {
+  for (int w0 = sub; w0 < n_rot + g.G; w0 += kUnroll * WPT) {
     Vec8<T> x[kUnroll];
+    auto mine = [&](int w) { return w < n_rot + g.G && (w >= n_rot || lane >= mixed) && wanted(w); };
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int w = w0 + u * kWarps, i = w / n_vec;
-      if (w < total) x[u].load(src(i, w - i * n_vec) + lane * 8);
-    }
-    if (!angles) {
-      for (int k = threadIdx.x; k < ntok * a.half; k += kThreads) {
-        const int i = k / a.half, p = k - i * a.half;
-        double s, c;
-        sincos((double)pos_s[i] * a.theta[p], &s, &c);
-        cs[i][p] = (float)c;
-        sn[i][p] = (float)s;
-      }
-      __syncthreads();
-      angles = true;
-    }
+    for (int u = 0; u < kUnroll; ++u)
+      if (mine(w0 + u * WPT)) x[u].load(from(w0 + u * WPT) + lane * 8);
+    if (!angles) form_angles();
+    angles = true;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int w = w0 + u * kWarps;
-      if (w >= total) break;
-      const int i = w / n_vec, v = w - i * n_vec;
-      T* out = dst(i, v);
-      if (v < n_rot) {
-        float f[8], y[8];                // this lane's dims and their partners
-        x[u].get(f);
-        if (by_lane) {
+    for (int u = 0; u < kUnroll; ++u)
+      if (mine(w0 + u * WPT)) x[u].store(to(w0 + u * WPT) + lane * 8);
+  }
+  if (!angles) form_angles();                                   // a warp without vectors may have rotations
+  __syncwarp();
+  if ((half & 7) == 0) {
+    const int per = half >> 3, tasks = n_rot * per;             // lane tasks of a vector, of the token
+    constexpr int kPairs = sizeof(T) == 2 ? 4 : 2;
+    for (int i0 = sub * 32 + lane; i0 < tasks; i0 += kPairs * WPT * 32) {
+      Vec8<T> x[kPairs], y[kPairs];
+      int w[kPairs], d[kPairs];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = __shfl_sync(0xffffffffu, f[k], lane < apart ? lane + apart : lane - apart);
-        } else {
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) row[warp][lane * 8 + k] = f[k];
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int d = lane * 8 + k;
-            y[k] = d < a.half ? row[warp][d + a.half] : d < 2 * a.half ? row[warp][d - a.half] : 0.f;
-          }
-        }
-        if (lane * 8 < 2 * a.half) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int d = lane * 8 + k;
-            float oa, ob;
-            if (d < a.half) {
-              rope_pair(f[k], y[k], cs[i][d], sn[i][d], oa, ob);
-              f[k] = oa;
-            } else if (d < 2 * a.half) {
-              rope_pair(y[k], f[k], cs[i][d - a.half], sn[i][d - a.half], oa, ob);
-              f[k] = ob;
-            }
-          }
-          x[u].set(f);
+      for (int u = 0; u < kPairs; ++u) {
+        const int i = i0 + u * WPT * 32;
+        w[u] = i / per;
+        d[u] = (i - w[u] * per) * 8;
+        if (i >= tasks || !wanted(w[u])) w[u] = -1;
+        if (w[u] >= 0) {
+          x[u].load(from(w[u]) + d[u]);
+          y[u].load(from(w[u]) + half + d[u]);
         }
       }
-      if (out) x[u].store(out + lane * 8);
+#pragma unroll
+      for (int u = 0; u < kPairs; ++u) {
+        if (w[u] < 0) continue;
+        float fx[8], fy[8];
+        x[u].get(fx);
+        y[u].get(fy);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float oa, ob;
+          rope_pair(fx[e], fy[e], cs[d[u] + e], sn[d[u] + e], oa, ob);
+          fx[e] = oa;
+          fy[e] = ob;
+        }
+        x[u].set(fx);
+        y[u].set(fy);
+        x[u].store(to(w[u]) + d[u]);
+        y[u].store(to(w[u]) + half + d[u]);
+      }
+    }
+  } else {                                                      // pairs, then the dims that share their pieces
+    const int rest = mixed * 8 - 2 * half, per = half + rest;
+    for (int i = sub * 32 + lane; i < n_rot * per; i += WPT * 32) {
+      const int w = i / per, d = i - w * per;
+      if (!wanted(w)) continue;
+      if (d < half) {
+        float oa, ob;
+        rope_pair(IO<T>::to_f(from(w)[d]), IO<T>::to_f(from(w)[half + d]), cs[d], sn[d], oa, ob);
+        to(w)[d] = IO<T>::from_f(oa);
+        to(w)[half + d] = IO<T>::from_f(ob);
+      } else {
+        to(w)[half + d] = from(w)[half + d];
+      }
     }
   }
 }

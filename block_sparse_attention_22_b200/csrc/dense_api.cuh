@@ -624,14 +624,16 @@ QSA_API qsa_status_t qsa_append_kv(const qsa_config_t* cfg, const qsa_pages_t* p
         segs, n_segs, [&](const qsa_segment_t& sg) { return (int64_t)sg.q_len; },
         [&](const SegTable& t) -> cudaError_t {
           count_launch();
-          const int n = t.item0[t.n], per = n <= 4 * kNumSms ? 1 : append::kTokens;
-          const dim3 grid((unsigned)cdiv(n, per)), block(append::kThreads);
+          // one warp per token once that fills the GPU's warp slots about once
+          const int n = t.item0[t.n];
+          const bool many = n >= 16 * kNumSms;
+          const dim3 grid((unsigned)(many ? cdiv(n, append::kWarps) : n)), block(append::kThreads);
           const cudaStream_t s0 = (cudaStream_t)stream;
           if (cfg->dtype == QSA_DTYPE_BF16)
-            return per == 1 ? launch_chained(append_kernel<__nv_bfloat16, 1>, grid, block, 0, s0, g, t, a)
-                            : launch_chained(append_kernel<__nv_bfloat16, append::kTokens>, grid, block, 0, s0, g, t, a);
-          return per == 1 ? launch_chained(append_kernel<float, 1>, grid, block, 0, s0, g, t, a)
-                          : launch_chained(append_kernel<float, append::kTokens>, grid, block, 0, s0, g, t, a);
+            return many ? launch_chained(append_kernel<__nv_bfloat16, 1>, grid, block, 0, s0, g, t, a)
+                        : launch_chained(append_kernel<__nv_bfloat16, append::kWarps>, grid, block, 0, s0, g, t, a);
+          return many ? launch_chained(append_kernel<float, 1>, grid, block, 0, s0, g, t, a)
+                      : launch_chained(append_kernel<float, append::kWarps>, grid, block, 0, s0, g, t, a);
         });
   });
 }
