@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(append::kThreads)
   auto wanted = [&](int w) { return stored || (w >= g.G && w < n_rot); };
   // values, and the pieces of the rotated vectors behind the rotation; kUnroll
   // loads before the first store, which may alias them (q in place)
-  constexpr int kUnroll = sizeof(T) == 2 ? 8 : 4;
+  constexpr int kUnroll = sizeof(T) == 2 ? 6 : 4;
   const int mixed = (2 * half + 7) >> 3;                        // pieces with rotated dims
   auto form_angles = [&]() {
     for (int p = lane; p < half; p += 32) {
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(append::kThreads)
   __syncwarp();
   if ((half & 7) == 0) {
     const int per = half >> 3, tasks = n_rot * per;             // lane tasks of a vector, of the token
-    constexpr int kPairs = sizeof(T) == 2 ? 4 : 2;
+    constexpr int kPairs = 2;
     for (int i0 = sub * 32 + lane; i0 < tasks; i0 += kPairs * WPT * 32) {
       Vec8<T> x[kPairs], y[kPairs];
       int w[kPairs], d[kPairs];
