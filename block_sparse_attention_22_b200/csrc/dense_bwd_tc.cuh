@@ -186,11 +186,12 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
   DensePiece p;
   DenseUnit x;
   // the next piece of a segment that is not flagged (the same in every role and CTA)
-  auto next = [&]() -> bool {
-    while (walk.next(t, p, x))
-      if (!a.flags[t.slot[x.si]]) return true;
+  auto next_of = [&](DensePiece& np, DenseUnit& nx) -> bool {
+    while (walk.next(t, np, nx))
+      if (!a.flags[t.slot[nx.si]]) return true;
     return false;
   };
+  auto next = [&]() { return next_of(p, x); };
   // a stationary row in its token-major array
   auto unit_row = [&](int32_t row) -> int64_t {
     return kByKeys ? (int64_t)(t.q_offset[x.si] + row) * t.G + x.grp : dense_q_row(t, x, row, a.H);
@@ -343,8 +344,11 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const float tau2 = a.scale * 1.4426950408889634f;
     int64_t gc = 0, uc = 0;
-    // No early exit: after an abort every wait returns at once.
-    while (next()) {
+    // No early exit: after an abort every wait returns at once.  The next piece is
+    // looked up while this one's last product runs.
+    DensePiece p_next;
+    DenseUnit x_next;
+    for (bool more = next(); more; p = p_next, x = x_next) {
       const int n = p.c1 - p.c0;
       const int valid = x.nrows - (int)rank * 128;
       const bool active = li < valid;
@@ -462,6 +466,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
           if (kByKeys) mbar_arrive(&ctl.st_free[sbuf]);
         }
       }
+      more = next_of(p_next, x_next);
       mbar_wait_fast(&ctl.o_full, (uint32_t)(uc & 1), abort_flag);
       tc_fence_after();
       const bool whole = p.part < 0;

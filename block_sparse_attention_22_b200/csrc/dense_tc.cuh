@@ -125,18 +125,22 @@ template <int CG>
 __device__ __forceinline__ void load_q_rows(unsigned char* tile, const CUtensorMap* tokens, const CUtensorMap* rows,
                                             const DenseTable& t, const DenseUnit& x, int32_t row0, int n, int H,
                                             int lane, uint64_t* bar) {
-  const int h0 = row0 % t.hpg;
+  const int32_t tok0 = row0 / t.hpg;
+  const int h0 = row0 - tok0 * t.hpg;
   const int lead = h0 == 0 ? 0 : min(t.hpg - h0, n), whole = (n - lead) / t.hpg, tail = n - lead - whole * t.hpg;
-  for (int i = lane; i < 4 * whole; i += 32) {
-    const int r = lead + (i >> 2) * t.hpg;
-    sm100::tma_load_2d_leader<CG>(tile + (i & 3) * 16384 + r * 128, tokens, (i & 3) * 64,
-                                  (int32_t)dense_q_row(t, x, row0 + r, H), bar);
-  }
+  const int32_t y0 = (t.q_offset[x.si] + tok0) * H + x.grp * t.hpg;      // head 0 of the first row's token
+  const int32_t y1 = h0 == 0 ? y0 : y0 + H;                              // of the first whole token
+  const int slab = lane & 3;
+#pragma unroll 1
+  for (int k = lane >> 2; k < whole; k += 8)
+    sm100::tma_load_2d_leader<CG>(tile + slab * 16384 + (lead + k * t.hpg) * 128, tokens, slab * 64, y1 + k * H, bar);
   const int step = t.hpg & -t.hpg;
-  for (int i = lane; i < 4 * (lead + tail) / step; i += 32) {
-    const int e = (i >> 2) * step, r = e < lead ? e : n - tail + (e - lead);
-    sm100::tma_load_2d_leader<CG>(tile + (i & 3) * 16384 + r * 128, rows, (i & 3) * 64,
-                                  (int32_t)dense_q_row(t, x, row0 + r, H), bar);
+#pragma unroll 1
+  for (int e = (lane >> 2) * step; e < lead + tail; e += 8 * step) {
+    const bool first = e < lead;
+    const int r = first ? e : n - tail + (e - lead);
+    sm100::tma_load_2d_leader<CG>(tile + slab * 16384 + r * 128, rows, slab * 64,
+                                  first ? y0 + h0 + e : y1 + whole * H + (e - lead), bar);
   }
 }
 
@@ -395,20 +399,19 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       uint32_t word = 0;
       for (int i0 = 0; i0 < own; i0 += 32) {
         const int64_t my_off = i0 + lane < own ? kv_row<PAGED>(a.kv, t, x.si, x.grp, first + 1 + i0 + lane) : -1;
-        uint32_t bits = 0;
-#pragma unroll 8
-        for (int i = 0; i < 32; ++i) {
+        const int rows = min(32, own - i0);
+        uint32_t bits = 0;                                   // rows whose 8 dims of this lane hold one
+#pragma unroll 4
+        for (int i = 0; i < rows; ++i) {
           const int64_t off = __shfl_sync(0xffffffffu, my_off, i);
-          bool nf = false;
-          if (off >= 0) {
-            const uint4 v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.kv.v + off + lane * 8);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              nf |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
-          }
-          bits |= (__any_sync(0xffffffffu, nf) ? 1u : 0u) << i;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (off >= 0) v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.kv.v + off + lane * 8);
+          // an exponent of all ones carries into the sign bit
+          const uint32_t c = ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                             ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+          bits |= (c & 0x80008000u ? 1u : 0u) << i;
         }
+        bits = __reduce_or_sync(0xffffffffu, bits);
         if (lane == (i0 >> 5)) word = bits;
       }
       if (lane < 8) ctl.nf[uc % kNfBufs][lane] = word;
@@ -424,7 +427,10 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
     const float tau2 = a.scale * 1.4426950408889634f;
     int64_t gc = 0, uc = 0;
     // No early exit: the two warps of a quadrant meet at a named barrier per chunk.
-    while (walk.next(t, p, x)) {
+    // The next piece is looked up while this one's last product runs.
+    DensePiece p_next;
+    DenseUnit x_next;
+    for (bool more = walk.next(t, p, x); more; p = p_next, x = x_next) {
       const int n = p.c1 - p.c0;
       const int valid = x.nrows - (int)rank * 128;
       const bool active = li < valid, warp_active = quad * 32 < valid;
@@ -561,6 +567,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
         lt = ctl.red[gc & 1][0][li] + ctl.red[gc & 1][1][li];
         named_bar_sync(1 + quad, 64);                        // the next piece's first chunk writes this buffer
       }
+      more = walk.next(t, p_next, x_next);
       mbar_wait_fast(&ctl.o_full, (uint32_t)(uc & 1), abort_flag);
       tc_fence_after();
       if (warp_active) {
