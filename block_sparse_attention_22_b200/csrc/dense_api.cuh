@@ -99,29 +99,26 @@ void cut_table(DenseTable& t, DenseSplits& sp, const DenseKind& kind) {
   int64_t tail = 0, whole = 0;
   for (int u = tail0; u < n_units; ++u) tail += chunks[u] + kUnitCost;
   for (int c = 0; c < grid; ++c) whole += best[c];
-  // cuts for CTAs filled up to `share` (at least kMinTail chunks at a time); true if that holds everything
+  // cuts for CTAs filled up to `share`, never leaving less than kMinTail chunks on
+  // either side of a cut; true if that holds everything
   auto lay = [&](int64_t share) -> bool {
     int u = tail0;
     int64_t at = 0;                     // chunks of unit u already taken
-    int64_t carry = 0;                  // what the CTAs so far took too little (or too much, negative)
     for (int c = 0; c < grid; ++c) {
       t.cut[c] = {u, (int32_t)at};
-      int64_t want = carry + std::max<int64_t>(share - best[c], kMinTail + kUnitCost);
-      while (u < n_units && want > 0) {
+      int64_t want = share - best[c];
+      while (u < n_units) {
         const int64_t left = chunks[u] - at;
-        if (want >= left + kUnitCost || left + kUnitCost - want < kMinTail) {
+        if (left + kUnitCost <= want) {
           want -= left + kUnitCost;
           ++u;
           at = 0;
-        } else {
-          if (want - kUnitCost >= kMinTail) {
-            at += want - kUnitCost;
-            want = 0;
-          }
-          break;
+          continue;
         }
+        const int64_t take = std::min(want - kUnitCost, left - kMinTail);
+        if (take >= kMinTail) at += take;
+        break;
       }
-      carry = want;
     }
     return u >= n_units;
   };
@@ -239,7 +236,7 @@ std::vector<DenseGroup> dense_groups(const Geo& g, bool tc, bool paged, const qs
     using N = dense_tc::Shape<1>;
     using W = dense_tc::Shape<2>;
     narrow.kind = {N::kRows, N::kKeys, N::kGrid, false};
-    wide.kind = {W::kRows, W::kKeys, W::kGrid, false};
+    wide.kind = {W::kRows, W::kKeys, W::kGrid, false, 4, 4};      // a unit's 5.5 us in chunks of 1.4 us
     decode.kind = {dense_decode::kRows, dense_decode::kKeys, kNumSms, false, 1, 1};
   } else {
     narrow.kind = {dense_simt::kRowsNarrow, dense_simt::kKeys, kNumSms, false};
@@ -407,7 +404,7 @@ struct DenseBwdPlan {
 };
 
 DenseKind dense_bwd_kind(bool tc, bool by_keys) {
-  if (tc) return {dense_bwd::kRows, dense_bwd::kKeys, dense_bwd::kGrid, by_keys};
+  if (tc) return {dense_bwd::kRows, dense_bwd::kKeys, dense_bwd::kGrid, by_keys, 3, 4};      // 6 us, 2.1 us
   using namespace dense_simt;
   return by_keys ? DenseKind{kBKeys, kBRows, kNumSms, true, 1, 1, 2 * kBKeys}
                  : DenseKind{kBRows, kBKeys, kNumSms, false, 1, 1};
