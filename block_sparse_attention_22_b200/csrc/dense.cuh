@@ -26,6 +26,17 @@ constexpr int kMaxGrid = 148;              // CTAs (or CTA pairs) a table is cut
 constexpr int kPartFloats = kHeadDim + 4;  // a row's partial: 256 sums, maximum and sum of its softmax, 2 unused
 }  // namespace dense
 
+// A kernel that needs nothing from the one launched before it, only what that
+// one itself waited for, runs beside its last CTAs: it waits for it at its end
+// instead of its start (`late`), so that the kernels after it may rely on both.
+__device__ __forceinline__ void dense_wait_first(bool late) {
+  if (!late) pdl_wait();
+  pdl_trigger();
+}
+__device__ __forceinline__ void dense_wait_last(bool late) {
+  if (late) pdl_wait();
+}
+
 struct DensePoint {
   int32_t unit, chunk;
 };

@@ -200,6 +200,7 @@ qsa_status_t for_each_dense(const Geo& g, std::vector<qsa_segment_t> segs, const
 struct DenseLaunch {
   DenseTable t;
   DenseSplits sp;
+  size_t part;                           // offset of its partial results
 };
 
 // Bytes of a table's partial results.
@@ -207,12 +208,12 @@ size_t partial_bytes(const DenseTable& t, const DenseSplits& sp) {
   return sp.n > 0 ? (size_t)2 * t.grid * t.prows * dense::kPartFloats * 4 : 0;
 }
 
-// The launches of one kind for the segments; `part` grows to the largest's partial results.
+// The launches of one kind for the segments; `part` grows by their partial results.
 qsa_status_t plan_launches(const Geo& g, const std::vector<qsa_segment_t>& segs, const DenseKind& kind,
                            std::vector<DenseLaunch>& out, size_t& part) {
   return for_each_dense(g, segs, kind, [&](const DenseTable& t, const DenseSplits& sp) {
-    out.push_back({t, sp});
-    part = std::max(part, partial_bytes(t, sp));
+    out.push_back({t, sp, part});
+    part += align_up(partial_bytes(t, sp), 256);
     return QSA_OK;
   });
 }
@@ -266,7 +267,6 @@ qsa_status_t plan_dense_fwd(const Geo& g, bool tc, bool paged, const qsa_segment
     const qsa_status_t r = plan_launches(g, d.segs, d.kind, d.launches, ws);
     if (r != QSA_OK) return r;
   }
-  ws = align_up(ws, 256);
   return QSA_OK;
 }
 
@@ -359,13 +359,12 @@ qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int
   if (r != QSA_OK) return r;
   if (need > 0 && (!ws || ws_bytes < need)) return QSA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return QSA_ERR_INVALID_ARG;
-  float* part = (float*)ws;
   CUtensorMap m[4];                      // K, V, Q by whole tokens, Q by parts of one
   DenseTcArgs a;
   if (tc) {
     if ((int64_t)n_tokens * g.H > INT32_MAX - 512) return QSA_ERR_UNSUPPORTED;      // TMA row coordinates
-    a = {kv, (const __nv_bfloat16*)q, (__nv_bfloat16*)o, lse, part, g.H, PAGED ? dense_box(kv.page_tokens) : 64,
-         g.scale};
+    a = {kv, (const __nv_bfloat16*)q, (__nv_bfloat16*)o, lse, nullptr, g.H, PAGED ? dense_box(kv.page_tokens) : 64,
+         g.scale, false};
     if ((groups.size() > 1 || groups[0].form != DenseForm::kDecode) &&      // decode takes no maps
         (!make_dense_map(&m[0], kv.k, kv_rows, kv_groups, a.box) ||
          !make_dense_map(&m[1], kv.v, kv_rows, kv_groups, a.box) ||
@@ -373,20 +372,29 @@ qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int
          !make_dense_map(&m[3], q, (int64_t)n_tokens * g.H, 1, g.hpg & -g.hpg)))
       return QSA_ERR_CUDA;
   }
+  // every launch's kernel, each after the first beside the one before; then the joins
+  auto part_of = [&](const DenseLaunch& x) { return (float*)((char*)ws + x.part); };
+  a.late = false;
   for (const DenseGroup& d : groups)
     for (const DenseLaunch& x : d.launches) {
       const bool is_wide = d.form == DenseForm::kWide;
+      a.part = part_of(x);
       cudaError_t e;
       if (d.form == DenseForm::kDecode)
         e = launch_dense_decode(x.t, a, st);
       else if (tc)
         e = is_wide ? launch_dense_tc<2, PAGED>(x.t, m, a, st) : launch_dense_tc<1, PAGED>(x.t, m, a, st);
       else
-        e = is_wide ? launch_dense_simt<dense_simt::kRowsWide, PAGED>(g, x.t, kv, q, o, lse, part, st)
-                    : launch_dense_simt<dense_simt::kRowsNarrow, PAGED>(g, x.t, kv, q, o, lse, part, st);
-      if (e == cudaSuccess && x.sp.n > 0)
-        e = tc ? launch_dense_combine<__nv_bfloat16>(g, x.t, x.sp, part, o, lse, st)
-               : launch_dense_combine<float>(g, x.t, x.sp, part, o, lse, st);
+        e = is_wide ? launch_dense_simt<dense_simt::kRowsWide, PAGED>(g, x.t, kv, q, o, lse, a.part, st)
+                    : launch_dense_simt<dense_simt::kRowsNarrow, PAGED>(g, x.t, kv, q, o, lse, a.part, st);
+      if (e != cudaSuccess) return QSA_ERR_CUDA;
+      a.late = true;
+    }
+  for (const DenseGroup& d : groups)
+    for (const DenseLaunch& x : d.launches) {
+      if (x.sp.n == 0) continue;
+      const cudaError_t e = tc ? launch_dense_combine<__nv_bfloat16>(g, x.t, x.sp, part_of(x), o, lse, st)
+                               : launch_dense_combine<float>(g, x.t, x.sp, part_of(x), o, lse, st);
       if (e != cudaSuccess) return QSA_ERR_CUDA;
     }
   return QSA_OK;
@@ -395,12 +403,12 @@ qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int
 // ------------------------------------------------------------------ backward
 // Workspace of the gradient: delta by token; for bf16 also the statistics by
 // head (segments padded to whole tiles) and the segments' flags; the partial
-// results of the cut units (of one kernel at a time).
+// results of the cut units, the keys' launches' twice (dv, dk).
 struct DenseBwdPlan {
   std::vector<qsa_segment_t> segs;       // non-empty; slot: the segment's first statistics tile
   std::vector<DenseLaunch> rows, keys;   // launches by rows (dq) and by keys (dk, dv)
   int64_t stat_rows = 0;
-  size_t off_lse2 = 0, off_delta_h = 0, off_flags = 0, flag_bytes = 0, off_part = 0, bytes = 0;
+  size_t off_lse2 = 0, off_delta_h = 0, off_flags = 0, flag_bytes = 0, off_part = 0, off_part2 = 0, bytes = 0;
 };
 
 DenseKind dense_bwd_kind(bool tc, bool by_keys) {
@@ -432,8 +440,10 @@ qsa_status_t plan_dense_bwd(const Geo& g, bool tc, const qsa_segment_t* segs, in
   p.off_part = at;
   size_t part = 0;
   qsa_status_t r = plan_launches(g, p.segs, dense_bwd_kind(tc, false), p.rows, part);
+  const size_t part_rows = part;
   if (r == QSA_OK) r = plan_launches(g, p.segs, dense_bwd_kind(tc, true), p.keys, part);
-  p.bytes = at + align_up(part, 256);
+  p.off_part2 = at + part - part_rows;   // the keys' offsets start behind the rows'
+  p.bytes = at + part + (tc ? part - part_rows : 0);
   return r;
 }
 
@@ -444,19 +454,19 @@ size_t dense_bwd_ws(const Geo& g, bool tc, const qsa_segment_t* segs, int n, int
 
 // Joins the cut units of a gradient launch.
 template <typename T>
-cudaError_t launch_bwd_combine(const Geo& g, const DenseLaunch& x, const float* part, const int32_t* flags, void* out,
+cudaError_t launch_bwd_combine(const Geo& g, const DenseLaunch& x, const char* parts, const int32_t* flags, void* out,
                                float factor, void* out2, cudaStream_t st) {
   if (x.sp.n == 0) return cudaSuccess;
   count_launch();
   return launch_chained(dense_bwd_combine_kernel<T>,
                         dim3(x.sp.n, (unsigned)cdiv(std::min(x.t.prows, x.t.rows), 4)), dim3(128), 0, st, x.t, x.sp,
-                        part, flags, (T*)out, factor, (T*)out2, dense_simt::kBKeys, g.H);
+                        (const float*)(parts + x.part), flags, (T*)out, factor, (T*)out2, dense_simt::kBKeys, g.H);
 }
 
 // The CUDA-core gradient over the given launches.
 template <typename T>
 qsa_status_t run_dense_bwd_simt(const Geo& g, const std::vector<DenseLaunch>& rows,
-                                const std::vector<DenseLaunch>& keys, const DenseBwdArgs& a, float* part,
+                                const std::vector<DenseLaunch>& keys, const DenseBwdArgs& a, char* parts,
                                 cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(dense_dq_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        dense_simt::kBwdSmem);
@@ -467,14 +477,16 @@ qsa_status_t run_dense_bwd_simt(const Geo& g, const std::vector<DenseLaunch>& ro
   for (const DenseLaunch& x : rows) {
     if (e != cudaSuccess) break;
     count_launch();
-    e = launch_chained(dense_dq_simt_kernel<T>, dim3(x.t.grid), block, dense_simt::kBwdSmem, st, x.t, a, part);
-    if (e == cudaSuccess) e = launch_bwd_combine<T>(g, x, part, nullptr, a.dq, g.scale, nullptr, st);
+    e = launch_chained(dense_dq_simt_kernel<T>, dim3(x.t.grid), block, dense_simt::kBwdSmem, st, x.t, a,
+                       (float*)(parts + x.part));
+    if (e == cudaSuccess) e = launch_bwd_combine<T>(g, x, parts, nullptr, a.dq, g.scale, nullptr, st);
   }
   for (const DenseLaunch& x : keys) {
     if (e != cudaSuccess) break;
     count_launch();
-    e = launch_chained(dense_dkv_simt_kernel<T>, dim3(x.t.grid), block, dense_simt::kBwdSmem, st, x.t, a, part);
-    if (e == cudaSuccess) e = launch_bwd_combine<T>(g, x, part, nullptr, a.dk, g.scale, a.dv, st);
+    e = launch_chained(dense_dkv_simt_kernel<T>, dim3(x.t.grid), block, dense_simt::kBwdSmem, st, x.t, a,
+                       (float*)(parts + x.part));
+    if (e == cudaSuccess) e = launch_bwd_combine<T>(g, x, parts, nullptr, a.dk, g.scale, a.dv, st);
   }
   return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
@@ -488,12 +500,12 @@ qsa_status_t run_dense_bwd_f32(const Geo& g, const DenseBwdPlan& p, const DenseB
         return launch_chained(dense_delta_kernel<float>, dim3((unsigned)cdiv((int64_t)t.item0[t.n] * g.H, 8)),
                               dim3(256), 0, st, t, (const float*)o, (const float*)a.dout, (float*)ws, g.H);
       });
-  return r != QSA_OK ? r : run_dense_bwd_simt<float>(g, p.rows, p.keys, a, (float*)(ws + p.off_part), st);
+  return r != QSA_OK ? r : run_dense_bwd_simt<float>(g, p.rows, p.keys, a, ws + p.off_part, st);
 }
 
-// One gradient on the tensor cores: its kernel, then the join of its cut units.
+// One gradient on the tensor cores; partial results from `parts` on.
 template <dense_bwd::Grad M>
-qsa_status_t run_dense_grad_tc(const Geo& g, const DenseBwdPlan& p, const DenseBwdMaps& m, const DenseBwdTcArgs& a,
+qsa_status_t run_dense_grad_tc(const DenseBwdPlan& p, const DenseBwdMaps& m, DenseBwdTcArgs a, char* parts,
                                cudaStream_t st) {
   auto kernel = dense_bwd_tc_kernel<M>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense_bwd::kSmemBytes);
@@ -512,11 +524,10 @@ qsa_status_t run_dense_grad_tc(const Geo& g, const DenseBwdPlan& p, const DenseB
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    a.part = (float*)(parts + x.part);
     count_launch();
     e = cudaLaunchKernelEx(&cfg, kernel, m, x.t, a);
-    if (e == cudaSuccess)
-      e = launch_bwd_combine<__nv_bfloat16>(g, x, a.part, a.flags, a.out, M == dense_bwd::kDv ? 1.f : g.scale, nullptr,
-                                            st);
+    a.late = true;
   }
   return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
@@ -547,13 +558,24 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
                               delta_h, flags, p.stat_rows, g.H, g.G);
       });
   if (r != QSA_OK) return r;
-  DenseBwdTcArgs b{lse2_h, delta_h, flags, (B*)a.dv, (float*)(ws + p.off_part),
-                   p.stat_rows, g.H, g.scale};
-  if ((r = run_dense_grad_tc<dense_bwd::kDv>(g, p, {mq, mq, mo, mk, mv, mk, mv}, b, st)) != QSA_OK) return r;
+  // the three kernels beside each other's ends, then the joins of their cut units
+  char* const parts = ws + p.off_part;
+  char* const parts2 = ws + p.off_part2;
+  DenseBwdTcArgs b{lse2_h, delta_h, flags, (B*)a.dv, nullptr, p.stat_rows, g.H, g.scale, false};
+  if ((r = run_dense_grad_tc<dense_bwd::kDv>(p, {mq, mq, mo, mk, mv, mk, mv}, b, parts, st)) != QSA_OK) return r;
+  b.late = true;
   b.out = (B*)a.dk;
-  if ((r = run_dense_grad_tc<dense_bwd::kDk>(g, p, {mq, mo, mq, mk, mv, mk, mv}, b, st)) != QSA_OK) return r;
+  if ((r = run_dense_grad_tc<dense_bwd::kDk>(p, {mq, mo, mq, mk, mv, mk, mv}, b, parts2, st)) != QSA_OK) return r;
   b.out = (B*)a.dq;
-  if ((r = run_dense_grad_tc<dense_bwd::kDq>(g, p, {mk, mv, mk, tq, to, rq, ro}, b, st)) != QSA_OK) return r;
+  if ((r = run_dense_grad_tc<dense_bwd::kDq>(p, {mk, mv, mk, tq, to, rq, ro}, b, parts, st)) != QSA_OK) return r;
+  cudaError_t e = cudaSuccess;
+  for (const DenseLaunch& x : p.keys) {
+    if (e == cudaSuccess) e = launch_bwd_combine<B>(g, x, parts, flags, a.dv, 1.f, nullptr, st);
+    if (e == cudaSuccess) e = launch_bwd_combine<B>(g, x, parts2, flags, a.dk, g.scale, nullptr, st);
+  }
+  for (const DenseLaunch& x : p.rows)
+    if (e == cudaSuccess) e = launch_bwd_combine<B>(g, x, parts, flags, a.dq, g.scale, nullptr, st);
+  if (e != cudaSuccess) return QSA_ERR_CUDA;
   // the flagged segments; their launches are not levelled (there are hardly ever any)
   a.flags = flags;
   std::vector<DenseLaunch> by_rows, by_keys;
@@ -562,7 +584,7 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
   kr.level = kk.level = false;
   if ((r = plan_launches(g, p.segs, kr, by_rows, part)) != QSA_OK) return r;
   if ((r = plan_launches(g, p.segs, kk, by_keys, part)) != QSA_OK) return r;
-  return run_dense_bwd_simt<B>(g, by_rows, by_keys, a, nullptr, st);
+  return run_dense_bwd_simt<B>(g, by_rows, by_keys, a, ws, st);      // no unit is cut
 }
 
 // Runs an entry point's body; host memory that runs out is an error code, not

@@ -85,6 +85,7 @@ struct DenseBwdTcArgs {
   int64_t stat_rows;
   int H;
   float scale;
+  bool late;                  // dense_wait_first
 };
 
 struct DenseBwdTcCtl {
@@ -178,8 +179,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  pdl_wait();
-  pdl_trigger();
+  dense_wait_first(a.late);
 
   DenseWalk walk;
   walk.init(t, cta);
@@ -501,6 +501,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     tc_fence_after();
     tmem_dealloc_cg<2>(tmem, dense_tc::kTmemCols);
   }
+  dense_wait_last(a.late);
 }
 
 // Row statistics for the gradient kernels, one warp per (token, head): delta =

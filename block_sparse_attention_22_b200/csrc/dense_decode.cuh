@@ -69,8 +69,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
   // 16-byte piece `piece` of line r of a tile, swizzled so that eight lines of one piece hit all banks
   auto at = [](int r, int piece) { return (uint32_t)(r * (kHeadDim * 2) + ((piece ^ (r & 7)) << 4)); };
   const int mi = lane >> 3, ml = lane & 7;              // this lane's matrix and line of an ldmatrix.x4
-  pdl_wait();
-  pdl_trigger();
+  dense_wait_first(a.late);
   DenseWalk walk;
   walk.init(t, blockIdx.x);
   DensePiece p;
@@ -265,6 +264,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
     }
     __syncthreads();                                      // shared memory free for the next piece
   }
+  dense_wait_last(a.late);
 }
 
 }  // namespace qsa

@@ -83,6 +83,7 @@ struct DenseTcArgs {
   int H;
   int box;                  // rows of a TMA box: keys that are contiguous in the cache
   float scale;
+  bool late;                // dense_wait_first
 };
 
 struct DenseTcCtl {
@@ -247,8 +248,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
   if constexpr (CG == 2) cluster_sync_all(); else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
-  pdl_wait();
-  pdl_trigger();
+  dense_wait_first(a.late);
 
   DenseWalk walk;
   walk.init(t, cta);
@@ -636,6 +636,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
     tc_fence_after();
     tmem_dealloc_cg<CG>(tmem, kTmemCols);
   }
+  dense_wait_last(a.late);
 }
 
 }  // namespace qsa
