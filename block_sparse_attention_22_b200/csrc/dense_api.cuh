@@ -558,16 +558,18 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
                               delta_h, flags, p.stat_rows, g.H, g.G);
       });
   if (r != QSA_OK) return r;
-  // the three kernels beside each other's ends, then the joins of their cut units
+  // dq, beside its end dv, then dk (which reads delta as dq leaves it); then the
+  // joins of their cut units
   char* const parts = ws + p.off_part;
   char* const parts2 = ws + p.off_part2;
-  DenseBwdTcArgs b{lse2_h, delta_h, flags, (B*)a.dv, nullptr, p.stat_rows, g.H, g.scale, false};
-  if ((r = run_dense_grad_tc<dense_bwd::kDv>(p, {mq, mq, mo, mk, mv, mk, mv}, b, parts, st)) != QSA_OK) return r;
+  DenseBwdTcArgs b{lse2_h, delta_h, flags, (B*)a.dq, nullptr, p.stat_rows, g.H, g.scale, false};
+  if ((r = run_dense_grad_tc<dense_bwd::kDq>(p, {mk, mv, mk, tq, to, rq, ro}, b, parts, st)) != QSA_OK) return r;
   b.late = true;
+  b.out = (B*)a.dv;
+  if ((r = run_dense_grad_tc<dense_bwd::kDv>(p, {mq, mq, mo, mk, mv, mk, mv}, b, parts, st)) != QSA_OK) return r;
+  b.late = false;
   b.out = (B*)a.dk;
   if ((r = run_dense_grad_tc<dense_bwd::kDk>(p, {mq, mo, mq, mk, mv, mk, mv}, b, parts2, st)) != QSA_OK) return r;
-  b.out = (B*)a.dq;
-  if ((r = run_dense_grad_tc<dense_bwd::kDq>(p, {mk, mv, mk, tq, to, rq, ro}, b, parts, st)) != QSA_OK) return r;
   cudaError_t e = cudaSuccess;
   for (const DenseLaunch& x : p.keys) {
     if (e == cudaSuccess) e = launch_bwd_combine<B>(g, x, parts, flags, a.dv, 1.f, nullptr, st);

@@ -25,7 +25,10 @@
 // dS alone makes the error of dq and dk 1.42 times that of rounding the result,
 // 1.50 with delta's (o comes rounded); the remainders of a quarter of the columns
 // (kLo) are therefore multiplied too, from the columns that dS leaves free: 1.41,
-// for 3% of the training step's time (all remainders: 1.11, 11%).
+// for 3% of the training step's time (all remainders: 1.11, 11%).  Rows of few
+// keys have an o as large as v, and delta's error is then several times dS's:
+// where a unit's keys are one chunk, the dQ kernel forms delta as the sum of P dP
+// instead and leaves it for the dK kernel.
 //
 // Roles per CTA (12 warps): eight softmax warps (two per lane quadrant, each
 // thread one lane and 64 of a chunk's columns), one TMA producer, one warp that
@@ -83,7 +86,7 @@ struct DenseBwdMaps {
 
 struct DenseBwdTcArgs {
   const float* lse2;          // [H][stat rows] lse * log2 e, +inf behind a segment's end
-  const float* delta;         // [H][stat rows]
+  float* delta;               // [H][stat rows]; rows of units of one chunk are rewritten by dQ
   const int32_t* flags;       // by first statistics tile of a segment: not for these kernels
   __nv_bfloat16* out;
   float* part;
@@ -368,8 +371,9 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       const int32_t own = kByKeys ? x.row0 + (int)rank * 128 + li : row / t.hpg;   // position
       const int64_t at = unit_row(row);
       float lse2 = 0.f, delta = 0.f;                 // of this thread's row (dQ)
+      int64_t sat = 0;
       if (!kByKeys) {
-        const int64_t sat = (int64_t)(x.grp * t.hpg + row - own * t.hpg) * a.stat_rows +
+        sat = (int64_t)(x.grp * t.hpg + row - own * t.hpg) * a.stat_rows +
                             (int64_t)t.slot[x.si] * kStatTile + own;
         lse2 = a.lse2[sat];
         delta = a.delta[sat];
@@ -438,6 +442,22 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
           dst = lane_addr + kTmemP + half * 64;
           mbar_wait_fast(&ctl.dp_done, (uint32_t)(gc & 1), abort_flag);
           tc_fence_after();
+          if (M == kDq && x.nchunks == 1) {          // delta from the row's own P and dP
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 64; k += 16) {
+              float v[16];
+              tmem_ld16(dst + k, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum += k + i < hi ? w[k + i] * v[i] : 0.f;
+            }
+            stats[half * 128 + li] = sum;
+            named_bar_sync(1 + quad, 64);
+            delta = stats[li] + stats[128 + li];
+            if (active && half == 0) a.delta[sat] = delta;
+            named_bar_sync(1 + quad, 64);            // read before the next unit's sums
+          }
 #pragma unroll
           for (int k = 0; k < 64; k += 32) {
             float v[2][16];
