@@ -80,14 +80,28 @@ __device__ __forceinline__ void simt_store4(__nv_bfloat16* dst, float a, float b
   *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<uint32_t*>(&x), *reinterpret_cast<uint32_t*>(&y));
 }
 
-// out[i][j] = a row (ra + i) . b row (rb + 16 j), rows of 256 floats
+// Two fp32 products and sums in one instruction: the FMA pipe's rate is the
+// same, but at two warps per scheduler its issue slots are what runs short.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 lo2(const float4& x) { return make_float2(x.x, x.y); }
+__device__ __forceinline__ float2 hi2(const float4& x) { return make_float2(x.z, x.w); }
+
+// out[i][j] = a row (ra + i) . b row (rb + 16 j), rows of 256 floats (sums of the
+// even and odd dims, then of both)
 template <int R, int N>
 __device__ __forceinline__ void simt_dots(const float* a, const float* b, int ra, int rb, float (&out)[R][N]) {
   using dense_simt::kLd;
+  float2 acc[R][N];
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int j = 0; j < N; ++j) out[i][j] = 0.f;
+    for (int j = 0; j < N; ++j) acc[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 2
   for (int d = 0; d < kHeadDim; d += 4) {
     float4 x[R], y[N];
@@ -99,12 +113,14 @@ __device__ __forceinline__ void simt_dots(const float* a, const float* b, int ra
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        out[i][j] = fmaf(x[i].x, y[j].x, out[i][j]);
-        out[i][j] = fmaf(x[i].y, y[j].y, out[i][j]);
-        out[i][j] = fmaf(x[i].z, y[j].z, out[i][j]);
-        out[i][j] = fmaf(x[i].w, y[j].w, out[i][j]);
+        acc[i][j] = fma2(lo2(x[i]), lo2(y[j]), acc[i][j]);
+        acc[i][j] = fma2(hi2(x[i]), hi2(y[j]), acc[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) out[i][j] = acc[i][j].x + acc[i][j].y;
 }
 
 // acc[i][16] += sum over n keys of p[row ra + i][key] * b[key][dims]; the
@@ -129,10 +145,9 @@ __device__ __forceinline__ void simt_accumulate(const float* p, int ldp, const f
         if (limited && k + kk >= limit[i]) continue;
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
-          acc[i][4 * jj] = fmaf(f, y[jj].x, acc[i][4 * jj]);
-          acc[i][4 * jj + 1] = fmaf(f, y[jj].y, acc[i][4 * jj + 1]);
-          acc[i][4 * jj + 2] = fmaf(f, y[jj].z, acc[i][4 * jj + 2]);
-          acc[i][4 * jj + 3] = fmaf(f, y[jj].w, acc[i][4 * jj + 3]);
+          float2* d = reinterpret_cast<float2*>(&acc[i][4 * jj]);
+          d[0] = fma2(make_float2(f, f), lo2(y[jj]), d[0]);
+          d[1] = fma2(make_float2(f, f), hi2(y[jj]), d[1]);
         }
       }
     }
@@ -140,7 +155,7 @@ __device__ __forceinline__ void simt_accumulate(const float* p, int ldp, const f
 }
 
 template <int ROWS, bool PAGED>
-__global__ void __launch_bounds__(dense_simt::kThreads)
+__global__ void __launch_bounds__(dense_simt::kThreads, 1)
     dense_fwd_simt_kernel(const __grid_constant__ DenseTable t, KvSource kv, const float* q, float* o, float* lse,
                           float* part, int H, float scale) {
   using namespace dense_simt;
@@ -302,17 +317,14 @@ __global__ void __launch_bounds__(256)
   if (lane == 0) delta[at] = s;
 }
 
-// P and dS of 64 rows x 32 keys into Ps and Ds ([row][key]); row statistics in
-// st_lse (log2 units) and st_delta; masked entries are zero.  row_pos0: the
-// tile's first row, in rows of the segment.
-__device__ __forceinline__ void simt_p_ds(const float* Qs, const float* Os, const float* Ks, const float* Vs,
-                                          float* Ps, float* Ds, const float* st_lse, const float* st_delta,
-                                          int32_t row0, int nrows, int hpg, int32_t j0, int32_t n_keys, float s2) {
+// From a thread's scores and dP of 64 rows x 32 keys, P (if Ps) and dS into shared
+// memory ([row][key]); row statistics in st_lse (log2 units) and st_delta; masked
+// entries are zero.  row0: the tile's first row, in rows of the segment.
+__device__ __forceinline__ void simt_p_ds(const float (&s)[4][2], const float (&dp)[4][2], float* Ps, float* Ds,
+                                          const float* st_lse, const float* st_delta, int32_t row0, int nrows, int hpg,
+                                          int32_t j0, int32_t n_keys, float s2) {
   using namespace dense_simt;
   const int tx = threadIdx.x & 15, ra = (threadIdx.x >> 4) * 4;
-  float s[4][2], dp[4][2];
-  simt_dots<4, 2>(Qs, Ks, ra, tx, s);
-  simt_dots<4, 2>(Os, Vs, ra, tx, dp);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ra + i;
@@ -322,7 +334,7 @@ __device__ __forceinline__ void simt_p_ds(const float* Qs, const float* Os, cons
       const int key = tx + 16 * j;
       const bool seen = r < nrows && j0 + key <= pos && j0 + key < n_keys;
       const float p = seen ? exp2f(fmaf(s[i][j], s2, -st_lse[r])) : 0.f;
-      Ps[r * kBLd + key] = p;
+      if (Ps) Ps[r * kBLd + key] = p;
       Ds[r * kBLd + key] = seen ? p * (dp[i][j] - st_delta[r]) : 0.f;
     }
   }
@@ -341,7 +353,7 @@ __device__ __forceinline__ bool simt_any(const Table& t, const int32_t* flags) {
 // dq of tiles of 64 rows, in chunks of 32 keys (dense.cuh); a piece of a cut
 // unit leaves its unscaled sum.
 template <typename T>
-__global__ void __launch_bounds__(dense_simt::kThreads)
+__global__ void __launch_bounds__(dense_simt::kThreads, 1)
     dense_dq_simt_kernel(const __grid_constant__ DenseTable t, DenseBwdArgs a, float* part) {
   using namespace dense_simt;
   extern __shared__ __align__(16) float sm[];
@@ -379,31 +391,43 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
       st_lse[threadIdx.x] = v ? a.lse[q_at(threadIdx.x)] * 1.4426950408889634f : 0.f;
       st_delta[threadIdx.x] = v ? a.delta[q_at(threadIdx.x)] : 0.f;
     }
+    auto load_keys = [&](float* dst, const void* base, int c) {
+      simt_load_rows(dst, kBKeys, (const T*)base, [&](int r) -> const T* {
+        const int32_t j = c * kBKeys + r;
+        return j < x.kv_len ? (const T*)base + ((int64_t)(t.q_offset[si] + j) * t.G + x.grp) * kHeadDim : nullptr;
+      });
+    };
+    load_keys(Vs, a.v, p.c0);
+    sm100::cp_async_commit();
+    load_keys(Ks, a.k, p.c0);
+    sm100::cp_async_commit();
     float acc[4][16];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][k] = 0.f;
     const int32_t first_pos = x.row0 / t.hpg;
+    // V of the next chunk loads under this one's sum, K under the next one's dP
     for (int c = p.c0; c < p.c1; ++c) {
       const int32_t j0 = c * kBKeys;
+      float sc[4][2], dp[4][2];
+      sm100::cp_async_wait<1>();
       __syncthreads();
-      auto keys_of = [&](const void* base) {
-        return [&, base](int r) -> const T* {
-          const int32_t j = j0 + r;
-          return j < x.kv_len ? (const T*)base + ((int64_t)(t.q_offset[si] + j) * t.G + x.grp) * kHeadDim : nullptr;
-        };
-      };
-      simt_load_rows(Ks, kBKeys, (const T*)a.k, keys_of(a.k));
-      simt_load_rows(Vs, kBKeys, (const T*)a.v, keys_of(a.v));
-      sm100::cp_async_wait_all();
+      simt_dots<4, 2>(Os, Vs, ra, tx, dp);
+      sm100::cp_async_wait<0>();
       __syncthreads();
-      simt_p_ds(Qs, Os, Ks, Vs, Ps, Ds, st_lse, st_delta, x.row0, x.nrows, t.hpg, j0, x.kv_len, s2);
+      simt_dots<4, 2>(Qs, Ks, ra, tx, sc);
+      simt_p_ds(sc, dp, nullptr, Ds, st_lse, st_delta, x.row0, x.nrows, t.hpg, j0, x.kv_len, s2);
       __syncthreads();
+      if (c + 1 < p.c1) load_keys(Vs, a.v, c + 1);
+      sm100::cp_async_commit();
       int limit[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) limit[i] = min(kBKeys, (x.row0 + ra + i) / t.hpg - j0 + 1);
       simt_accumulate<4>(Ds, kBLd, Ks, ra, tx, kBKeys, j0 + kBKeys - 1 > first_pos, limit, acc);
+      __syncthreads();
+      if (c + 1 < p.c1) load_keys(Ks, a.k, c + 1);
+      sm100::cp_async_commit();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -430,7 +454,7 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
 // its unscaled sums, dv's rows kBKeys behind dk's.  (One block per unit held 64 of
 // 148 SMs at 989 tokens x 2 groups, and the longest of them 3.5 ms.)
 template <typename T>
-__global__ void __launch_bounds__(dense_simt::kThreads)
+__global__ void __launch_bounds__(dense_simt::kThreads, 1)
     dense_dkv_simt_kernel(const __grid_constant__ DenseTable t, DenseBwdArgs a, float* part) {
   using namespace dense_simt;
   extern __shared__ __align__(16) float sm[];
@@ -467,56 +491,69 @@ __global__ void __launch_bounds__(dense_simt::kThreads)
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) dk[i][k] = dv[i][k] = 0.f;
-    for (int c = p.c0; c < p.c1; ++c) {
-      const int32_t i0 = j0 + c / t.hpg * kBRows;                     // first token of the chunk
+    // rows of chunk c: 64 tokens of one head
+    auto load_chunk = [&](float* dst, const void* base, int c, bool stats) {
+      const int32_t i0 = j0 + c / t.hpg * kBRows;
       const int nrows = min(kBRows, n - i0);
-      const int64_t head = x.grp * t.hpg + c % t.hpg;
-      auto q_at = [&](int r) { return (q0 + i0 + r) * a.H + head; };
-      auto rows_of = [&](const void* base) {
-        return [&, base](int r) -> const T* {
-          return r < nrows ? (const T*)base + q_at(r) * kHeadDim : nullptr;
-        };
-      };
-      __syncthreads();
-      simt_load_rows(Qs, kBRows, (const T*)a.q, rows_of(a.q));
-      simt_load_rows(Os, kBRows, (const T*)a.dout, rows_of(a.dout));
-      if (threadIdx.x < kBRows) {
+      const int64_t at = (q0 + i0) * a.H + x.grp * t.hpg + c % t.hpg;
+      simt_load_rows(dst, kBRows, (const T*)base, [&](int r) -> const T* {
+        return r < nrows ? (const T*)base + (at + (int64_t)r * a.H) * kHeadDim : nullptr;
+      });
+      if (stats && threadIdx.x < kBRows) {
         const bool v = threadIdx.x < nrows;
-        st_lse[threadIdx.x] = v ? a.lse[q_at(threadIdx.x)] * 1.4426950408889634f : 0.f;
-        st_delta[threadIdx.x] = v ? a.delta[q_at(threadIdx.x)] : 0.f;
+        const int64_t row = at + (int64_t)threadIdx.x * a.H;
+        st_lse[threadIdx.x] = v ? a.lse[row] * 1.4426950408889634f : 0.f;
+        st_delta[threadIdx.x] = v ? a.delta[row] : 0.f;
       }
-      sm100::cp_async_wait_all();
+    };
+    load_chunk(Os, a.dout, p.c0, true);
+    sm100::cp_async_commit();
+    load_chunk(Qs, a.q, p.c0, false);
+    sm100::cp_async_commit();
+    const int tx = threadIdx.x & 15, ra = (threadIdx.x >> 4) * 4;
+    // dO of the next chunk loads under this one's dk, Q under the next one's dP
+    for (int c = p.c0; c < p.c1; ++c) {
+      const int32_t i0 = j0 + c / t.hpg * kBRows;
+      const int nrows = min(kBRows, n - i0);
+      float sc[4][2], dp[4][2];
+      sm100::cp_async_wait<1>();
       __syncthreads();
-      simt_p_ds(Qs, Os, Ks, Vs, Ps, Ds, st_lse, st_delta, i0, nrows, 1, j0, n, s2);
+      simt_dots<4, 2>(Os, Vs, ra, tx, dp);
+      sm100::cp_async_wait<0>();
       __syncthreads();
-      // a row before a key does not touch it
+      simt_dots<4, 2>(Qs, Ks, ra, tx, sc);
+      simt_p_ds(sc, dp, Ps, Ds, st_lse, st_delta, i0, nrows, 1, j0, n, s2);
+      __syncthreads();
+      // sums over the chunk's rows of w[row][key] times the row, for this thread's
+      // keys; a row before a key does not touch it
       const bool limited = j0 + kBKeys - 1 > i0;
-      for (int r = 0; r < nrows; ++r) {
-        const float4 pr = *reinterpret_cast<const float4*>(Ps + r * kBLd + kq);
-        const float4 sr = *reinterpret_cast<const float4*>(Ds + r * kBLd + kq);
-        const float pp[4] = {pr.x, pr.y, pr.z, pr.w}, ss[4] = {sr.x, sr.y, sr.z, sr.w};
-        float4 xq[2], xo[2];
+      auto add_rows = [&](const float* w, const float* rows, float (&g)[4][8]) {
+#pragma unroll 2
+        for (int r = 0; r < nrows; ++r) {
+          const float4 wr = *reinterpret_cast<const float4*>(w + r * kBLd + kq);
+          const float ww[4] = {wr.x, wr.y, wr.z, wr.w};
+          const float4 x0 = *reinterpret_cast<const float4*>(rows + r * kLd + dl);
+          const float4 x1 = *reinterpret_cast<const float4*>(rows + r * kLd + dl + 128);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          xq[h] = *reinterpret_cast<const float4*>(Qs + r * kLd + dl + 128 * h);
-          xo[h] = *reinterpret_cast<const float4*>(Os + r * kLd + dl + 128 * h);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (limited && j0 + kq + i > i0 + r) continue;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            dk[i][4 * h] = fmaf(ss[i], xq[h].x, dk[i][4 * h]);
-            dk[i][4 * h + 1] = fmaf(ss[i], xq[h].y, dk[i][4 * h + 1]);
-            dk[i][4 * h + 2] = fmaf(ss[i], xq[h].z, dk[i][4 * h + 2]);
-            dk[i][4 * h + 3] = fmaf(ss[i], xq[h].w, dk[i][4 * h + 3]);
-            dv[i][4 * h] = fmaf(pp[i], xo[h].x, dv[i][4 * h]);
-            dv[i][4 * h + 1] = fmaf(pp[i], xo[h].y, dv[i][4 * h + 1]);
-            dv[i][4 * h + 2] = fmaf(pp[i], xo[h].z, dv[i][4 * h + 2]);
-            dv[i][4 * h + 3] = fmaf(pp[i], xo[h].w, dv[i][4 * h + 3]);
+          for (int i = 0; i < 4; ++i) {
+            if (limited && j0 + kq + i > i0 + r) continue;
+            float2* d = reinterpret_cast<float2*>(g[i]);
+            const float2 f = make_float2(ww[i], ww[i]);
+            d[0] = fma2(f, lo2(x0), d[0]);
+            d[1] = fma2(f, hi2(x0), d[1]);
+            d[2] = fma2(f, lo2(x1), d[2]);
+            d[3] = fma2(f, hi2(x1), d[3]);
           }
         }
-      }
+      };
+      add_rows(Ps, Os, dv);
+      __syncthreads();
+      if (c + 1 < p.c1) load_chunk(Os, a.dout, c + 1, true);
+      sm100::cp_async_commit();
+      add_rows(Ds, Qs, dk);
+      __syncthreads();
+      if (c + 1 < p.c1) load_chunk(Qs, a.q, c + 1, false);
+      sm100::cp_async_commit();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
