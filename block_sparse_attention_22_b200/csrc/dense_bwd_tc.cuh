@@ -44,6 +44,8 @@
 // anything: their scores are replaced and their operand rows zeroed in shared
 // memory.  Every mbarrier wait is bounded.
 #pragma once
+#include <type_traits>
+
 #include "dense_tc.cuh"
 
 namespace qsa {
@@ -111,19 +113,6 @@ struct DenseBwdTcCtl {
 constexpr int kBwdStatOff = 1024;                     // of the control block: lse2[128] by buffer, then delta[128] (dK)
 static_assert(sizeof(DenseBwdTcCtl) <= kBwdStatOff, "control block");
 static_assert(kBwdStatOff + 2 * 1024 <= dense_bwd::kCtlBytes, "control block");
-
-// Ring position j of a piece of n chunks: which operand (0: S, 1: dP, 2: the
-// gradient's product) of which chunk.
-template <dense_bwd::Grad M>
-__device__ __forceinline__ void bwd_item(int j, int n, int& kind, int& c) {
-  if constexpr (M == dense_bwd::kDv) {
-    kind = (j == 0) ? 0 : (j == 2 * n - 1) ? 2 : (j & 1) ? 0 : 2;
-    c = (j == 0) ? 0 : (j == 2 * n - 1) ? n - 1 : (j & 1) ? (j + 1) / 2 : j / 2 - 1;
-  } else {
-    kind = (j == 0) ? 0 : (j == 3 * n - 1) ? 2 : (j % 3 == 1) ? 1 : (j % 3 == 2) ? 0 : 2;
-    c = (j == 0) ? 0 : (j == 3 * n - 1) ? n - 1 : (j % 3 == 1) ? j / 3 : (j % 3 == 2) ? (j + 1) / 3 : j / 3 - 1;
-  }
-}
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -208,54 +197,86 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     // ============================================================ TMA producer
     // A slot is four boxes of 64 lines x 64 dims, one per lane: rows of this
     // CTA's half x 256 dims (S, dP), or 128 rows x this CTA's half of the dims.
-    int64_t gc = 0;                                  // chunks of the pieces before
+    const int off_s = (lane & 3) * 8192, x_s = (lane & 3) * 64, y_s = (int)rank * 64;
+    const int off_d = (lane & 1) * 16384 + ((lane >> 1) & 1) * 8192;
+    const int x_d = (lane & 1) * 64 + (int)rank * 128, y_d = ((lane >> 1) & 1) * 64;
+    uint32_t slot[3] = {0, 0, 0}, phase[3] = {0, 0, 0}, st_buf = 0, st_phase = 0;
     bool ok = true;
+    // a chunk's first row of the segment and its head (dQ: KV group)
+    struct Chunk {
+      int32_t r0, head, left;                        // left: heads until the next rows
+    };
+    auto advance = [&](Chunk& c) {
+      if (!kByKeys) {
+        c.r0 += kKeys;
+      } else if (--c.left > 0) {
+        ++c.head;
+      } else {
+        c.r0 += kKeys;
+        c.head -= t.hpg - 1;
+        c.left = t.hpg;
+      }
+    };
+    auto put = [&](auto kind_c, const Chunk& c) -> bool {
+      constexpr int kind = decltype(kind_c)::value;
+      constexpr uint32_t kN = R::slots(kind);
+      const uint32_t b = slot[kind], ph = phase[kind];
+      slot[kind] = b + 1 == kN ? 0 : b + 1;
+      if (b + 1 == kN) phase[kind] ^= 1;
+      unsigned char* to = smem + R::offset(kind) + b * kSlotBytes;
+      const int32_t cx = c.head * kHeadDim, cy = t.q_offset[x.si] + c.r0;
+      uint64_t* const free_bar = kind == 0 ? &ctl.s_done[b] : kind == 1 ? &ctl.dp_done : &ctl.d_done[b];
+      if (!warp_wait_fast(free_bar, ph ^ 1, abort_flag)) return false;
+      if constexpr (kind == 2) {
+        if (lane == 0) mbar_expect_tx(&ctl.d_full[b], kSlotBytes);
+        __syncwarp();
+        if (lane < 4) tma_load_2d(to + off_d, &tm.d, cx + x_d, cy + y_d, &ctl.d_full[b]);
+      } else {
+        if (lane == 0) mbar_expect_tx_leader<2>(&ctl.full[kind][b], kSlotBytes);
+        __syncwarp();
+        if (lane < 4)
+          tma_load_2d_leader<2>(to + off_s, kind == 0 ? &tm.s : &tm.p, cx + x_s, cy + y_s, &ctl.full[kind][b]);
+      }
+      // The chunk's row statistics, behind a load whose slot was freed after
+      // the softmax that held the buffer: this wait does not hold up the ring.
+      if constexpr (kByKeys && kind == kProducts - 2) {
+        if (!warp_wait_fast(&ctl.st_free[st_buf], st_phase ^ 1, abort_flag)) return false;
+        if (lane == 0) {
+          const int64_t at = (int64_t)c.head * a.stat_rows + t.slot[x.si] * kStatTile + c.r0;
+          mbar_expect_tx(&ctl.st_full[st_buf], M == kDv ? 512 : 1024);
+          bulk_load(stats + st_buf * 128, a.lse2 + at, 512, &ctl.st_full[st_buf]);
+          if (M != kDv) bulk_load(stats + (R::kStats + st_buf) * 128, a.delta + at, 512, &ctl.st_full[st_buf]);
+        }
+        __syncwarp();
+        st_buf = st_buf + 1 == R::kStats ? 0 : st_buf + 1;
+        if (st_buf == 0) st_phase ^= 1;
+      }
+      return true;
+    };
+    using std::integral_constant;
+    constexpr integral_constant<int, 0> kPutS{};
+    constexpr integral_constant<int, kProducts == 3 ? 1 : 0> kPutP{};
+    constexpr integral_constant<int, 2> kPutD{};
     while (ok && next()) {
-      if (warp_aborted(abort_flag)) {
-        ok = false;
-        break;
-      }
       const int n = p.c1 - p.c0;
-      for (int j = 0; j < kProducts * n && ok; ++j) {
-        int kind, c;
-        bwd_item<M>(j, n, kind, c);
-        const int64_t xg = gc + c;
-        c += p.c0;
-        const int slot = (int)(xg % R::slots(kind));
-        const uint32_t phase = (uint32_t)((xg / R::slots(kind)) & 1);
-        unsigned char* to = smem + R::offset(kind) + slot * kSlotBytes;
-        const int slab = kind == 2 ? lane & 1 : lane & 3, run = kind == 2 ? (lane >> 1) & 1 : 0;
-        const int off = kind == 2 ? slab * 16384 + run * 8192 : slab * 8192;
-        const int head = kByKeys ? x.grp * t.hpg + c % t.hpg : x.grp;
-        const int32_t r0 = kByKeys ? x.row0 + c / t.hpg * kKeys : c * kKeys;   // of the segment
-        const int32_t cx = head * kHeadDim + slab * 64 + (kind == 2 ? (int)rank * 128 : 0);
-        const int32_t cy = t.q_offset[x.si] + r0 + (kind == 2 ? run * 64 : (int)rank * 64);
-        uint64_t* const free_bar = kind == 0 ? &ctl.s_done[slot] : kind == 1 ? &ctl.dp_done : &ctl.d_done[slot];
-        if (!(ok = warp_wait_sleep(free_bar, phase ^ 1, abort_flag))) break;
-        if (kind == 2) {
-          if (lane == 0) mbar_expect_tx(&ctl.d_full[slot], kSlotBytes);
-          __syncwarp();
-          if (lane < 4) tma_load_2d(to + off, &tm.d, cx, cy, &ctl.d_full[slot]);
-        } else {
-          if (lane == 0) mbar_expect_tx_leader<2>(&ctl.full[kind][slot], kSlotBytes);
-          __syncwarp();
-          if (lane < 4) tma_load_2d_leader<2>(to + off, kind == 0 ? &tm.s : &tm.p, cx, cy, &ctl.full[kind][slot]);
-        }
-        // The chunk's row statistics, behind a load whose slot was freed after
-        // the softmax that held the buffer: this wait does not hold up the ring.
-        if (kByKeys && kind == kProducts - 2) {
-          const int b = (int)(xg % R::kStats);
-          if (!(ok = warp_wait_sleep(&ctl.st_free[b], (uint32_t)(((xg / R::kStats) & 1) ^ 1), abort_flag))) break;
-          if (lane == 0) {
-            const int64_t at = (int64_t)head * a.stat_rows + (int64_t)t.slot[x.si] * kStatTile + r0;
-            mbar_expect_tx(&ctl.st_full[b], M == kDv ? 512 : 1024);
-            bulk_load(stats + b * 128, a.lse2 + at, 512, &ctl.st_full[b]);
-            if (M != kDv) bulk_load(stats + (R::kStats + b) * 128, a.delta + at, 512, &ctl.st_full[b]);
-          }
-          __syncwarp();
-        }
+      Chunk cur;
+      if (kByKeys) {
+        const int tile = p.c0 / t.hpg, hl = p.c0 - tile * t.hpg;
+        cur = {x.row0 + tile * kKeys, x.grp * t.hpg + hl, t.hpg - hl};
+      } else {
+        cur = {p.c0 * kKeys, x.grp, 0};
       }
-      gc += n;
+      Chunk nxt = cur;
+      advance(nxt);
+      ok = put(kPutS, cur);
+      if (kProducts == 3) ok = ok && put(kPutP, cur);
+      for (int c = 0; c < n && ok; ++c) {
+        if (c + 1 < n) ok = put(kPutS, nxt);
+        ok = ok && put(kPutD, cur);
+        if (kProducts == 3 && c + 1 < n) ok = ok && put(kPutP, nxt);
+        cur = nxt;
+        advance(nxt);
+      }
     }
     if (!ok) drain_copies();                         // no copy outlives the CTA
   } else if (warp == kMmaWarp && rank == 0) {

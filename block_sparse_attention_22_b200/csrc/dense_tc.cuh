@@ -55,7 +55,7 @@ constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kNfWarp = 11;
-constexpr int kSlots = 4, kKSlots = 2, kVSlots = 2;        // K's as many as S buffers: they share barriers
+constexpr int kSlots = 4, kKSlots = 2, kVSlots = 2;   // K's as many as S buffers, V's as P: they share barriers
 constexpr int kSlotBytes = 32768;
 constexpr int kQBytes = 65536;                        // 128 rows x 256 dims, 4 slabs of 16 KiB
 constexpr int kOffV = kKSlots * kSlotBytes;
@@ -197,6 +197,11 @@ __device__ __forceinline__ void store_cols32(const float (&o)[32], float f, __nv
   }
 }
 
+// mbar_wait_fast by a whole warp, with one answer.
+__device__ __forceinline__ bool warp_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, sm100::mbar_wait_fast(bar, parity, abort_flag));
+}
+
 // After an abort: copies in flight land within microseconds; the CTA stays for
 // about a millisecond.
 __device__ __forceinline__ void drain_copies() {
@@ -256,68 +261,66 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
   DenseUnit x;
   if (warp == kProducerWarp) {
     // ============================================================ TMA producer
-    // Lane b < 256 / box issues box b of a slot: `box` keys x 64 dims.
-    const int nbox = 256 / a.box;
-    int64_t gc = 0;                                          // chunks of the pieces before
+    // A slot is 256 / box boxes of `box` keys x 64 dims, one per lane.  A chunk's
+    // cache rows are formed once, a run of `box` keys per lane, a chunk ahead of
+    // their use: a product's time is 500 of this warp's instructions.
+    constexpr int kSlabsV = CG == 2 ? 2 : 4;
+    const int nbox = 256 / a.box, runs = KC / a.box;
+    // this lane's box: K keys run_k.. of this CTA's 64, V all keys x this CTA's dims
+    const int slab_k = lane & 3, run_k = (lane >> 2) + (CG == 2 ? (int)rank * 64 / a.box : 0);
+    const int slab_v = lane % kSlabsV, run_v = lane / kSlabsV;
+    const int off_k = slab_k * 8192 + (lane >> 2) * a.box * 128;
+    const int off_v = slab_v * (256 / kSlabsV) * 128 + run_v * a.box * 128;
+    const int x_v = slab_v * 64 + (CG == 2 ? (int)rank * 128 : 0);
+    const bool has_box = lane < nbox;
+    uint32_t gk = 0, gv = 0;                                 // chunks of K and V so far
     bool ok = true;
+    // cache row of run `lane` of chunk c (of the piece); < 0: not loaded
+    auto rows_of = [&](int c) -> int32_t {
+      const int32_t key = (p.c0 + c) * KC + lane * a.box;
+      if (lane >= runs || c >= p.c1 - p.c0 || key >= x.kv_len) return -1;
+      if (!PAGED) return t.q_offset[x.si] + key;
+      const int32_t pi = key / a.kv.page_tokens;
+      const int32_t page = a.kv.table[(int64_t)t.slot[x.si] * a.kv.max_pages + pi];
+      if (page < 0 || page >= a.kv.n_pages) {
+        report_error(kErrBadIndex);
+        return -1;
+      }
+      return (page * t.G + x.grp) * a.kv.page_tokens + (key - pi * a.kv.page_tokens);
+    };
+    auto put = [&](bool is_v, int32_t rows, int32_t x0) -> bool {
+      uint32_t& g = is_v ? gv : gk;
+      const uint32_t slot = g & 1, phase = (g >> 1) & 1;
+      ++g;
+      const int32_t y = __shfl_sync(0xffffffffu, rows, is_v ? run_v : run_k);
+      const uint32_t live = __ballot_sync(0xffffffffu, has_box && y >= 0);
+      const uint32_t bytes = (uint32_t)__popc(live) * (uint32_t)(a.box * 128);
+      if (!warp_wait_fast(is_v ? &ctl.pv_done[slot] : &ctl.s_done[slot], phase ^ 1, abort_flag)) return false;
+      if (is_v) {
+        if (lane == 0) mbar_expect_tx(&ctl.v_full[slot], bytes);
+        __syncwarp();
+        if (has_box && y >= 0)
+          tma_load_2d(smem + kOffV + slot * kSlotBytes + off_v, &tm_v, x0 + x_v, y, &ctl.v_full[slot]);
+      } else {
+        if (lane == 0) mbar_expect_tx_leader<CG>(&ctl.k_full[slot], bytes);
+        __syncwarp();
+        if (has_box && y >= 0)
+          tma_load_2d_leader<CG>(smem + slot * kSlotBytes + off_k, &tm_k, x0 + slab_k * 64, y, &ctl.k_full[slot]);
+      }
+      return true;
+    };
     while (ok && walk.next(t, p, x)) {
-      if (warp_aborted(abort_flag)) {
-        ok = false;
-        break;
-      }
       const int n = p.c1 - p.c0;
-      // box `lane` of ring position j: its coordinates; y < 0: not loaded
-      auto place = [&](int j, int& kind, int& c, int& off, int& cx, int& key) {
-        kind = (j == 0) ? 0 : (j == 2 * n - 1) ? 1 : (j & 1) ? 0 : 1;
-        c = (j == 0) ? 0 : (j == 2 * n - 1) ? n - 1 : (j & 1) ? (j + 1) / 2 : j / 2 - 1;
-        const int slabs = (CG == 2 && kind == 1) ? 2 : 4;
-        const int slab = lane % slabs, run = lane / slabs;
-        const int lines = 256 / slabs;                       // lines of a slab: 64 or 128
-        off = slab * lines * 128 + run * a.box * 128;
-        cx = slab * 64 + ((CG == 2 && kind == 1) ? (int)rank * 128 : 0);
-        key = (p.c0 + c) * KC + run * a.box + ((CG == 2 && kind == 0) ? (int)rank * 64 : 0);
-      };
-      auto page_of = [&](int j) -> int32_t {                 // page of this lane's box (paged only)
-        int kind, c, off, cx, key;
-        place(j, kind, c, off, cx, key);
-        if (lane >= nbox || key >= x.kv_len) return -1;
-        return a.kv.table[(int64_t)t.slot[x.si] * a.kv.max_pages + key / a.kv.page_tokens];
-      };
-      int32_t page = PAGED ? page_of(0) : 0;
-      for (int j = 0; j < 2 * n; ++j) {
-        int kind, c, off, cx, key;
-        place(j, kind, c, off, cx, key);
-        int32_t y = -1;
-        if (lane < nbox && key < x.kv_len) {
-          if (PAGED) {
-            if (page >= 0 && page < a.kv.n_pages)
-              y = (page * t.G + x.grp) * a.kv.page_tokens + key % a.kv.page_tokens;
-            else
-              report_error(kErrBadIndex);
-          } else {
-            y = t.q_offset[x.si] + key;
-            cx += x.grp * kHeadDim;
-          }
-        }
-        if (PAGED && j + 1 < 2 * n) page = page_of(j + 1);
-        const int64_t xg = gc + c;
-        const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
-        const uint32_t bytes = (uint32_t)__popc(live) * (uint32_t)(a.box * 128);
-        if (kind == 0) {
-          const int slot = (int)(xg % kKSlots);
-          if (!(ok = warp_wait_sleep(&ctl.s_done[slot], (uint32_t)(((xg / kKSlots) & 1) ^ 1), abort_flag))) break;
-          if (lane == 0) mbar_expect_tx_leader<CG>(&ctl.k_full[slot], bytes);
-          __syncwarp();
-          if (y >= 0) tma_load_2d_leader<CG>(smem + slot * kSlotBytes + off, &tm_k, cx, y, &ctl.k_full[slot]);
-        } else {
-          const int slot = (int)(xg % kVSlots);
-          if (!(ok = warp_wait_sleep(&ctl.pv_done[slot], (uint32_t)(((xg / kVSlots) & 1) ^ 1), abort_flag))) break;
-          if (lane == 0) mbar_expect_tx(&ctl.v_full[slot], bytes);
-          __syncwarp();
-          if (y >= 0) tma_load_2d(smem + kOffV + slot * kSlotBytes + off, &tm_v, cx, y, &ctl.v_full[slot]);
-        }
+      const int32_t x0 = PAGED ? 0 : x.grp * kHeadDim;
+      int32_t cur = rows_of(0), next = rows_of(1);
+      ok = put(false, cur, x0);
+      for (int c = 0; c < n && ok; ++c) {
+        const int32_t after = rows_of(c + 2);
+        if (c + 1 < n) ok = put(false, next, x0);
+        ok = ok && put(true, cur, x0);
+        cur = next;
+        next = after;
       }
-      gc += n;
     }
     if (!ok) drain_copies();                                 // no copy outlives the CTA
   } else if (warp == kMmaWarp && rank == 0) {
