@@ -409,10 +409,12 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
               make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
       };
+      // first position of a chunk's columns; by keys, `left` heads until the next tokens
+      const int tile0 = kByKeys ? p.c0 / t.hpg : 0;
+      int left = kByKeys ? t.hpg - (p.c0 - tile0 * t.hpg) : 0;
+      int32_t j0 = kByKeys ? x.row0 + tile0 * kKeys : p.c0 * kKeys;
       for (int c = 0; c < n; ++c, ++gc) {
-        const int cc = p.c0 + c;
         const int b = (int)(gc % kBufs);
-        const int32_t j0 = kByKeys ? x.row0 + (cc / t.hpg) * kKeys : cc * kKeys;   // first position of the columns
         const int sbuf = (int)(gc % R::kStats);
         const float* st_l = stats + sbuf * 128 + half * 64;
         const float* st_d = st_l + R::kStats * 128;
@@ -479,21 +481,18 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
             if (active && half == 0) a.delta[sat] = delta;
             named_bar_sync(1 + quad, 64);            // read before the next unit's sums
           }
+          float v[4][16];                            // one wait for all: dS is what the next products wait for
 #pragma unroll
-          for (int k = 0; k < 64; k += 32) {
-            float v[2][16];
-            tmem_ld16(dst + k, v[0]);
-            tmem_ld16(dst + k + 16, v[1]);
-            tmem_wait_ld();
+          for (int k = 0; k < 4; ++k) tmem_ld16(dst + 16 * k, v[k]);
+          tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              float4 d = make_float4(delta, delta, delta, delta);
-              if (kByKeys) d = *reinterpret_cast<const float4*>(st_d + k + i);
-              w[k + i] *= v[i >> 4][i & 15] - d.x;
-              w[k + i + 1] *= v[i >> 4][(i & 15) + 1] - d.y;
-              w[k + i + 2] *= v[i >> 4][(i & 15) + 2] - d.z;
-              w[k + i + 3] *= v[i >> 4][(i & 15) + 3] - d.w;
-            }
+          for (int i = 0; i < 64; i += 4) {
+            float4 d = make_float4(delta, delta, delta, delta);
+            if (kByKeys) d = *reinterpret_cast<const float4*>(st_d + i);
+            w[i] *= v[i >> 4][i & 15] - d.x;
+            w[i + 1] *= v[i >> 4][(i & 15) + 1] - d.y;
+            w[i + 2] *= v[i >> 4][(i & 15) + 2] - d.z;
+            w[i + 3] *= v[i >> 4][(i & 15) + 3] - d.w;
           }
           if (cut) {
 #pragma unroll
@@ -523,6 +522,10 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         if (lane == 0) {
           if (clear) mbar_arrive_cluster(&ctl.w_full[b], 0); else mbar_arrive_leader<2>(&ctl.w_full[b]);
           if (kByKeys) mbar_arrive(&ctl.st_free[sbuf]);
+        }
+        if (!kByKeys || --left == 0) {
+          j0 += kKeys;
+          left = t.hpg;
         }
       }
       more = next_of(p_next, x_next);
