@@ -408,7 +408,7 @@ struct DenseBwdPlan {
   std::vector<qsa_segment_t> segs;       // non-empty; slot: the segment's first statistics tile
   std::vector<DenseLaunch> rows, keys;   // launches by rows (dq) and by keys (dk, dv)
   int64_t stat_rows = 0;
-  size_t off_lse2 = 0, off_delta_h = 0, off_flags = 0, flag_bytes = 0, off_part = 0, off_part2 = 0, bytes = 0;
+  size_t off_lse2 = 0, off_delta_h = 0, off_flags = 0, off_part = 0, off_part2 = 0, bytes = 0;
 };
 
 DenseKind dense_bwd_kind(bool tc, bool by_keys) {
@@ -434,8 +434,7 @@ qsa_status_t plan_dense_bwd(const Geo& g, bool tc, const qsa_segment_t* segs, in
     p.off_lse2 = at;
     p.off_delta_h = at + stats;
     p.off_flags = at + 2 * stats;
-    p.flag_bytes = (size_t)tiles * 4;
-    at = p.off_flags + align_up(p.flag_bytes, 256);
+    at = p.off_flags + align_up((size_t)tiles * (dense_bwd::kStatTile / 4), 256);
   }
   p.off_part = at;
   size_t part = 0;
@@ -452,43 +451,31 @@ size_t dense_bwd_ws(const Geo& g, bool tc, const qsa_segment_t* segs, int n, int
   return plan_dense_bwd(g, tc, segs, n, n_tokens, p) == QSA_OK ? p.bytes : SIZE_MAX;
 }
 
-// Joins the cut units of a gradient launch.
+// Joins the cut units of every launch's gradients: dq's from `parts`, dk's and
+// dv's from `dk_parts` and `dv_parts`, dv's partial rows `dv_row` behind dk's.
 template <typename T>
-cudaError_t launch_bwd_combine(const Geo& g, const DenseLaunch& x, const char* parts, const int32_t* flags, void* out,
-                               float factor, void* out2, cudaStream_t st) {
-  if (x.sp.n == 0) return cudaSuccess;
-  count_launch();
-  return launch_chained(dense_bwd_combine_kernel<T>,
-                        dim3(x.sp.n, (unsigned)cdiv(std::min(x.t.prows, x.t.rows), 4)), dim3(128), 0, st, x.t, x.sp,
-                        (const float*)(parts + x.part), flags, (T*)out, factor, (T*)out2, dense_simt::kBKeys, g.H);
-}
-
-// The CUDA-core gradient over the given launches.
-template <typename T>
-qsa_status_t run_dense_bwd_simt(const Geo& g, const std::vector<DenseLaunch>& rows,
-                                const std::vector<DenseLaunch>& keys, const DenseBwdArgs& a, char* parts,
-                                cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(dense_dq_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       dense_simt::kBwdSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(dense_dkv_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             dense_simt::kBwdSmem);
-  const dim3 block(dense_simt::kThreads);
-  for (const DenseLaunch& x : rows) {
-    if (e != cudaSuccess) break;
+cudaError_t launch_bwd_joins(const Geo& g, const DenseBwdPlan& p, const DenseBwdArgs& a, const char* parts,
+                             const char* dk_parts, const char* dv_parts, int dv_row, const uint8_t* flags,
+                             cudaStream_t st) {
+  for (size_t i = 0; i < std::max(p.rows.size(), p.keys.size()); ++i) {
+    static const DenseLaunch kNone{};
+    const DenseLaunch& r = i < p.rows.size() ? p.rows[i] : kNone;
+    const DenseLaunch& k = i < p.keys.size() ? p.keys[i] : kNone;
+    if (r.sp.n == 0 && k.sp.n == 0) continue;
+    auto rows_of = [](const DenseLaunch& x) { return x.sp.n ? std::min(x.t.prows, x.t.rows) : 0; };
+    const DenseBwdJoins<T> joins{{{(const float*)(parts + r.part), (T*)a.dq, g.scale, 0, 0},
+                                  {(const float*)(dk_parts + k.part), (T*)a.dk, g.scale, 0, 1},
+                                  {(const float*)(dv_parts + k.part), (T*)a.dv, 1.f, dv_row, 1}},
+                                 flags,
+                                 g.H};
     count_launch();
-    e = launch_chained(dense_dq_simt_kernel<T>, dim3(x.t.grid), block, dense_simt::kBwdSmem, st, x.t, a,
-                       (float*)(parts + x.part));
-    if (e == cudaSuccess) e = launch_bwd_combine<T>(g, x, parts, nullptr, a.dq, g.scale, nullptr, st);
+    const cudaError_t e = launch_chained(
+        dense_bwd_combine_kernel<T>,
+        dim3(std::max(r.sp.n, k.sp.n), (unsigned)cdiv(std::max(rows_of(r), rows_of(k)), 4), 3), dim3(128), 0, st, r.t,
+        r.sp, k.t, k.sp, joins);
+    if (e != cudaSuccess) return e;
   }
-  for (const DenseLaunch& x : keys) {
-    if (e != cudaSuccess) break;
-    count_launch();
-    e = launch_chained(dense_dkv_simt_kernel<T>, dim3(x.t.grid), block, dense_simt::kBwdSmem, st, x.t, a,
-                       (float*)(parts + x.part));
-    if (e == cudaSuccess) e = launch_bwd_combine<T>(g, x, parts, nullptr, a.dk, g.scale, a.dv, st);
-  }
-  return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
+  return cudaSuccess;
 }
 
 qsa_status_t run_dense_bwd_f32(const Geo& g, const DenseBwdPlan& p, const DenseBwdArgs& a, const void* o, char* ws,
@@ -500,7 +487,21 @@ qsa_status_t run_dense_bwd_f32(const Geo& g, const DenseBwdPlan& p, const DenseB
         return launch_chained(dense_delta_kernel<float>, dim3((unsigned)cdiv((int64_t)t.item0[t.n] * g.H, 8)),
                               dim3(256), 0, st, t, (const float*)o, (const float*)a.dout, (float*)ws, g.H);
       });
-  return r != QSA_OK ? r : run_dense_bwd_simt<float>(g, p.rows, p.keys, a, ws + p.off_part, st);
+  if (r != QSA_OK) return r;
+  cudaError_t e = cudaFuncSetAttribute(dense_dq_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       dense_simt::kBwdSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(dense_dkv_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense_simt::kBwdSmem);
+  char* const parts = ws + p.off_part;
+  for (const bool keys : {false, true})
+    for (const DenseLaunch& x : keys ? p.keys : p.rows) {
+      if (e != cudaSuccess) break;
+      count_launch();
+      e = launch_chained(keys ? dense_dkv_simt_kernel : dense_dq_simt_kernel, dim3(x.t.grid),
+                         dim3(dense_simt::kThreads), dense_simt::kBwdSmem, st, x.t, a, (float*)(parts + x.part));
+    }
+  if (e == cudaSuccess) e = launch_bwd_joins<float>(g, p, a, parts, parts, parts, dense_simt::kBKeys, nullptr, st);
+  return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 
 // One gradient on the tensor cores; partial results from `parts` on.
@@ -538,7 +539,7 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
   float* delta = (float*)ws;
   float* lse2_h = (float*)(ws + p.off_lse2);
   float* delta_h = (float*)(ws + p.off_delta_h);
-  int32_t* flags = (int32_t*)(ws + p.off_flags);
+  uint8_t* flags = (uint8_t*)(ws + p.off_flags);
   CUtensorMap mq, mo, mk, mv, tq, to, rq, ro;      // boxes of 64 rows; Q and dO by whole tokens and parts of one
   const int64_t rows = (int64_t)n_tokens * g.H;
   if (rows > INT32_MAX - 512) return QSA_ERR_UNSUPPORTED;
@@ -547,13 +548,12 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
       !make_dense_map(&tq, a.q, rows, 1, g.hpg) || !make_dense_map(&to, a.dout, rows, 1, g.hpg) ||
       !make_dense_map(&rq, a.q, rows, 1, g.hpg & -g.hpg) || !make_dense_map(&ro, a.dout, rows, 1, g.hpg & -g.hpg))
     return QSA_ERR_CUDA;
-  if (cudaMemsetAsync(flags, 0, p.flag_bytes, st) != cudaSuccess) return QSA_ERR_CUDA;
   qsa_status_t r = for_each_table(
       p.segs.data(), (int)p.segs.size(),
       [&](const qsa_segment_t& s) { return cdiv(s.q_len, dense_bwd::kStatTile) * dense_bwd::kStatTile; },
       [&](const SegTable& t) -> cudaError_t {
         count_launch();
-        return launch_chained(dense_stats_kernel, dim3((unsigned)cdiv((int64_t)t.item0[t.n] * g.H, 8)), dim3(256), 0,
+        return launch_chained(dense_stats_kernel, dim3((unsigned)(t.item0[t.n] / 4)), dim3(256), 0,
                               st, t, (const B*)o, (const B*)a.dout, a.lse, (const B*)a.k, (const B*)a.v, delta, lse2_h,
                               delta_h, flags, p.stat_rows, g.H, g.G);
       });
@@ -570,23 +570,25 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
   b.late = false;
   b.out = (B*)a.dk;
   if ((r = run_dense_grad_tc<dense_bwd::kDk>(p, {mq, mo, mq, mk, mv, mk, mv}, b, parts2, st)) != QSA_OK) return r;
-  cudaError_t e = cudaSuccess;
-  for (const DenseLaunch& x : p.keys) {
-    if (e == cudaSuccess) e = launch_bwd_combine<B>(g, x, parts, flags, a.dv, 1.f, nullptr, st);
-    if (e == cudaSuccess) e = launch_bwd_combine<B>(g, x, parts2, flags, a.dk, g.scale, nullptr, st);
-  }
-  for (const DenseLaunch& x : p.rows)
-    if (e == cudaSuccess) e = launch_bwd_combine<B>(g, x, parts, flags, a.dq, g.scale, nullptr, st);
-  if (e != cudaSuccess) return QSA_ERR_CUDA;
-  // the flagged segments; their launches are not levelled (there are hardly ever any)
+  cudaError_t e = launch_bwd_joins<B>(g, p, a, parts, parts2, parts, 0, flags, st);
+  // the flagged segments; their launches are not levelled
   a.flags = flags;
-  std::vector<DenseLaunch> by_rows, by_keys;
+  std::vector<DenseLaunch> rows_l, keys_l;
   size_t part = 0;
   DenseKind kr = dense_bwd_kind(false, false), kk = dense_bwd_kind(false, true);
   kr.level = kk.level = false;
-  if ((r = plan_launches(g, p.segs, kr, by_rows, part)) != QSA_OK) return r;
-  if ((r = plan_launches(g, p.segs, kk, by_keys, part)) != QSA_OK) return r;
-  return run_dense_bwd_simt<B>(g, by_rows, by_keys, a, ws, st);      // no unit is cut
+  if ((r = plan_launches(g, p.segs, kr, rows_l, part)) != QSA_OK) return r;
+  if ((r = plan_launches(g, p.segs, kk, keys_l, part)) != QSA_OK) return r;
+  if (rows_l.size() != keys_l.size()) return QSA_ERR_UNSUPPORTED;
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(dense_bwd_flagged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             dense_simt::kBwdSmem);
+  for (size_t i = 0; i < rows_l.size() && e == cudaSuccess; ++i) {
+    count_launch();
+    e = launch_chained(dense_bwd_flagged_kernel, dim3(rows_l[i].t.grid), dim3(dense_simt::kThreads),
+                       dense_simt::kBwdSmem, st, rows_l[i].t, keys_l[i].t, a);
+  }
+  return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 
 // Runs an entry point's body; host memory that runs out is an error code, not

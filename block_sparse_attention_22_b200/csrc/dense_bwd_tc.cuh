@@ -89,7 +89,7 @@ struct DenseBwdMaps {
 struct DenseBwdTcArgs {
   const float* lse2;          // [H][stat rows] lse * log2 e, +inf behind a segment's end
   float* delta;               // [H][stat rows]; rows of units of one chunk are rewritten by dQ
-  const int32_t* flags;       // by first statistics tile of a segment: not for these kernels
+  const uint8_t* flags;       // segment_flagged: not for these kernels
   __nv_bfloat16* out;
   float* part;
   int64_t stat_rows;
@@ -183,9 +183,16 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
   DensePiece p;
   DenseUnit x;
   // the next piece of a segment that is not flagged (the same in every role and CTA)
+  int seen = -1;                                     // the segment looked up last
+  bool flagged = false;
   auto next_of = [&](DensePiece& np, DenseUnit& nx) -> bool {
-    while (walk.next(t, np, nx))
-      if (!a.flags[t.slot[nx.si]]) return true;
+    while (walk.next(t, np, nx)) {
+      if (nx.si != seen) {
+        seen = nx.si;
+        flagged = segment_flagged(a.flags, t.slot[nx.si], t.q_len[nx.si]);
+      }
+      if (!flagged) return true;
+    }
     return false;
   };
   auto next = [&]() { return next_of(p, x); };
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     // ============================================================ MMA issuer
     int64_t gc = 0, uc = 0;                          // chunks and pieces so far
     const uint32_t sb = smem_u32(smem), leader = elect_one();
-    auto wait = [&](uint64_t* bar, int64_t phase) { return mbar_wait_fast(bar, (uint32_t)(phase & 1), abort_flag); };
+    auto wait = [&](uint64_t* bar, int64_t phase) { return warp_wait_fast(bar, (uint32_t)(phase & 1), abort_flag); };
     // S (kind 0) or dP (kind 1) of the piece's chunk c
     auto scores = [&](int kind, int c, int n) -> bool {
       const int64_t xg = gc + c;
@@ -566,58 +573,79 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
   dense_wait_last(a.late);
 }
 
-// Row statistics for the gradient kernels, one warp per (token, head): delta =
-// dout . o, by token for the CUDA-core kernels and, with lse in log2 units, by
-// head and statistics row for the tensor-core kernels; rows behind a segment's
-// end get lse +inf (P = 0).  A segment with an lse, delta, key or value that
-// is not finite is flagged.  Items: a segment's tokens rounded up to 128.
+// Row statistics for the gradient kernels, a block per 4 tokens (a segment's
+// tokens rounded up to 128): delta = dout . o, by token for the CUDA-core kernel
+// and, with lse in log2 units, by head and statistics row for the tensor-core
+// kernels; rows behind a segment's end get lse +inf (P = 0).  The block's flag: an
+// lse, delta, key or value of its tokens is not finite.  A warp takes a head's four
+// rows at once and reduces them together (6 exchanges instead of 20); bound by the
+// HBM read of o and dout.
 __global__ void __launch_bounds__(256)
     dense_stats_kernel(const __grid_constant__ SegTable st, const __nv_bfloat16* o, const __nv_bfloat16* dout,
                        const float* lse, const __nv_bfloat16* k, const __nv_bfloat16* v, float* delta, float* lse2_h,
-                       float* delta_h, int32_t* flags, int64_t stat_rows, int H, int G) {
+                       float* delta_h, uint8_t* flags, int64_t stat_rows, int H, int G) {
   pdl_wait();
   pdl_trigger();
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int item = (int)(w / H), h = (int)(w - (int64_t)item * H);
-  if (item >= st.item0[st.n]) return;
-  const int si = find_segment(st, item);
-  const int j = item - st.item0[si];
-  const int64_t sat = (int64_t)h * stat_rows + (int64_t)st.slot[si] * dense_bwd::kStatTile + j;
-  if (j >= st.q_len[si]) {
-    if (lane == 0) {
-      lse2_h[sat] = INFINITY;
-      delta_h[sat] = 0.f;
-    }
-    return;
-  }
-  const int64_t at = (int64_t)(st.q_offset[si] + j) * H + h;
-  Vec8<__nv_bfloat16> a, b;
-  a.load(o + at * kHeadDim + lane * 8);
-  b.load(dout + at * kHeadDim + lane * 8);
-  const float l = lse[at];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int item0 = (int)blockIdx.x * 4;
+  const int si = find_segment(st, item0);            // padded to 128: the four tokens are of one segment
+  const int j0 = item0 - st.item0[si], left = st.q_len[si] - j0;
+  const int64_t tok0 = (int64_t)st.q_offset[si] + j0;
+  const int64_t stat0 = (int64_t)st.slot[si] * dense_bwd::kStatTile + j0;
+  const int mine = ((lane >> 4) & 1) + ((lane >> 2) & 2);      // the token whose sum this lane's group of 8 ends with
   bool bad = false;
-  if (h < G) {
-    const int64_t kv = ((int64_t)(st.q_offset[si] + j) * G + h) * kHeadDim + lane * 8;
-    const uint4 x = *reinterpret_cast<const uint4*>(k + kv), y = *reinterpret_cast<const uint4*>(v + kv);
-    const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  for (int h = warp; h < H + G; h += 8) {
+    const bool is_kv = h >= H;
+    const int64_t ld = (int64_t)(is_kv ? G : H) * kHeadDim;
+    const int64_t at = tok0 * ld + (int64_t)(is_kv ? h - H : h) * kHeadDim + lane * 8;
+    const __nv_bfloat16* pa = (is_kv ? k : o) + at;
+    const __nv_bfloat16* pb = (is_kv ? v : dout) + at;
+    Vec8<__nv_bfloat16> a[4], b[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) bad |= (u[i] & 0x7f80u) == 0x7f80u || (u[i] & 0x7f800000u) == 0x7f800000u;
+    for (int q = 0; q < 4; ++q) {
+      a[q].x = b[q].x = make_uint4(0, 0, 0, 0);
+      if (q < left) {
+        a[q].load(pa + q * ld);
+        b[q].load(pb + q * ld);
+      }
+    }
+    if (is_kv) {                                     // an exponent of all ones carries into the sign bit
+      uint32_t c = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t u[8] = {a[q].x.x, a[q].x.y, a[q].x.z, a[q].x.w, b[q].x.x, b[q].x.y, b[q].x.z, b[q].x.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c |= (u[e] & 0x7f807f80u) + 0x00800080u;
+      }
+      bad |= (c & 0x80008000u) != 0;
+      continue;
+    }
+    const float l = mine < left ? lse[(tok0 + mine) * H + h] : 0.f;
+    float s[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float fa[8], fb[8];
+      a[q].get(fa);
+      b[q].get(fb);
+      s[q] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[q] = fmaf(fa[e], fb[e], s[q]);
+    }
+    const bool up = lane & 16, up8 = lane & 8;
+    const float s01 = (up ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, up ? s[0] : s[1], 16);
+    const float s23 = (up ? s[3] : s[2]) + __shfl_xor_sync(0xffffffffu, up ? s[2] : s[3], 16);
+    float d = (up8 ? s23 : s01) + __shfl_xor_sync(0xffffffffu, up8 ? s01 : s23, 8);
+#pragma unroll
+    for (int off = 4; off; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    bad |= !isfinite(d) || !isfinite(l);
+    if ((lane & 7) == 0) {
+      if (mine < left) delta[(tok0 + mine) * H + h] = d;
+      lse2_h[h * stat_rows + stat0 + mine] = mine < left ? l * 1.4426950408889634f : INFINITY;
+      delta_h[h * stat_rows + stat0 + mine] = d;
+    }
   }
-  float fa[8], fb[8], s = 0.f;
-  a.get(fa);
-  b.get(fb);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s = fmaf(fa[i], fb[i], s);
-#pragma unroll
-  for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  bad |= !isfinite(s) || !isfinite(l);
-  if (__any_sync(0xffffffffu, bad) && lane == 0) flags[st.slot[si]] = 1;
-  if (lane == 0) {
-    delta[at] = s;
-    lse2_h[sat] = l * 1.4426950408889634f;
-    delta_h[sat] = s;
-  }
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) flags[stat0 / 4] = any != 0;
 }
 
 }  // namespace qsa

@@ -289,7 +289,7 @@ struct DenseBwdArgs {
   void* dv;
   int H;
   float scale;
-  const int32_t* flags;    // null: every segment; else by SegTable/DenseTable slot, nonzero: this segment
+  const uint8_t* flags;    // null: every segment; else the flagged ones (segment_flagged)
 };
 
 // delta[i][h] = dout[i][h] . o[i][h], one warp per row of the segments.
@@ -340,21 +340,23 @@ __device__ __forceinline__ void simt_p_ds(const float (&s)[4][2], const float (&
   }
 }
 
-// True if a segment of the table is these kernels' work: all of them, or (with
-// flags) those whose flag is set.
-template <typename Table>
-__device__ __forceinline__ bool simt_any(const Table& t, const int32_t* flags) {
-  if (!flags) return true;
-  bool any = false;
-  for (int i = threadIdx.x; i < t.n; i += blockDim.x) any |= flags[t.slot[i]] != 0;
-  return __syncthreads_or(any);
+// Flags of the bf16 gradient: 32 bytes for each 128 tokens of a segment (from its
+// first statistics tile on), one per 4 tokens; nonzero: they hold what is not
+// finite.  True if any of the segment's is; called by whole warps.
+__device__ __forceinline__ bool segment_flagged(const uint8_t* flags, int32_t tile, int32_t n) {
+  const uint4* f = reinterpret_cast<const uint4*>(flags) + 2 * (int64_t)tile;
+  uint32_t any = 0;
+  for (int i = threadIdx.x & 31; i < (n + 127) / 128 * 2; i += 32) {
+    const uint4 v = f[i];
+    any |= v.x | v.y | v.z | v.w;
+  }
+  return __any_sync(0xffffffffu, any != 0);
 }
 
 // dq of tiles of 64 rows, in chunks of 32 keys (dense.cuh); a piece of a cut
 // unit leaves its unscaled sum.
 template <typename T>
-__global__ void __launch_bounds__(dense_simt::kThreads, 1)
-    dense_dq_simt_kernel(const __grid_constant__ DenseTable t, DenseBwdArgs a, float* part) {
+__device__ __forceinline__ void simt_dq(const DenseTable& t, const DenseBwdArgs& a, float* part) {
   using namespace dense_simt;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
@@ -367,16 +369,13 @@ __global__ void __launch_bounds__(dense_simt::kThreads, 1)
   float* st_delta = st_lse + kBRows;
   const float s2 = a.scale * 1.4426950408889634f;
   const int tx = threadIdx.x & 15, ra = (threadIdx.x >> 4) * 4;
-  pdl_wait();
-  pdl_trigger();
-  if (!simt_any(t, a.flags)) return;
   DenseWalk walk;
   walk.init(t, blockIdx.x);
   DensePiece p;
   DenseUnit x;
   while (walk.next(t, p, x)) {
     const int si = x.si;
-    if (a.flags && !a.flags[t.slot[si]]) continue;
+    if (a.flags && !segment_flagged(a.flags, t.slot[si], t.q_len[si])) continue;
     __syncthreads();
     auto q_at = [&](int r) { return dense_q_row(t, x, x.row0 + r, a.H); };
     auto rows_of = [&](const void* base) {
@@ -454,8 +453,7 @@ __global__ void __launch_bounds__(dense_simt::kThreads, 1)
 // its unscaled sums, dv's rows kBKeys behind dk's.  (One block per unit held 64 of
 // 148 SMs at 989 tokens x 2 groups, and the longest of them 3.5 ms.)
 template <typename T>
-__global__ void __launch_bounds__(dense_simt::kThreads, 1)
-    dense_dkv_simt_kernel(const __grid_constant__ DenseTable t, DenseBwdArgs a, float* part) {
+__device__ __forceinline__ void simt_dkv(const DenseTable& t, const DenseBwdArgs& a, float* part) {
   using namespace dense_simt;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
@@ -468,15 +466,12 @@ __global__ void __launch_bounds__(dense_simt::kThreads, 1)
   float* st_delta = st_lse + kBRows;
   const float s2 = a.scale * 1.4426950408889634f;
   const int kq = (threadIdx.x >> 5) * 4, dl = (threadIdx.x & 31) * 4;
-  pdl_wait();
-  pdl_trigger();
-  if (!simt_any(t, a.flags)) return;
   DenseWalk walk;
   walk.init(t, blockIdx.x);
   DensePiece p;
   DenseUnit x;
   while (walk.next(t, p, x)) {
-    if (a.flags && !a.flags[t.slot[x.si]]) continue;
+    if (a.flags && !segment_flagged(a.flags, t.slot[x.si], t.q_len[x.si])) continue;
     __syncthreads();
     const int32_t j0 = x.row0, n = x.kv_len;
     const int64_t q0 = t.q_offset[x.si];
@@ -576,42 +571,90 @@ __global__ void __launch_bounds__(dense_simt::kThreads, 1)
   }
 }
 
-// Adds up the pieces of each cut unit in the order of their chunks, scales and
-// rounds: out, then (if given) out2 from the partial rows `rows2` behind.  One
-// warp per stationary row.  With flags: not the units of flagged segments.
-template <typename T>
-__global__ void __launch_bounds__(128)
-    dense_bwd_combine_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseSplits sp,
-                             const float* part, const int32_t* flags, T* out, float factor, T* out2,
-                             int rows2, int H) {
+// fp32: dq, or dk and dv, of a launch.
+__global__ void __launch_bounds__(dense_simt::kThreads, 1)
+    dense_dq_simt_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseBwdArgs a, float* part) {
   pdl_wait();
   pdl_trigger();
+  simt_dq<float>(t, a, part);
+}
+__global__ void __launch_bounds__(dense_simt::kThreads, 1)
+    dense_dkv_simt_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseBwdArgs a, float* part) {
+  pdl_wait();
+  pdl_trigger();
+  simt_dkv<float>(t, a, part);
+}
+// bf16: all gradients of the flagged segments, of which there are hardly ever
+// any; no unit of the tables is cut.
+__global__ void __launch_bounds__(dense_simt::kThreads, 1)
+    dense_bwd_flagged_kernel(const __grid_constant__ DenseTable rows, const __grid_constant__ DenseTable keys,
+                             const __grid_constant__ DenseBwdArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  bool any = false;
+  for (int i = threadIdx.x >> 5; i < rows.n; i += dense_simt::kThreads / 32)
+    any |= segment_flagged(a.flags, rows.slot[i], rows.q_len[i]);
+  if (!__syncthreads_or(any)) return;
+  simt_dq<__nv_bfloat16>(rows, a, nullptr);
+  simt_dkv<__nv_bfloat16>(keys, a, nullptr);
+}
+
+// Adds up the pieces of each cut unit in the order of their chunks, scales and
+// rounds.  blockIdx.z: an output of the call; one warp per stationary row.  With
+// flags: not the units of flagged segments.
+template <typename T>
+struct DenseBwdJoin {
+  const float* part;
+  T* out;
+  float factor;
+  int row;                 // of a unit's partial result, for its first stationary row
+  int keys;                // which table
+};
+template <typename T>
+struct DenseBwdJoins {
+  DenseBwdJoin<T> join[3];
+  const uint8_t* flags;    // or null
+  int H;
+};
+template <typename T>
+__global__ void __launch_bounds__(128)
+    dense_bwd_combine_kernel(const __grid_constant__ DenseTable rows, const __grid_constant__ DenseSplits srows,
+                             const __grid_constant__ DenseTable keys, const __grid_constant__ DenseSplits skeys,
+                             const __grid_constant__ DenseBwdJoins<T> joins) {
+  pdl_wait();
+  pdl_trigger();
+  const DenseBwdJoin<T>& w = joins.join[blockIdx.z];
+  const DenseTable& t = w.keys ? keys : rows;
+  const DenseSplits& sp = w.keys ? skeys : srows;
   const int i = blockIdx.x;
+  if (i >= sp.n) return;
   const int u = sp.unit[i];
   const DenseUnit x = dense_unit(t, u);
   const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (r >= x.nrows || (flags && flags[t.slot[x.si]])) return;
-  const int32_t row = x.row0 + r;
-  const int64_t at =
-      t.by_keys ? (int64_t)(t.q_offset[x.si] + row) * t.G + x.grp : dense_q_row(t, x, row, H);
-  for (int k = 0; k < (out2 ? 2 : 1); ++k) {
-    float acc[8] = {};
-    for (int c = sp.first[i]; c <= sp.last[i]; ++c) {
-      const int slot = dense_piece_slot(t, u, c);
-      if (slot < 0) continue;
+  if (r >= x.nrows || (joins.flags && segment_flagged(joins.flags, t.slot[x.si], t.q_len[x.si]))) return;
+  float acc[8] = {};
+  for (int c0 = sp.first[i]; c0 <= sp.last[i]; c0 += 32) {
+    const int my = c0 + lane <= sp.last[i] ? dense_piece_slot(t, u, c0 + lane) : -1;
+    const int n = min(32, sp.last[i] - c0 + 1);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const int slot = __shfl_sync(0xffffffffu, my, k);
       const float4* p =
-          reinterpret_cast<const float4*>(part + ((int64_t)slot * t.prows + r + k * rows2) * dense::kPartFloats);
-      const float4 v0 = p[2 * lane], v1 = p[2 * lane + 1];
+          reinterpret_cast<const float4*>(w.part + ((int64_t)max(slot, 0) * t.prows + w.row + r) * dense::kPartFloats);
+      const float4 v0 = slot >= 0 ? p[2 * lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 v1 = slot >= 0 ? p[2 * lane + 1] : make_float4(0.f, 0.f, 0.f, 0.f);
       acc[0] += v0.x; acc[1] += v0.y; acc[2] += v0.z; acc[3] += v0.w;
       acc[4] += v1.x; acc[5] += v1.y; acc[6] += v1.z; acc[7] += v1.w;
     }
-    const float f = k == 0 ? factor : 1.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] *= f;
-    Vec8<T> v;
-    v.set(acc);
-    v.store((k == 0 ? out : out2) + at * kHeadDim + lane * 8);
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] *= w.factor;
+  const int32_t row = x.row0 + r;
+  const int64_t at =
+      t.by_keys ? (int64_t)(t.q_offset[x.si] + row) * t.G + x.grp : dense_q_row(t, x, row, joins.H);
+  Vec8<T> v;
+  v.set(acc);
+  v.store(w.out + at * kHeadDim + lane * 8);
 }
 
 }  // namespace qsa
