@@ -419,7 +419,9 @@ qsa_status_t qsa_prompt_attn_fwd(const qsa_config_t* cfg, const qsa_segment_t* s
  * written (not accumulated into), other rows are left as they were.  fp32
  * accumulation in a fixed order, one rounding at the end: repeated calls give
  * the same bits.  bf16: P and the score gradients are rounded to bf16 for the
- * tensor-core products.  workspace: QSA_OP_PROMPT_ATTN_BWD.
+ * tensor-core products (a quarter of the latter with their remainders).  A
+ * prompt that holds infinities or NaN in k, v, lse or dout . o is done on CUDA
+ * cores, where only the pairs it enters see them.  workspace: QSA_OP_PROMPT_ATTN_BWD.
  */
 qsa_status_t qsa_prompt_attn_bwd(const qsa_config_t* cfg, const qsa_segment_t* segs,
                                  int32_t n_segs, int32_t n_tokens, const void* q, const void* k,
