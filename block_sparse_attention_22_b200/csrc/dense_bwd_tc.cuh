@@ -43,6 +43,10 @@
 // masked pairs are multiplied by zero.  Rows behind a segment's end may be
 // anything: their scores are replaced and their operand rows zeroed in shared
 // memory.  Every mbarrier wait is bounded.
+//
+// Measured (two prompts of 8192, 24 heads, 2 groups): dQ 1.75 ms, dV 1.35, dK 2.1,
+// 6.6 TFLOP issued in 5.2 ms, the tensor pipe 73 to 84 % active at the 1.3 to 1.5
+// GHz that the power cap leaves.
 #pragma once
 #include <type_traits>
 

@@ -14,7 +14,9 @@
 // log2 units), sum and O (128 registers); at the end of a piece the warps join
 // through shared memory.  P is rounded to bf16 for its product, the row sum
 // adds the unrounded values.  Tables, pieces and their join: dense.cuh, rows =
-// 16 and a chunk of 128 keys, 16 for each warp.
+// 16 and a chunk of 128 keys, 16 for each warp.  Measured: 32 sequences of 16K to
+// 50K keys (2.1 GB) 349 us with the join, 0.95 of the HBM rate; one row at 256K 100
+// us, 0.83.
 //
 // A token's keys are all visible to it, so nothing is masked but keys beyond
 // the sequence and of pages out of range: neither is read (zeros are filled
