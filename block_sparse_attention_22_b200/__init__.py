@@ -157,8 +157,22 @@ def make_cache(k_idx, khat, k, v) -> qsa_cache_t:
 def _stream(stream) -> int:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # a tenth of the public call's 3 us
+    if raw is not None:
+        return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+_TORCH = None
+
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def workspace_size(cfg, segs, n_tokens: int, op: int) -> int:
@@ -267,12 +281,13 @@ def make_pages(k, v, table) -> qsa_pages_t:
     _one_device("make_pages", k, v, table)
     pages = qsa_pages_t(_ptr(k), _ptr(v), _ptr(table), k.shape[0], k.shape[2], table.shape[0], table.shape[1])
     pages.tensors = (k, v, table)
+    pages.layout = (k.dtype, k.shape[1], k.shape[3], k.device)
     return pages
 
 
 def _one_device(where, *tensors):
     """The tensors' device; they are contiguous and on the current one."""
-    import torch
+    torch = _torch()
     dev = None
     for t in tensors:
         if t is None:
@@ -288,25 +303,20 @@ def _one_device(where, *tensors):
     return dev
 
 
-def _shaped(where, cfg, n_tokens, pages=None, **tensors):
-    """Checks the dtype and shape of token-major tensors: q-like names hold
-    n_q_heads rows per token, k/v-like names n_kv_groups; lse is fp32."""
-    import torch
-    want = torch.bfloat16 if cfg.dtype == QSA_DTYPE_BF16 else torch.float32
-    groups, dim = cfg.n_kv_groups, cfg.head_dim
-    if pages is not None:
-        pk = pages.tensors[0]
-        if pk.dtype != want or pk.shape[1] != groups or pk.shape[3] != dim:
-            raise ValueError(f"{where}: pages are {tuple(pk.shape)} {pk.dtype}, not {want} with {groups} groups "
-                             f"of {dim}")
-    kv, qo, stat = (n_tokens, groups, dim), (n_tokens, cfg.n_q_heads, dim), (n_tokens, cfg.n_q_heads)
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        shape = kv if name in ("k", "v", "dk", "dv") else stat if name == "lse" else qo
-        dtype = torch.float32 if name == "lse" else want
-        if t.shape != shape or t.dtype != dtype:
-            raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype}, not {shape} {dtype}")
+def _layout(where, cfg, n_tokens, pages=None):
+    """The I/O dtype and the shapes of k-like, q-like and lse tensors; checks the pages against them."""
+    torch = _torch()
+    dtype = torch.bfloat16 if cfg.dtype == QSA_DTYPE_BF16 else torch.float32
+    heads, groups, dim = cfg.n_q_heads, cfg.n_kv_groups, cfg.head_dim
+    if pages is not None and pages.layout[:3] != (dtype, groups, dim):
+        raise ValueError(f"{where}: pages are {tuple(pages.tensors[0].shape)} {pages.layout[0]}, not {dtype} with "
+                         f"{groups} groups of {dim}")
+    return dtype, (n_tokens, groups, dim), (n_tokens, heads, dim), (n_tokens, heads)
+
+
+def _check_like(where, name, t, shape, dtype):
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{where}: {name} is {tuple(t.shape)} {t.dtype}, not {shape} {dtype}")
 
 
 def _token_stride(where, name, t) -> int:
@@ -318,31 +328,44 @@ def _token_stride(where, name, t) -> int:
     return max(ld, heads * dim) if n <= 1 else ld
 
 
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
 def qsa_append_kv(cfg, pages, segs, n_tokens, k, v, q=None, q_out=None, stream=None):
     """Writes the tokens' k (rotated) and v to the paged cache, and the rotated q to q_out.
     k, v, q: [T, heads, D]; the tokens may be strided (slices of a fused projection)."""
     where = "qsa_append_kv"
     arr, n = segs
-    _shaped(where, cfg, n_tokens, pages, k=k, v=v, q=q, q_out=q_out)
-    _one_device(where, q_out, *pages.tensors)
-    for t in (k, v, q):
-        if t is not None and t.device != pages.tensors[0].device:
-            raise ValueError(f"{where}: tensors on {t.device} and {pages.tensors[0].device}")
-    _check(get_lib().qsa_append_kv(ctypes.byref(cfg), ctypes.byref(pages), arr, n, n_tokens, _ptr(k),
-                                   _token_stride(where, "k", k), _ptr(v), _token_stride(where, "v", v), _ptr(q),
-                                   0 if q is None else _token_stride(where, "q", q), _ptr(q_out), _stream(stream)),
-           where)
+    dtype, kv, qo, _ = _layout(where, cfg, n_tokens, pages)
+    _check_like(where, "k", k, kv, dtype)
+    _check_like(where, "v", v, kv, dtype)
+    dev = _one_device(where, pages.tensors[2], q_out)
+    ld_q = 0
+    if q is not None:
+        _check_like(where, "q", q, qo, dtype)
+        ld_q = _token_stride(where, "q", q)
+    if q_out is not None:
+        _check_like(where, "q_out", q_out, qo, dtype)
+    if k.device != dev or v.device != dev or (q is not None and q.device != dev):
+        raise ValueError(f"{where}: tensors on {dev} and {', '.join(str(t.device) for t in (k, v, q) if t is not None)}")
+    _check(get_lib().qsa_append_kv(cfg, pages, arr, n, n_tokens, k.data_ptr(), _token_stride(where, "k", k),
+                                   v.data_ptr(), _token_stride(where, "v", v), _ptr(q), ld_q, _ptr(q_out),
+                                   _stream(stream)), where)
 
 
 def qsa_paged_attn_fwd(cfg, pages, segs, n_tokens, q, o, lse=None, workspace=None, stream=None):
     """Dense causal attention of the new tokens over the paged cache (workspace: QSA_OP_PAGED_ATTN)."""
     where = "qsa_paged_attn_fwd"
     arr, n = segs
-    _shaped(where, cfg, n_tokens, pages, q=q, o=o, lse=lse)
-    _one_device(where, q, o, lse, workspace, *pages.tensors)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(get_lib().qsa_paged_attn_fwd(ctypes.byref(cfg), ctypes.byref(pages), arr, n, n_tokens, _ptr(q), _ptr(o),
-                                        _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)), where)
+    dtype, _, qo, stat = _layout(where, cfg, n_tokens, pages)
+    _check_like(where, "q", q, qo, dtype)
+    _check_like(where, "o", o, qo, dtype)
+    if lse is not None:
+        _check_like(where, "lse", lse, stat, _torch().float32)
+    _one_device(where, q, o, lse, workspace, pages.tensors[2])
+    _check(get_lib().qsa_paged_attn_fwd(cfg, pages, arr, n, n_tokens, q.data_ptr(), o.data_ptr(), _ptr(lse),
+                                        _ptr(workspace), _bytes(workspace), _stream(stream)), where)
 
 
 def qsa_prompt_attn_fwd(cfg, segs, n_tokens, q, k, v, o, lse=None, workspace=None, stream=None):
@@ -350,11 +373,14 @@ def qsa_prompt_attn_fwd(cfg, segs, n_tokens, q, k, v, o, lse=None, workspace=Non
     (workspace: QSA_OP_PROMPT_ATTN)."""
     where = "qsa_prompt_attn_fwd"
     arr, n = segs
-    _shaped(where, cfg, n_tokens, q=q, k=k, v=v, o=o, lse=lse)
+    dtype, kv, qo, stat = _layout(where, cfg, n_tokens)
+    for name, t, shape in (("q", q, qo), ("k", k, kv), ("v", v, kv), ("o", o, qo)):
+        _check_like(where, name, t, shape, dtype)
+    if lse is not None:
+        _check_like(where, "lse", lse, stat, _torch().float32)
     _one_device(where, q, k, v, o, lse, workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(get_lib().qsa_prompt_attn_fwd(ctypes.byref(cfg), arr, n, n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(o),
-                                         _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)), where)
+    _check(get_lib().qsa_prompt_attn_fwd(cfg, arr, n, n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+                                         _ptr(workspace), _bytes(workspace), _stream(stream)), where)
 
 
 def qsa_prompt_attn_bwd(cfg, segs, n_tokens, q, k, v, o, lse, dout, dq, dk, dv, workspace=None, stream=None):
@@ -362,12 +388,15 @@ def qsa_prompt_attn_bwd(cfg, segs, n_tokens, q, k, v, o, lse, dout, dq, dk, dv, 
     (workspace: QSA_OP_PROMPT_ATTN_BWD)."""
     where = "qsa_prompt_attn_bwd"
     arr, n = segs
-    _shaped(where, cfg, n_tokens, q=q, k=k, v=v, o=o, lse=lse, dout=dout, dq=dq, dk=dk, dv=dv)
+    dtype, kv, qo, stat = _layout(where, cfg, n_tokens)
+    for name, t, shape in (("q", q, qo), ("k", k, kv), ("v", v, kv), ("o", o, qo), ("dout", dout, qo), ("dq", dq, qo),
+                           ("dk", dk, kv), ("dv", dv, kv)):
+        _check_like(where, name, t, shape, dtype)
+    _check_like(where, "lse", lse, stat, _torch().float32)
     _one_device(where, q, k, v, o, lse, dout, dq, dk, dv, workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(get_lib().qsa_prompt_attn_bwd(ctypes.byref(cfg), arr, n, n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(o),
-                                         _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-                                         ws_bytes, _stream(stream)), where)
+    _check(get_lib().qsa_prompt_attn_bwd(cfg, arr, n, n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+                                         _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), _bytes(workspace),
+                                         _stream(stream)), where)
 
 
 def qsa_device_status(stream=None):
