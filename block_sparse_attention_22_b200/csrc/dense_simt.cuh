@@ -9,7 +9,11 @@
 // scores and the same R rows x 16 dims of the result; the 16 threads of a row
 // are half a warp, so the softmax exchanges by shuffles.  cp.async brings the
 // next chunk's K during the softmax and products of this one and its V during
-// the next scores.
+// the next scores.  At two warps per scheduler FMA and shared-memory reads hardly
+// overlap, so what counts is reads per product and instructions: packed f32x2
+// products, tiles as large as the registers allow.  Measured: the training step of
+// prompts of 256, 700 and 33 tokens (24 heads, 2 groups, 24 GFLOP) 1.06 ms,
+// the FMA pipe half busy, shared-memory reads two thirds.
 //
 // Masked places may hold anything: keys past the sequence are filled with
 // zeros instead of being read, scores of keys after the row's position are
@@ -102,7 +106,7 @@ __device__ __forceinline__ void simt_dots(const float* a, const float* b, int ra
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[i][j] = make_float2(0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 8
   for (int d = 0; d < kHeadDim; d += 4) {
     float4 x[R], y[N];
 #pragma unroll
@@ -130,6 +134,7 @@ template <int R>
 __device__ __forceinline__ void simt_accumulate(const float* p, int ldp, const float* b, int ra, int tx, int n,
                                                 bool limited, const int (&limit)[R], float (&acc)[R][16]) {
   using dense_simt::kLd;
+#pragma unroll 2
   for (int k = 0; k < n; k += 4) {
     float4 w[R];
 #pragma unroll
@@ -317,6 +322,61 @@ __global__ void __launch_bounds__(256)
   if (lane == 0) delta[at] = s;
 }
 
+// The gradient's products of 64 rows of a with 32 rows of b: a thread adds up 8 x 4
+// of them over a quarter of the dims (every fourth group of four), so that 12
+// shared-memory reads feed 128 products (4 x 2 over all dims: 6 for 32); the four
+// quarters, in the lanes 8 apart, then meet by exchanging halves.  out[i][j] is
+// that of row simt_row0() + i and key simt_key0() + j.
+__device__ __forceinline__ int simt_row0() {
+  const int lane = threadIdx.x & 31;
+  return (threadIdx.x >> 6) * 16 + 4 * ((lane >> 2) & 1) + 8 * ((lane >> 3) & 1);
+}
+__device__ __forceinline__ int simt_key0() {
+  const int lane = threadIdx.x & 31;
+  return ((threadIdx.x >> 5) & 1) * 16 + 4 * (lane & 3) + 2 * (lane >> 4);
+}
+__device__ __forceinline__ void simt_dots_64x32(const float* a, const float* b, float (&out)[4][2]) {
+  using dense_simt::kLd;
+  const int lane = threadIdx.x & 31, quarter = lane >> 3;
+  const float* pa = a + ((threadIdx.x >> 6) * 16 + 4 * ((lane >> 2) & 1)) * kLd + 4 * quarter;
+  const float* pb = b + (((threadIdx.x >> 5) & 1) * 16 + 4 * (lane & 3)) * kLd + 4 * quarter;
+  float2 acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 2
+  for (int d = 0; d < kHeadDim; d += 16) {
+    float4 x[8], y[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const float4*>(pa + ((i & 3) + 8 * (i >> 2)) * kLd + d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(pb + j * kLd + d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = fma2(lo2(x[i]), lo2(y[j]), acc[i][j]);
+        acc[i][j] = fma2(hi2(x[i]), hi2(y[j]), acc[i][j]);
+      }
+  }
+  const bool odd = quarter & 1, high = quarter & 2;
+  float half[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v0 = acc[i][j].x + acc[i][j].y, v1 = acc[i + 4][j].x + acc[i + 4][j].y;
+      half[i][j] = (odd ? v1 : v0) + __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 8);
+    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      out[i][j] = (high ? half[i][j + 2] : half[i][j]) +
+                  __shfl_xor_sync(0xffffffffu, high ? half[i][j] : half[i][j + 2], 16);
+}
+
 // From a thread's scores and dP of 64 rows x 32 keys, P (if Ps) and dS into shared
 // memory ([row][key]); row statistics in st_lse (log2 units) and st_delta; masked
 // entries are zero.  row0: the tile's first row, in rows of the segment.
@@ -324,14 +384,14 @@ __device__ __forceinline__ void simt_p_ds(const float (&s)[4][2], const float (&
                                           const float* st_lse, const float* st_delta, int32_t row0, int nrows, int hpg,
                                           int32_t j0, int32_t n_keys, float s2) {
   using namespace dense_simt;
-  const int tx = threadIdx.x & 15, ra = (threadIdx.x >> 4) * 4;
+  const int ra = simt_row0(), ka = simt_key0();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ra + i;
     const int32_t pos = (row0 + r) / hpg;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int key = tx + 16 * j;
+      const int key = ka + j;
       const bool seen = r < nrows && j0 + key <= pos && j0 + key < n_keys;
       const float p = seen ? exp2f(fmaf(s[i][j], s2, -st_lse[r])) : 0.f;
       if (Ps) Ps[r * kBLd + key] = p;
@@ -412,10 +472,10 @@ __device__ __forceinline__ void simt_dq(const DenseTable& t, const DenseBwdArgs&
       float sc[4][2], dp[4][2];
       sm100::cp_async_wait<1>();
       __syncthreads();
-      simt_dots<4, 2>(Os, Vs, ra, tx, dp);
+      simt_dots_64x32(Os, Vs, dp);
       sm100::cp_async_wait<0>();
       __syncthreads();
-      simt_dots<4, 2>(Qs, Ks, ra, tx, sc);
+      simt_dots_64x32(Qs, Ks, sc);
       simt_p_ds(sc, dp, nullptr, Ds, st_lse, st_delta, x.row0, x.nrows, t.hpg, j0, x.kv_len, s2);
       __syncthreads();
       if (c + 1 < p.c1) load_keys(Vs, a.v, c + 1);
@@ -505,7 +565,6 @@ __device__ __forceinline__ void simt_dkv(const DenseTable& t, const DenseBwdArgs
     sm100::cp_async_commit();
     load_chunk(Qs, a.q, p.c0, false);
     sm100::cp_async_commit();
-    const int tx = threadIdx.x & 15, ra = (threadIdx.x >> 4) * 4;
     // dO of the next chunk loads under this one's dk, Q under the next one's dP
     for (int c = p.c0; c < p.c1; ++c) {
       const int32_t i0 = j0 + c / t.hpg * kBRows;
@@ -513,17 +572,17 @@ __device__ __forceinline__ void simt_dkv(const DenseTable& t, const DenseBwdArgs
       float sc[4][2], dp[4][2];
       sm100::cp_async_wait<1>();
       __syncthreads();
-      simt_dots<4, 2>(Os, Vs, ra, tx, dp);
+      simt_dots_64x32(Os, Vs, dp);
       sm100::cp_async_wait<0>();
       __syncthreads();
-      simt_dots<4, 2>(Qs, Ks, ra, tx, sc);
+      simt_dots_64x32(Qs, Ks, sc);
       simt_p_ds(sc, dp, Ps, Ds, st_lse, st_delta, i0, nrows, 1, j0, n, s2);
       __syncthreads();
       // sums over the chunk's rows of w[row][key] times the row, for this thread's
       // keys; a row before a key does not touch it
       const bool limited = j0 + kBKeys - 1 > i0;
       auto add_rows = [&](const float* w, const float* rows, float (&g)[4][8]) {
-#pragma unroll 2
+#pragma unroll 4
         for (int r = 0; r < nrows; ++r) {
           const float4 wr = *reinterpret_cast<const float4*>(w + r * kBLd + kq);
           const float ww[4] = {wr.x, wr.y, wr.z, wr.w};
