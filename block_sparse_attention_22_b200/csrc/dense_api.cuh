@@ -227,8 +227,8 @@ struct DenseGroup {
   std::vector<DenseLaunch> launches;
 };
 
-// bf16: single tokens over a cache go to the decode kernel, other segments of
-// at most 128 rows to single CTAs unless larger ones are there, whose pairs then
+// Single tokens over a cache go to the decode kernels.  bf16: other segments of
+// at most 128 rows go to single CTAs unless larger ones are there, whose pairs then
 // take them too (one launch and its tail, 15 us, for a few half-empty tiles).
 std::vector<DenseGroup> dense_groups(const Geo& g, bool tc, bool paged, const qsa_segment_t* segs, int n) {
   DenseGroup wide{DenseForm::kWide, {}, {}, {}}, narrow{DenseForm::kNarrow, {}, {}, {}},
@@ -238,15 +238,15 @@ std::vector<DenseGroup> dense_groups(const Geo& g, bool tc, bool paged, const qs
     using W = dense_tc::Shape<2>;
     narrow.kind = {N::kRows, N::kKeys, N::kGrid, false};
     wide.kind = {W::kRows, W::kKeys, W::kGrid, false, 4, 4};      // a unit's 5.5 us in chunks of 1.4 us
-    decode.kind = {dense_decode::kRows, dense_decode::kKeys, kNumSms, false, 1, 1};
   } else {
     narrow.kind = {dense_simt::kRowsNarrow, dense_simt::kKeys, kNumSms, false};
     wide.kind = {dense_simt::kRowsWide, dense_simt::kKeys, kNumSms, false};
   }
+  decode.kind = {dense_decode::kRows, dense_decode::kKeys, kNumSms, false, 1, 1};
   for (int i = 0; i < n; ++i) {
     if (segs[i].q_len <= 0) continue;
     const bool few = (int64_t)segs[i].q_len * g.hpg <= narrow.kind.rows;
-    (tc && paged && segs[i].q_len == 1 ? decode : few ? narrow : wide).segs.push_back(segs[i]);
+    (paged && segs[i].q_len == 1 ? decode : few ? narrow : wide).segs.push_back(segs[i]);
   }
   if (tc && !wide.segs.empty()) {
     wide.segs.insert(wide.segs.end(), narrow.segs.begin(), narrow.segs.end());
@@ -335,6 +335,21 @@ cudaError_t launch_dense_decode(const DenseTable& t, const DenseTcArgs& a, cudaS
                         t, a);
 }
 
+template <int HP>
+cudaError_t launch_decode_f32(const DenseTable& t, const DenseDecodeF32Args& a, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(dense_decode_f32_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             dense_decode::kSmemBytes32);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return launch_chained(dense_decode_f32_kernel<HP>, dim3(t.grid), dim3(dense_decode::kThreads),
+                        dense_decode::kSmemBytes32, st, t, a);
+}
+cudaError_t launch_dense_decode(const DenseTable& t, const DenseDecodeF32Args& a, cudaStream_t st) {
+  if (t.hpg <= 4) return launch_decode_f32<4>(t, a, st);
+  if (t.hpg <= 8) return launch_decode_f32<8>(t, a, st);
+  return t.hpg <= 12 ? launch_decode_f32<12>(t, a, st) : launch_decode_f32<16>(t, a, st);
+}
+
 template <typename T>
 cudaError_t launch_dense_combine(const Geo& g, const DenseTable& t, const DenseSplits& sp, const float* part, void* o,
                                  float* lse, cudaStream_t st) {
@@ -381,7 +396,11 @@ qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int
       a.part = part_of(x);
       cudaError_t e;
       if (d.form == DenseForm::kDecode)
-        e = launch_dense_decode(x.t, a, st);
+        e = tc ? launch_dense_decode(x.t, a, st)
+               : launch_dense_decode(x.t,
+                                     DenseDecodeF32Args{kv, (const float*)q, (float*)o, lse, part_of(x), g.H, g.scale,
+                                                        false},
+                                     st);
       else if (tc)
         e = is_wide ? launch_dense_tc<2, PAGED>(x.t, m, a, st) : launch_dense_tc<1, PAGED>(x.t, m, a, st);
       else

@@ -56,6 +56,41 @@ __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], const uint32_t (&a)[
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Joins the warps' maxima, sums and O (in shared memory, a warp's over its slots)
+// of a piece: a whole unit's result, or the piece's partial one.  Thread d has
+// dim d.
+template <typename T>
+__device__ __forceinline__ void decode_join(const DenseUnit& x, const DensePiece& p, int prows, int64_t head0,
+                                            const unsigned char* smem, const float* m_s, const float* l_s, T* o,
+                                            float* lse, float* part) {
+  using namespace dense_decode;
+  const int d = threadIdx.x;
+  for (int r = 0; r < x.nrows; ++r) {
+    float mr = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, m_s[w * kRows + r]);
+    float lr = 0.f, v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = m_s[w * kRows + r];
+      const float f = mw == -INFINITY ? 0.f : exp2f(mw - mr);
+      lr = fmaf(f, l_s[w * kRows + r], lr);
+      v = fmaf(f, reinterpret_cast<const float*>(smem + w * kSlots * kSlotBytes)[r * kOLd + d], v);
+    }
+    if (p.part < 0) {
+      o[(head0 + r) * kHeadDim + d] = IO<T>::from_f(lr != 0.f ? v / lr : 0.f);
+      if (d == 0 && lse) lse[head0 + r] = lr != 0.f ? (mr + log2f(lr)) * 0.6931471805599453f : -INFINITY;
+    } else {
+      float* dst = part + ((int64_t)p.part * prows + r) * dense::kPartFloats;
+      dst[d] = v;
+      if (d == 0) {
+        dst[kHeadDim] = mr;
+        dst[kHeadDim + 1] = lr;
+      }
+    }
+  }
+}
+
 __global__ void __launch_bounds__(dense_decode::kThreads, 1)
     dense_decode_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseTcArgs a) {
   using namespace dense_decode;
@@ -239,31 +274,265 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
       *reinterpret_cast<float2*>(dst + 8 * kOLd) = make_float2(o[j][2], o[j][3]);
     }
     __syncthreads();
-    const int d = threadIdx.x;                            // dim
-    for (int r = 0; r < x.nrows; ++r) {
-      float mr = -INFINITY;
+    decode_join(x, p, t.prows, head0, smem, m_s, l_s, a.o, a.lse, a.part);
+    __syncthreads();                                      // shared memory free for the next piece
+  }
+  dense_wait_last(a.late);
+}
+
+// ------------------------------------------------------------------ fp32
+// The same for fp32, on CUDA cores: 12 heads make 6 products per byte, half of
+// what the FMA pipe does at HBM rate.  A warp takes 16 keys of a chunk four at a
+// time through six 4 KiB slots (K, V, K, V, ...); a lane holds 8 dims of the four
+// rows and of every head's O, reads each head's q from shared memory (two reads
+// for 32 products), and the 4 x HP sums over the lanes are reduced together, halving
+// their number with each exchange.  Lane h then does head h's softmax.  HP: heads,
+// rounded up to 4.
+namespace dense_decode {
+constexpr int kStep = 4;                              // keys
+constexpr int kF32Slots = 6, kF32SlotBytes = kStep * kHeadDim * 4;
+static_assert(kF32Slots * kF32SlotBytes == kSlots * kSlotBytes, "a warp's slots as in the bf16 kernel");
+constexpr int kOffQ32 = kWarps * kSlots * kSlotBytes;
+constexpr int kOffStat32 = kOffQ32 + kRows * kHeadDim * 4;
+constexpr int kOffP32 = kOffStat32 + 2 * kWarps * kRows * 4;         // per warp: scores or P [16][4], factors [16]
+constexpr int kSmemBytes32 = kOffP32 + kWarps * (kRows * kStep + kRows) * 4;
+}  // namespace dense_decode
+
+struct DenseDecodeF32Args {
+  KvSource kv;
+  const float* q;           // [T][H][D]
+  float* o;
+  float* lse;               // [T][H] or null
+  float* part;
+  int H;
+  float scale;
+  bool late;                // dense_wait_first
+};
+
+// Sums of v[0 .. N-1] over the warp's lanes, the number of values halved at each of
+// the first exchanges (MASK = 16, 8, ..) while it is even; `base` ends as the index
+// of the first sum that the lane is left with.
+template <int N, int MASK>
+__device__ __forceinline__ void reduce_halving(float* v, int& base) {
+  if constexpr (MASK >= 1) {
+    const bool up = threadIdx.x & MASK;
+    if constexpr (N % 2 == 0) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, m_s[w * kRows + r]);
-      float lr = 0.f, v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = m_s[w * kRows + r];
-        const float f = mw == -INFINITY ? 0.f : exp2f(mw - mr);
-        lr = fmaf(f, l_s[w * kRows + r], lr);
-        v = fmaf(f, reinterpret_cast<const float*>(smem + w * kSlots * kSlotBytes)[r * kOLd + d], v);
+      for (int i = 0; i < N / 2; ++i) {
+        const float keep = up ? v[i + N / 2] : v[i], send = up ? v[i] : v[i + N / 2];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, MASK);
       }
-      if (p.part < 0) {
-        a.o[(head0 + r) * kHeadDim + d] = __float2bfloat16_rn(lr != 0.f ? v / lr : 0.f);
-        if (d == 0 && a.lse) a.lse[head0 + r] = lr != 0.f ? (mr + log2f(lr)) * 0.6931471805599453f : -INFINITY;
-      } else {
-        float* dst = a.part + ((int64_t)p.part * t.prows + r) * dense::kPartFloats;
-        dst[d] = v;
-        if (d == 0) {
-          dst[kHeadDim] = mr;
-          dst[kHeadDim + 1] = lr;
+      base += up ? N / 2 : 0;
+      reduce_halving<N / 2, MASK / 2>(v, base);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], MASK);
+      reduce_halving<N, MASK / 2>(v, base);
+    }
+  }
+}
+constexpr int reduce_left(int n, int mask) {
+  return mask < 1 ? n : n % 2 == 0 ? reduce_left(n / 2, mask / 2) : reduce_left(n, mask / 2);
+}
+
+template <int HP>
+__global__ void __launch_bounds__(dense_decode::kThreads, 1)
+    dense_decode_f32_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseDecodeF32Args a) {
+  using namespace dense_decode;
+  using namespace sm100;
+  extern __shared__ __align__(1024) unsigned char smem_1k[];
+  unsigned char* const smem = smem_1k;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned char* const ring = smem + warp * kF32Slots * kF32SlotBytes;
+  float* const q_s = reinterpret_cast<float*>(smem + kOffQ32);
+  float* const m_s = reinterpret_cast<float*>(smem + kOffStat32);
+  float* const l_s = m_s + kWarps * kRows;
+  float* const p_s = reinterpret_cast<float*>(smem + kOffP32) + warp * (kRows * kStep + kRows);
+  float* const f_s = p_s + kRows * kStep;
+  const float tau2 = a.scale * 1.4426950408889634f;
+  dense_wait_first(a.late);
+  DenseWalk walk;
+  walk.init(t, blockIdx.x);
+  DensePiece p;
+  DenseUnit x;
+  while (walk.next(t, p, x)) {
+    const int64_t head0 = (int64_t)t.q_offset[x.si] * a.H + x.grp * t.hpg;
+    for (int i = threadIdx.x; i < kRows * (kHeadDim / 4); i += kThreads) {     // rows beyond the heads zero
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i / (kHeadDim / 4) < x.nrows) v = reinterpret_cast<const float4*>(a.q + head0 * kHeadDim)[i];
+      reinterpret_cast<float4*>(q_s)[i] = v;
+    }
+    // this warp's keys: 16 of each chunk, in steps of 4 (step j: chunk j / 4)
+    const int32_t key0 = p.c0 * kKeys + warp * kTile;
+    const int nc = min(p.c1 - p.c0, max(0, (x.kv_len - key0 + kKeys - 1) / kKeys)), n = nc * (kTile / kStep);
+    int32_t look0 = -32;
+    int64_t my_row = -1;
+    auto chunk_row = [&](int c) -> int64_t {              // first cache row of this warp's 16 keys of chunk c
+      if (c - look0 >= 32) {
+        look0 = c;
+        const int32_t key = key0 + (c + lane) * kKeys;
+        my_row = -1;
+        if (c + lane < nc) {
+          const int32_t pi = key / a.kv.page_tokens;
+          const int32_t page = a.kv.table[(int64_t)t.slot[x.si] * a.kv.max_pages + pi];
+          if (page >= 0 && page < a.kv.n_pages)
+            my_row = ((int64_t)page * t.G + x.grp) * a.kv.page_tokens + (key - pi * a.kv.page_tokens);
+          else
+            report_error(kErrBadIndex);
         }
       }
+      return __shfl_sync(0xffffffffu, my_row, c - look0);
+    };
+    auto load = [&](int j) {                              // K and V of step j, one group each
+      int64_t row = -1;
+      int valid = 0;
+      if (j < n) {
+        row = chunk_row(j / (kTile / kStep));
+        valid = row < 0 ? 0 : max(0, min(kStep, x.kv_len - (key0 + j / (kTile / kStep) * kKeys + j % (kTile / kStep) * kStep)));
+        if (valid > 0) row += j % (kTile / kStep) * kStep;
+      }
+#pragma unroll
+      for (int is_v = 0; is_v < 2; ++is_v) {
+        if (j < n) {
+          const float* src = (const float*)(is_v ? a.kv.v : a.kv.k) + (valid > 0 ? row : 0) * kHeadDim + lane * 4;
+          const uint32_t dst = smem_u32(ring + (2 * j + is_v) % kF32Slots * kF32SlotBytes) + lane * 16;
+#pragma unroll
+          for (int r = 0; r < kStep; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              cp_async16(dst + r * (kHeadDim * 4) + h * 512, r < valid ? src + r * kHeadDim + h * 128 : src,
+                         r < valid ? 16u : 0u);
+        }
+        cp_async_commit();
+      }
+      return row;
+    };
+    float2 o[HP][4];                                      // dims 4 lane .. +3 and 128 + 4 lane .. +3
+#pragma unroll
+    for (int h = 0; h < HP; ++h)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[h][k] = make_float2(0.f, 0.f);
+    float m = -INFINITY, l = 0.f;                         // of head `lane`
+    int64_t rows_ahead[3];                                // of the steps in flight, oldest first
+#pragma unroll
+    for (int j = 0; j < 3; ++j) rows_ahead[j] = load(j);
+    __syncthreads();                                      // q written
+    for (int j = 0; j < n; ++j) {
+      const bool bad = rows_ahead[0] < 0;
+      // ---- scores
+      cp_async_wait<5>();
+      __syncwarp();
+      float dots[HP * kStep];
+      {
+        const float4* ks = reinterpret_cast<const float4*>(ring + (2 * j) % kF32Slots * kF32SlotBytes) + lane;
+        float4 k0[kStep], k1[kStep];
+#pragma unroll
+        for (int r = 0; r < kStep; ++r) {
+          k0[r] = ks[r * 64];
+          k1[r] = ks[r * 64 + 32];
+        }
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          const float4 q0 = reinterpret_cast<const float4*>(q_s + h * kHeadDim)[lane];
+          const float4 q1 = reinterpret_cast<const float4*>(q_s + h * kHeadDim)[lane + 32];
+#pragma unroll
+          for (int r = 0; r < kStep; ++r) {
+            float2 s = fma2(lo2(q0), lo2(k0[r]), make_float2(0.f, 0.f));
+            s = fma2(hi2(q0), hi2(k0[r]), s);
+            s = fma2(lo2(q1), lo2(k1[r]), s);
+            s = fma2(hi2(q1), hi2(k1[r]), s);
+            dots[h * kStep + r] = s.x + s.y;
+          }
+        }
+      }
+      int base = 0;
+      reduce_halving<HP * kStep, 16>(dots, base);
+#pragma unroll
+      for (int i = 0; i < reduce_left(HP * kStep, 16); ++i) p_s[base + i] = dots[i];
+      __syncwarp();
+      // ---- softmax of head `lane`
+      bool need = false;
+      if (lane < HP) {
+        const int left = bad ? 0 : x.kv_len - (key0 + j / (kTile / kStep) * kKeys + j % (kTile / kStep) * kStep);
+        float4 s4 = reinterpret_cast<const float4*>(p_s)[lane];
+        float s[kStep] = {s4.x, s4.y, s4.z, s4.w}, mx = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < kStep; ++r) {
+          s[r] = r < left ? s[r] * tau2 : -INFINITY;
+          mx = fmaxf(mx, s[r]);
+        }
+        float f = 1.f;
+        if (mx > m + 8.f) {                               // false while both are -inf
+          if (m != -INFINITY) {
+            f = exp2f(m - mx);
+            need = true;
+          }
+          m = mx;
+        }
+        f_s[lane] = f;
+        l *= f;
+        const float mb = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int r = 0; r < kStep; ++r) {
+          s[r] = exp2f(s[r] - mb);
+          l += s[r];
+        }
+        reinterpret_cast<float4*>(p_s)[lane] = make_float4(s[0], s[1], s[2], s[3]);
+      }
+      __syncwarp();
+      if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          const float f = f_s[h];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[h][k] = make_float2(o[h][k].x * f, o[h][k].y * f);
+        }
+      }
+      // ---- O += P V
+      cp_async_wait<4>();
+      __syncwarp();
+      {
+        const float4* vs = reinterpret_cast<const float4*>(ring + (2 * j + 1) % kF32Slots * kF32SlotBytes) + lane;
+        float4 v0[kStep], v1[kStep];
+#pragma unroll
+        for (int r = 0; r < kStep; ++r) {
+          v0[r] = vs[r * 64];
+          v1[r] = vs[r * 64 + 32];
+        }
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+          const float4 p4 = reinterpret_cast<const float4*>(p_s)[h];
+          const float pr[kStep] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+          for (int r = 0; r < kStep; ++r) {
+            const float2 f = make_float2(pr[r], pr[r]);
+            o[h][0] = fma2(f, lo2(v0[r]), o[h][0]);
+            o[h][1] = fma2(f, hi2(v0[r]), o[h][1]);
+            o[h][2] = fma2(f, lo2(v1[r]), o[h][2]);
+            o[h][3] = fma2(f, hi2(v1[r]), o[h][3]);
+          }
+        }
+      }
+      __syncwarp();                                       // the step's slots and P are read
+      rows_ahead[0] = rows_ahead[1];
+      rows_ahead[1] = rows_ahead[2];
+      rows_ahead[2] = load(j + 3);
     }
+    // ---- join the warps
+    cp_async_wait_all();
+    __syncwarp();
+    if (lane < kRows) {
+      m_s[warp * kRows + lane] = lane < HP ? m : -INFINITY;
+      l_s[warp * kRows + lane] = lane < HP ? l : 0.f;
+    }
+    float* const o_s = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int h = 0; h < HP; ++h) {
+      reinterpret_cast<float4*>(o_s + h * kOLd)[lane] = make_float4(o[h][0].x, o[h][0].y, o[h][1].x, o[h][1].y);
+      reinterpret_cast<float4*>(o_s + h * kOLd)[lane + 32] = make_float4(o[h][2].x, o[h][2].y, o[h][3].x, o[h][3].y);
+    }
+    __syncthreads();
+    decode_join(x, p, t.prows, head0, smem, m_s, l_s, a.o, a.lse, a.part);
     __syncthreads();                                      // shared memory free for the next piece
   }
   dense_wait_last(a.late);

@@ -74,6 +74,35 @@ def test_decode_lengths_around_the_tiles(heads, groups, page):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("heads,groups", [(24, 2), (32, 2), (14, 2), (8, 1), (4, 1), (5, 5)])
+@pytest.mark.parametrize("page", [16, 48, 256])
+def test_fp32_decode_lengths_around_the_tiles(heads, groups, page):
+    lens = [1, 2, 3, 4, 5, 15, 16, 17, 18, 31, 33, 48, 49, 127, 128, 129, 131, 144, 255, 257, 1000, 4099]
+    x = _cache(heads, groups, page, [(n - 1, 1) for n in lens], dtype="f32")
+    o, lse = _attend(x)
+    qsa.qsa_device_status()
+    _check(x, o, lse)
+    o2, lse2 = _attend(x)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_fp32_decode_rescales_and_skips_bad_pages():
+    x = _cache(24, 2, 16, [(900, 1), (300, 1)], seed=14, dtype="f32")
+    k, v = x["kv"][0]
+    k.add_(torch.linspace(0, 3, k.shape[0], device="cuda")[:, None, None])
+    fill_pages(x["kp"], x["vp"], x["table"], 16, 0, k, v)
+    x["q"].add_(0.7)
+    t = x["table"].clone()
+    t[0, 5], t[0, 56], t[1, :] = -1, 1 << 30, -2          # 56 holds the row's own key
+    x["pages"] = qsa.make_pages(x["kp"], x["vp"], t.cuda())
+    o, lse = _attend(x)
+    assert qsa.device_status() == qsa.QSA_ERR_BAD_INDEX
+    keep = torch.tensor([j for j in range(901) if j // 16 not in (5, 56)]).cuda()
+    q = x["q"][:1]
+    check_forward(o[:1], lse[:1], attend64(q, k[keep], v[keep], 900, SCALE), score_error(q, k, SCALE), x["dt"])
+    assert (o[1] == 0).all() and (lse[1] == -math.inf).all()
+
+
 def test_decode_of_one_long_row_in_many_pieces():
     x = _cache(24, 2, 64, [(50000, 1)], seed=2)
     o, lse = _attend(x)
