@@ -20,6 +20,8 @@
 // replaced, and in a chunk that holds such keys their V rows are skipped
 // row by row (0 * NaN would spread).
 #pragma once
+#include <type_traits>
+
 #include "qsa_internal.cuh"
 #include "sm100.cuh"
 #include "dense.cuh"
@@ -130,9 +132,9 @@ __device__ __forceinline__ void simt_dots(const float* a, const float* b, int ra
 // acc[i][16] += sum over n keys of p[row ra + i][key] * b[key][dims]; the
 // thread's dims are 4 tx + 64 jj.  With limit[i] < n only the first limit[i]
 // keys of row i are added.
-template <int R>
-__device__ __forceinline__ void simt_accumulate(const float* p, int ldp, const float* b, int ra, int tx, int n,
-                                                bool limited, const int (&limit)[R], float (&acc)[R][16]) {
+template <int R, bool kLimited>
+__device__ __forceinline__ void simt_accumulate_as(const float* p, int ldp, const float* b, int ra, int tx, int n,
+                                                   const int (&limit)[R], float (&acc)[R][16]) {
   using dense_simt::kLd;
 #pragma unroll 2
   for (int k = 0; k < n; k += 4) {
@@ -147,7 +149,7 @@ __device__ __forceinline__ void simt_accumulate(const float* p, int ldp, const f
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const float f = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
-        if (limited && k + kk >= limit[i]) continue;
+        if (kLimited && k + kk >= limit[i]) continue;
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
           float2* d = reinterpret_cast<float2*>(&acc[i][4 * jj]);
@@ -157,6 +159,15 @@ __device__ __forceinline__ void simt_accumulate(const float* p, int ldp, const f
       }
     }
   }
+}
+
+template <int R>
+__device__ __forceinline__ void simt_accumulate(const float* p, int ldp, const float* b, int ra, int tx, int n,
+                                                bool limited, const int (&limit)[R], float (&acc)[R][16]) {
+  if (limited)                                     // a copy of the loop: its comparisons are a fifth of its instructions
+    simt_accumulate_as<R, true>(p, ldp, b, ra, tx, n, limit, acc);
+  else
+    simt_accumulate_as<R, false>(p, ldp, b, ra, tx, n, limit, acc);
 }
 
 template <int ROWS, bool PAGED>
@@ -581,7 +592,7 @@ __device__ __forceinline__ void simt_dkv(const DenseTable& t, const DenseBwdArgs
       // sums over the chunk's rows of w[row][key] times the row, for this thread's
       // keys; a row before a key does not touch it
       const bool limited = j0 + kBKeys - 1 > i0;
-      auto add_rows = [&](const float* w, const float* rows, float (&g)[4][8]) {
+      auto add_rows = [&](auto is_limited, const float* w, const float* rows, float (&g)[4][8]) {
 #pragma unroll 4
         for (int r = 0; r < nrows; ++r) {
           const float4 wr = *reinterpret_cast<const float4*>(w + r * kBLd + kq);
@@ -590,7 +601,7 @@ __device__ __forceinline__ void simt_dkv(const DenseTable& t, const DenseBwdArgs
           const float4 x1 = *reinterpret_cast<const float4*>(rows + r * kLd + dl + 128);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (limited && j0 + kq + i > i0 + r) continue;
+            if (decltype(is_limited)::value && j0 + kq + i > i0 + r) continue;
             float2* d = reinterpret_cast<float2*>(g[i]);
             const float2 f = make_float2(ww[i], ww[i]);
             d[0] = fma2(f, lo2(x0), d[0]);
@@ -600,11 +611,11 @@ __device__ __forceinline__ void simt_dkv(const DenseTable& t, const DenseBwdArgs
           }
         }
       };
-      add_rows(Ps, Os, dv);
+      if (limited) add_rows(std::true_type{}, Ps, Os, dv); else add_rows(std::false_type{}, Ps, Os, dv);
       __syncthreads();
       if (c + 1 < p.c1) load_chunk(Os, a.dout, c + 1, true);
       sm100::cp_async_commit();
-      add_rows(Ds, Qs, dk);
+      if (limited) add_rows(std::true_type{}, Ds, Qs, dk); else add_rows(std::false_type{}, Ds, Qs, dk);
       __syncthreads();
       if (c + 1 < p.c1) load_chunk(Qs, a.q, c + 1, false);
       sm100::cp_async_commit();
