@@ -12,7 +12,7 @@
 // the next scores.  At two warps per scheduler FMA and shared-memory reads hardly
 // overlap, so what counts is reads per product and instructions: packed f32x2
 // products, tiles as large as the registers allow.  Measured: the training step of
-// prompts of 256, 700 and 33 tokens (24 heads, 2 groups, 24 GFLOP) 1.06 ms,
+// prompts of 256, 700 and 33 tokens (24 heads, 2 groups, 24 GFLOP) 1.04 ms,
 // the FMA pipe half busy, shared-memory reads two thirds.
 //
 // Masked places may hold anything: keys past the sequence are filled with
