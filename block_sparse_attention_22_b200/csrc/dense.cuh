@@ -161,8 +161,6 @@ template <typename T>
 __global__ void __launch_bounds__(128)
     dense_combine_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseSplits sp,
                          const float* part, T* o, float* lse, int H) {
-  pdl_wait();
-  pdl_trigger();
   const int i = blockIdx.x;
   const int u = sp.unit[i];
   const DenseUnit x = dense_unit(t, u);
@@ -173,6 +171,9 @@ __global__ void __launch_bounds__(128)
     const int slot = dense_piece_slot(t, u, c);
     return slot < 0 ? nullptr : part + ((int64_t)slot * t.prows + r) * dense::kPartFloats;
   };
+  const int64_t at = dense_q_row(t, x, x.row0 + r, H);
+  pdl_wait();                                            // so far only the launch's own tables
+  pdl_trigger();
   float m = -INFINITY;
   for (int c = sp.first[i]; c <= sp.last[i]; ++c)
     if (const float* p = piece(c)) m = fmaxf(m, p[kHeadDim]);
@@ -192,7 +193,6 @@ __global__ void __launch_bounds__(128)
     }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;     // l = 0: no key at all
-  const int64_t at = dense_q_row(t, x, x.row0 + r, H);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     o[at * kHeadDim + lane * 2 + k * 64] = IO<T>::from_f(acc[2 * k] * inv);
@@ -205,13 +205,11 @@ __global__ void __launch_bounds__(128)
 // of a long sequence: 74 of them): the pieces' statistics are read at once, the
 // warps add up every eighth piece and then join in order.
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 1)
     dense_combine_many_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseSplits sp,
                               const float* part, T* o, float* lse, int H) {
   __shared__ float w_s[dense::kMaxGrid], red[8], acc_s[8][kHeadDim];
   __shared__ int64_t at_s[dense::kMaxGrid];
-  pdl_wait();
-  pdl_trigger();
   const int u = sp.unit[blockIdx.x], c0 = sp.first[blockIdx.x], n = sp.last[blockIdx.x] - c0 + 1;
   const DenseUnit x = dense_unit(t, u);
   const int r = blockIdx.y;
@@ -231,35 +229,47 @@ __global__ void __launch_bounds__(256)
     for (int k = 1; k < 8; ++k) v = is_max ? fmaxf(v, red[k]) : v + red[k];
     return v;
   };
+  const int slot = threadIdx.x < n ? dense_piece_slot(t, u, c0 + (int)threadIdx.x) : -1;
+  const int64_t at_part = ((int64_t)slot * t.prows + r) * dense::kPartFloats;
+  if (threadIdx.x < n) at_s[threadIdx.x] = at_part;
+  const int64_t at = dense_q_row(t, x, x.row0 + r, H);
+  pdl_wait();                                            // so far only the launch's own tables
+  pdl_trigger();
   float mp = -INFINITY, lp = 0.f;
-  if (threadIdx.x < n) {
-    const int slot = dense_piece_slot(t, u, c0 + (int)threadIdx.x);
-    const int64_t at = ((int64_t)slot * t.prows + r) * dense::kPartFloats;
-    at_s[threadIdx.x] = at;
-    if (slot >= 0) {
-      mp = part[at + kHeadDim];
-      lp = part[at + kHeadDim + 1];
-    }
+  if (slot >= 0) {
+    const float2 ml = *reinterpret_cast<const float2*>(part + at_part + kHeadDim);
+    mp = ml.x;
+    lp = ml.y;
   }
   const float m = block_reduce(mp, true);
   const float w = mp == -INFINITY ? 0.f : exp2f(mp - m);
   if (threadIdx.x < n) w_s[threadIdx.x] = w;
   const float l = block_reduce(w * lp, false);          // its barriers also order w_s, at_s
   float acc[8] = {};
-#pragma unroll 4
-  for (int k = warp; k < n; k += 8) {
-    const float f = w_s[k];
-    if (f == 0.f) continue;
-    const float4* p = reinterpret_cast<const float4*>(part + at_s[k]);
-    const float4 v0 = p[lane], v1 = p[lane + 32];
-    acc[0] = fmaf(f, v0.x, acc[0]);
-    acc[1] = fmaf(f, v0.y, acc[1]);
-    acc[2] = fmaf(f, v0.z, acc[2]);
-    acc[3] = fmaf(f, v0.w, acc[3]);
-    acc[4] = fmaf(f, v1.x, acc[4]);
-    acc[5] = fmaf(f, v1.y, acc[5]);
-    acc[6] = fmaf(f, v1.z, acc[6]);
-    acc[7] = fmaf(f, v1.w, acc[7]);
+  constexpr int kBatch = 5;                              // pieces in flight: 74 of a long row are two batches
+  for (int k0 = warp; k0 < n; k0 += 8 * kBatch) {
+    float f[kBatch];
+    float4 v[kBatch][2];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int k = k0 + 8 * b;
+      f[b] = k < n ? w_s[k] : 0.f;
+      v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (f[b] != 0.f) {
+        const float4* p = reinterpret_cast<const float4*>(part + at_s[k]);
+        v[b][0] = p[lane];
+        v[b][1] = p[lane + 32];
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        acc[4 * h] = fmaf(f[b], v[b][h].x, acc[4 * h]);
+        acc[4 * h + 1] = fmaf(f[b], v[b][h].y, acc[4 * h + 1]);
+        acc[4 * h + 2] = fmaf(f[b], v[b][h].z, acc[4 * h + 2]);
+        acc[4 * h + 3] = fmaf(f[b], v[b][h].w, acc[4 * h + 3]);
+      }
   }
   reinterpret_cast<float4*>(acc_s[warp])[lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
   reinterpret_cast<float4*>(acc_s[warp])[lane + 32] = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -267,7 +277,6 @@ __global__ void __launch_bounds__(256)
   float v = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) v += acc_s[k][threadIdx.x];
-  const int64_t at = dense_q_row(t, x, x.row0 + r, H);
   o[at * kHeadDim + threadIdx.x] = IO<T>::from_f(l != 0.f ? v / l : 0.f);      // l = 0: no key at all
   if (lse && threadIdx.x == 0) lse[at] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
