@@ -15,8 +15,8 @@
 // through shared memory.  P is rounded to bf16 for its product, the row sum
 // adds the unrounded values.  Tables, pieces and their join: dense.cuh, rows =
 // 16 and a chunk of 128 keys, 16 for each warp.  Measured: 32 sequences of 16K to
-// 50K keys (2.1 GB) 349 us with the join, 0.95 of the HBM rate; one row at 256K 100
-// us, 0.83.
+// 50K keys (2.1 GB) 349 us with the join, 0.95 of the HBM rate; one row at 256K 96
+// us, 0.87.
 //
 // A token's keys are all visible to it, so nothing is masked but keys beyond
 // the sequence and of pages out of range: neither is read (zeros are filled
@@ -57,36 +57,55 @@ __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], const uint32_t (&a)[
 }
 
 // Joins the warps' maxima, sums and O (in shared memory, a warp's over its slots)
-// of a piece: a whole unit's result, or the piece's partial one.  Thread d has
-// dim d.
+// of a piece: a whole unit's result, or the piece's partial one.  Eight lanes
+// make a row's factors first, in place of the maxima; then a thread joins four
+// dims of every fourth row.
 template <typename T>
 __device__ __forceinline__ void decode_join(const DenseUnit& x, const DensePiece& p, int prows, int64_t head0,
-                                            const unsigned char* smem, const float* m_s, const float* l_s, T* o,
-                                            float* lse, float* part) {
+                                            const unsigned char* smem, float* m_s, float* l_s, T* o, float* lse,
+                                            float* part) {
   using namespace dense_decode;
-  const int d = threadIdx.x;
-  for (int r = 0; r < x.nrows; ++r) {
-    float mr = -INFINITY;
+  static_assert(kWarps == 8 && kRows * kWarps <= kThreads && kThreads == kHeadDim, "thread layouts below");
+  float* const dst = part + (int64_t)p.part * prows * dense::kPartFloats;      // used by a cut unit's piece only
+  if (threadIdx.x < kRows * kWarps) {
+    const int r = threadIdx.x >> 3, at = (threadIdx.x & 7) * kRows + r;
+    const float m = m_s[at];
+    float mr = m, l;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, m_s[w * kRows + r]);
-    float lr = 0.f, v = 0.f;
+    for (int off = 4; off; off >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, off));
+    const float f = m == -INFINITY ? 0.f : exp2f(m - mr);
+    l = f * l_s[at];
+#pragma unroll
+    for (int off = 4; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    m_s[at] = f;
+    if ((threadIdx.x & 7) == 0) {
+      l_s[at] = l;
+      if (r < x.nrows && p.part >= 0)
+        *reinterpret_cast<float2*>(dst + r * dense::kPartFloats + kHeadDim) = make_float2(mr, l);
+      else if (r < x.nrows && lse)
+        lse[head0 + r] = l != 0.f ? (mr + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
+  }
+  __syncthreads();
+  const int d = (threadIdx.x & 63) * 4;
+#pragma unroll 2
+  for (int r = threadIdx.x >> 6; r < x.nrows; r += 4) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float mw = m_s[w * kRows + r];
-      const float f = mw == -INFINITY ? 0.f : exp2f(mw - mr);
-      lr = fmaf(f, l_s[w * kRows + r], lr);
-      v = fmaf(f, reinterpret_cast<const float*>(smem + w * kSlots * kSlotBytes)[r * kOLd + d], v);
+      const float f = m_s[w * kRows + r];
+      const float4 y =
+          *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * kSlots * kSlotBytes) + r * kOLd + d);
+      v.x = fmaf(f, y.x, v.x);
+      v.y = fmaf(f, y.y, v.y);
+      v.z = fmaf(f, y.z, v.z);
+      v.w = fmaf(f, y.w, v.w);
     }
-    if (p.part < 0) {
-      o[(head0 + r) * kHeadDim + d] = IO<T>::from_f(lr != 0.f ? v / lr : 0.f);
-      if (d == 0 && lse) lse[head0 + r] = lr != 0.f ? (mr + log2f(lr)) * 0.6931471805599453f : -INFINITY;
+    if (p.part >= 0) {
+      *reinterpret_cast<float4*>(dst + r * dense::kPartFloats + d) = v;
     } else {
-      float* dst = part + ((int64_t)p.part * prows + r) * dense::kPartFloats;
-      dst[d] = v;
-      if (d == 0) {
-        dst[kHeadDim] = mr;
-        dst[kHeadDim + 1] = lr;
-      }
+      const float l = l_s[r], inv = l != 0.f ? 1.f / l : 0.f;
+      simt_store4(o + (head0 + r) * kHeadDim + d, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     }
   }
 }
@@ -113,12 +132,10 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
   DenseUnit x;
   while (walk.next(t, p, x)) {
     const int64_t head0 = (int64_t)t.q_offset[x.si] * a.H + x.grp * t.hpg;
-    // Q, rows beyond the group's heads zero
+    // Q, rows beyond the group's heads zero; it arrives with the first tile's K
     for (int i = threadIdx.x; i < kRows * 32; i += kThreads) {
       const int r = i >> 5, c = i & 31;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < x.nrows) v = *reinterpret_cast<const uint4*>(a.q + (head0 + r) * kHeadDim + c * 8);
-      *reinterpret_cast<uint4*>(smem + kOffQ + at(r, c)) = v;
+      cp_async16(q_addr + at(r, c), a.q + (head0 + (r < x.nrows ? r : 0)) * kHeadDim + c * 8, r < x.nrows ? 16u : 0u);
     }
     // this warp's tiles: keys (p.c0 + i) * 128 + 16 warp, of those that hold a key
     const int32_t key0 = p.c0 * kKeys + warp * kTile;
@@ -172,6 +189,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
     load(1);
     int64_t row_now = row_k;
     load(2);
+    cp_async_wait<2>();
     __syncthreads();                                      // Q written
     for (int i = 0; i < n; ++i) {
       // ---- S of tile i
@@ -288,8 +306,8 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
 // for 32 products), and the 4 x HP sums over the lanes are reduced together, halving
 // their number with each exchange.  Lane h then does head h's softmax.  HP: heads,
 // rounded up to 4.  Bound by the instructions per key, not HBM, from 12 heads on:
-// 24 heads in two groups, 16 sequences of 8000 keys 120 us (0.68 of the HBM rate),
-// 8 of 2000 keys 28 us; 8 heads in 8 groups reach 0.93.
+// 24 heads in two groups, 16 sequences of 8000 keys 112 us (0.72 of the HBM rate),
+// 8 of 2000 keys 24 us; 8 heads in 8 groups reach 0.92.
 namespace dense_decode {
 constexpr int kStep = 4;                              // keys
 constexpr int kF32Slots = 6, kF32SlotBytes = kStep * kHeadDim * 4;
@@ -360,9 +378,8 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
   while (walk.next(t, p, x)) {
     const int64_t head0 = (int64_t)t.q_offset[x.si] * a.H + x.grp * t.hpg;
     for (int i = threadIdx.x; i < kRows * (kHeadDim / 4); i += kThreads) {     // rows beyond the heads zero
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i / (kHeadDim / 4) < x.nrows) v = reinterpret_cast<const float4*>(a.q + head0 * kHeadDim)[i];
-      reinterpret_cast<float4*>(q_s)[i] = v;
+      const bool in = i / (kHeadDim / 4) < x.nrows;
+      cp_async16(smem_u32(q_s) + i * 16, a.q + head0 * kHeadDim + (in ? i * 4 : 0), in ? 16u : 0u);
     }
     // this warp's keys: 16 of each chunk, in steps of 4 (step j: chunk j / 4)
     const int32_t key0 = p.c0 * kKeys + warp * kTile;
@@ -418,6 +435,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
     int64_t rows_ahead[3];                                // of the steps in flight, oldest first
 #pragma unroll
     for (int j = 0; j < 3; ++j) rows_ahead[j] = load(j);
+    cp_async_wait<5>();
     __syncthreads();                                      // q written
     for (int j = 0; j < n; ++j) {
       const bool bad = rows_ahead[0] < 0;
