@@ -156,7 +156,16 @@ __device__ __forceinline__ int dense_piece_slot(const DenseTable& t, int u, int 
 // Joins the pieces of each cut unit: with m the largest of the pieces' maxima
 // (log2 units), l = sum l_p 2^(m_p - m), o = sum o_p 2^(m_p - m) / l.  A piece
 // without a key of a row has m_p = -inf and counts nothing.  One warp per row,
-// 8 dims per lane; pieces are added in the order of their keys.
+// 8 dims per lane, for units in kFewPieces or fewer, all read at once; pieces are
+// added in the order of their keys.
+constexpr int kFewPieces = 4;
+__device__ __forceinline__ void store4(float* dst, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* dst, float a, float b, float c, float d) {
+  __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<uint32_t*>(&x), *reinterpret_cast<uint32_t*>(&y));
+}
 template <typename T>
 __global__ void __launch_bounds__(128)
     dense_combine_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseSplits sp,
@@ -167,38 +176,47 @@ __global__ void __launch_bounds__(128)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = blockIdx.y * 4 + warp;
   if (r >= x.nrows) return;
-  auto piece = [&](int c) -> const float* {      // null: CTA c has no piece of the unit
-    const int slot = dense_piece_slot(t, u, c);
-    return slot < 0 ? nullptr : part + ((int64_t)slot * t.prows + r) * dense::kPartFloats;
-  };
-  const int64_t at = dense_q_row(t, x, x.row0 + r, H);
-  pdl_wait();                                            // so far only the launch's own tables
-  pdl_trigger();
-  float m = -INFINITY;
-  for (int c = sp.first[i]; c <= sp.last[i]; ++c)
-    if (const float* p = piece(c)) m = fmaxf(m, p[kHeadDim]);
-  float l = 0.f, acc[8] = {};
-  for (int c = sp.first[i]; c <= sp.last[i]; ++c) {
-    const float* p = piece(c);
-    if (!p) continue;
-    const float mp = p[kHeadDim];
-    if (mp == -INFINITY) continue;
-    const float w = exp2f(mp - m);
-    l += w * p[kHeadDim + 1];
+  const int64_t at = dense_q_row(t, x, x.row0 + r, H) * kHeadDim + lane * 4;
+  const float* p[kFewPieces];                      // null: no such piece
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = *reinterpret_cast<const float2*>(p + lane * 2 + k * 64);
-      acc[2 * k] += w * f.x;
-      acc[2 * k + 1] += w * f.y;
+  for (int k = 0; k < kFewPieces; ++k) {
+    const int c = sp.first[i] + k, slot = c <= sp.last[i] ? dense_piece_slot(t, u, c) : -1;
+    p[k] = slot < 0 ? nullptr : part + ((int64_t)slot * t.prows + r) * dense::kPartFloats;
+  }
+  pdl_wait();                                      // so far only the launch's own tables
+  pdl_trigger();
+  float2 ml[kFewPieces];
+  float4 v[kFewPieces][2];
+#pragma unroll
+  for (int k = 0; k < kFewPieces; ++k) {
+    ml[k] = make_float2(-INFINITY, 0.f);
+    if (p[k]) {
+      ml[k] = *reinterpret_cast<const float2*>(p[k] + kHeadDim);
+      v[k][0] = reinterpret_cast<const float4*>(p[k])[lane];
+      v[k][1] = reinterpret_cast<const float4*>(p[k])[lane + 32];
+    }
+  }
+  float m = -INFINITY, l = 0.f, acc[8] = {};
+#pragma unroll
+  for (int k = 0; k < kFewPieces; ++k) m = fmaxf(m, ml[k].x);
+#pragma unroll
+  for (int k = 0; k < kFewPieces; ++k) {
+    if (ml[k].x == -INFINITY) continue;
+    const float w = exp2f(ml[k].x - m);
+    l += w * ml[k].y;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      acc[4 * h] += w * v[k][h].x;
+      acc[4 * h + 1] += w * v[k][h].y;
+      acc[4 * h + 2] += w * v[k][h].z;
+      acc[4 * h + 3] += w * v[k][h].w;
     }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;     // l = 0: no key at all
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    o[at * kHeadDim + lane * 2 + k * 64] = IO<T>::from_f(acc[2 * k] * inv);
-    o[at * kHeadDim + lane * 2 + k * 64 + 1] = IO<T>::from_f(acc[2 * k + 1] * inv);
-  }
-  if (lse && lane == 0) lse[at] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  for (int h = 0; h < 2; ++h)
+    store4(o + at + 128 * h, acc[4 * h] * inv, acc[4 * h + 1] * inv, acc[4 * h + 2] * inv, acc[4 * h + 3] * inv);
+  if (lse && lane == 0) lse[at / kHeadDim] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // The same by a block of eight warps per row, for units in many pieces (decode

@@ -356,7 +356,7 @@ cudaError_t launch_dense_combine(const Geo& g, const DenseTable& t, const DenseS
   count_launch();
   int most = 0;
   for (int i = 0; i < sp.n; ++i) most = std::max(most, sp.last[i] - sp.first[i] + 1);
-  if (most > 4)                          // a warp per row adds four pieces in the time of a barrier or two
+  if (most > kFewPieces)                 // a warp per row adds four pieces in the time of a barrier or two
     return launch_chained(dense_combine_many_kernel<T>, dim3(sp.n, (unsigned)t.prows), dim3(256), 0, st, t, sp, part,
                           (T*)o, lse, g.H);
   return launch_chained(dense_combine_kernel<T>, dim3(sp.n, (unsigned)cdiv(t.prows, 4)), dim3(128), 0, st, t, sp,

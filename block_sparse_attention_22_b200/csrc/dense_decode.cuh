@@ -105,7 +105,7 @@ __device__ __forceinline__ void decode_join(const DenseUnit& x, const DensePiece
       *reinterpret_cast<float4*>(dst + r * dense::kPartFloats + d) = v;
     } else {
       const float l = l_s[r], inv = l != 0.f ? 1.f / l : 0.f;
-      simt_store4(o + (head0 + r) * kHeadDim + d, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+      store4(o + (head0 + r) * kHeadDim + d, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     }
   }
 }

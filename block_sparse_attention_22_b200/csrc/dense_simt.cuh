@@ -78,14 +78,6 @@ __device__ __forceinline__ void simt_load_rows(float* dst, int rows, const T* an
   }
 }
 
-__device__ __forceinline__ void simt_store4(float* dst, float a, float b, float c, float d) {
-  *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
-}
-__device__ __forceinline__ void simt_store4(__nv_bfloat16* dst, float a, float b, float c, float d) {
-  __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
-  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<uint32_t*>(&x), *reinterpret_cast<uint32_t*>(&y));
-}
-
 // Two fp32 products and sums in one instruction: the FMA pipe's rate is the
 // same, but at two warps per scheduler its issue slots are what runs short.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -274,7 +266,7 @@ __global__ void __launch_bounds__(dense_simt::kThreads, 1)
         const int64_t at = q_at(ra + i);
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
-          simt_store4(o + at * kHeadDim + 4 * tx + 64 * jj, acc[i][4 * jj] * inv, acc[i][4 * jj + 1] * inv,
+          store4(o + at * kHeadDim + 4 * tx + 64 * jj, acc[i][4 * jj] * inv, acc[i][4 * jj + 1] * inv,
                       acc[i][4 * jj + 2] * inv, acc[i][4 * jj + 3] * inv);
         if (lse && tx == 0) lse[at] = l[i] != 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
       } else {
@@ -506,13 +498,13 @@ __device__ __forceinline__ void simt_dq(const DenseTable& t, const DenseBwdArgs&
         T* dst = (T*)a.dq + q_at(ra + i) * kHeadDim;
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
-          simt_store4(dst + 4 * tx + 64 * jj, acc[i][4 * jj] * a.scale, acc[i][4 * jj + 1] * a.scale,
+          store4(dst + 4 * tx + 64 * jj, acc[i][4 * jj] * a.scale, acc[i][4 * jj + 1] * a.scale,
                       acc[i][4 * jj + 2] * a.scale, acc[i][4 * jj + 3] * a.scale);
       } else {
         float* dst = part + ((int64_t)p.part * t.prows + ra + i) * dense::kPartFloats;
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
-          simt_store4(dst + 4 * tx + 64 * jj, acc[i][4 * jj], acc[i][4 * jj + 1], acc[i][4 * jj + 2],
+          store4(dst + 4 * tx + 64 * jj, acc[i][4 * jj], acc[i][4 * jj + 1], acc[i][4 * jj + 2],
                       acc[i][4 * jj + 3]);
       }
     }
@@ -629,12 +621,12 @@ __device__ __forceinline__ void simt_dkv(const DenseTable& t, const DenseBwdArgs
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (p.part < 0) {
-          simt_store4((T*)a.dk + at + 128 * h, dk[i][4 * h] * a.scale, dk[i][4 * h + 1] * a.scale,
+          store4((T*)a.dk + at + 128 * h, dk[i][4 * h] * a.scale, dk[i][4 * h + 1] * a.scale,
                       dk[i][4 * h + 2] * a.scale, dk[i][4 * h + 3] * a.scale);
-          simt_store4((T*)a.dv + at + 128 * h, dv[i][4 * h], dv[i][4 * h + 1], dv[i][4 * h + 2], dv[i][4 * h + 3]);
+          store4((T*)a.dv + at + 128 * h, dv[i][4 * h], dv[i][4 * h + 1], dv[i][4 * h + 2], dv[i][4 * h + 3]);
         } else {
-          simt_store4(pk + 128 * h, dk[i][4 * h], dk[i][4 * h + 1], dk[i][4 * h + 2], dk[i][4 * h + 3]);
-          simt_store4(pv + 128 * h, dv[i][4 * h], dv[i][4 * h + 1], dv[i][4 * h + 2], dv[i][4 * h + 3]);
+          store4(pk + 128 * h, dk[i][4 * h], dk[i][4 * h + 1], dk[i][4 * h + 2], dk[i][4 * h + 3]);
+          store4(pv + 128 * h, dv[i][4 * h], dv[i][4 * h + 1], dv[i][4 * h + 2], dv[i][4 * h + 3]);
         }
       }
     }
@@ -691,8 +683,6 @@ __global__ void __launch_bounds__(128)
     dense_bwd_combine_kernel(const __grid_constant__ DenseTable rows, const __grid_constant__ DenseSplits srows,
                              const __grid_constant__ DenseTable keys, const __grid_constant__ DenseSplits skeys,
                              const __grid_constant__ DenseBwdJoins<T> joins) {
-  pdl_wait();
-  pdl_trigger();
   const DenseBwdJoin<T>& w = joins.join[blockIdx.z];
   const DenseTable& t = w.keys ? keys : rows;
   const DenseSplits& sp = w.keys ? skeys : srows;
@@ -701,7 +691,10 @@ __global__ void __launch_bounds__(128)
   const int u = sp.unit[i];
   const DenseUnit x = dense_unit(t, u);
   const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (r >= x.nrows || (joins.flags && segment_flagged(joins.flags, t.slot[x.si], t.q_len[x.si]))) return;
+  if (r >= x.nrows) return;
+  pdl_wait();                                      // so far only the launch's own tables
+  pdl_trigger();
+  if (joins.flags && segment_flagged(joins.flags, t.slot[x.si], t.q_len[x.si])) return;
   float acc[8] = {};
   for (int c0 = sp.first[i]; c0 <= sp.last[i]; c0 += 32) {
     const int my = c0 + lane <= sp.last[i] ? dense_piece_slot(t, u, c0 + lane) : -1;
