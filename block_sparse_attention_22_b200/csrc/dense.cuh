@@ -155,7 +155,8 @@ __device__ __forceinline__ int dense_piece_slot(const DenseTable& t, int u, int 
 
 // Joins the pieces of each cut unit: with m the largest of the pieces' maxima
 // (log2 units), l = sum l_p 2^(m_p - m), o = sum o_p 2^(m_p - m) / l.  A piece
-// without a key of a row has m_p = -inf and counts nothing.  One warp per row,
+// without a key of a row has m_p = -inf and l_p = 0 and counts nothing (scores that
+// are all NaN: m_p = -inf, l_p = NaN).  One warp per row,
 // 8 dims per lane, for units in kFewPieces or fewer, all read at once; pieces are
 // added in the order of their keys.
 constexpr int kFewPieces = 4;
@@ -201,9 +202,9 @@ __global__ void __launch_bounds__(128)
   for (int k = 0; k < kFewPieces; ++k) m = fmaxf(m, ml[k].x);
 #pragma unroll
   for (int k = 0; k < kFewPieces; ++k) {
-    if (ml[k].x == -INFINITY) continue;
-    const float w = exp2f(ml[k].x - m);
-    l += w * ml[k].y;
+    const float w = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - m);
+    l += w * ml[k].y;                              // NaN if the piece's scores are all NaN
+    if (w == 0.f) continue;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       acc[4 * h] += w * v[k][h].x;

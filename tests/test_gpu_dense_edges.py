@@ -119,6 +119,29 @@ def test_decode_with_rising_scores_rescales():
     _check(x, o, lse)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("seqs", [[(2000, 1)] * 8, [(900, 1)] * 60, [(4000, 5)] * 3, [(1500, 300), (40, 70)]],
+                         ids=["many pieces", "few pieces", "short", "chunks"])
+def test_queries_and_keys_that_are_nan_show_in_their_rows_alone(seqs, dtype):
+    """A row whose every score is NaN has no maximum in any piece, one with a NaN
+    score among others has one: NaN by the formula both, whole or cut."""
+    x = _cache(24, 2, 64, seqs, dtype=dtype)
+    clean, clean_lse = _attend(x)
+    last = [off + n - 1 for (c, n), off in zip(seqs, x["offs"])]
+    hit = torch.zeros(clean_lse.shape, dtype=torch.bool, device="cuda")
+    for i, (row, h) in enumerate(zip(last, [0, 5, 11, 12, 23] * len(seqs))):
+        x["q"][row, h, (37 * i) % D] = NAN
+        hit[row, h] = True
+    c, n = seqs[-1]
+    page = x["table"][len(seqs) - 1, c // 64]              # key c, of the first of these queries: all attend it
+    x["kp"][page, 1, c % 64, 200] = NAN
+    hit[x["offs"][-1]:, 12:] = True
+    o, lse = _attend(x)
+    assert torch.equal(torch.isnan(lse), hit)
+    assert bool(torch.isnan(o[hit]).all())
+    assert torch.equal(o[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
 def test_decode_skips_bad_pages_inside_a_sequence():
     x = _cache(24, 2, 16, [(400, 1), (300, 1), (20, 1)], seed=4)
     t = x["table"].clone()
