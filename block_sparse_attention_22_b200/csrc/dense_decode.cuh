@@ -15,7 +15,7 @@
 // through shared memory.  P is rounded to bf16 for its product, the row sum
 // adds the unrounded values.  Tables, pieces and their join: dense.cuh, rows =
 // 16 and a chunk of 128 keys, 16 for each warp.  Measured: 32 sequences of 16K to
-// 50K keys (2.1 GB) 349 us with the join, 0.95 of the HBM rate; one row at 256K 96
+// 50K keys (2.1 GB) 342 us with the join, 0.97 of the HBM rate; one row at 256K 95
 // us, 0.87.
 //
 // A token's keys are all visible to it, so nothing is masked but keys beyond
