@@ -69,7 +69,7 @@ constexpr int kOffCtl = kOffQ + kQBytes;              // 196608
 constexpr int kCtlBytes = 3072;
 constexpr int kSmemBytes = kOffCtl + kCtlBytes;       // 199680: the base itself is 1024-byte aligned
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
-constexpr int kNfBufs = 4;                            // units whose non-finite lists may be in use at once
+constexpr int kNfBufs = 4;                            // units whose non-finite lists may be in use at once, or made ahead
 template <int CG> struct Shape {
   static constexpr int kRows = 128 * CG;
   static constexpr int kKeys = 64 * CG;
@@ -97,7 +97,7 @@ struct DenseTcCtl {
   uint64_t q_full, q_empty;
   uint64_t s_done[2], p_full[2], pv_done[2];          // by chunk parity
   uint64_t o_full, o_free;
-  uint64_t nf_full[dense_tc::kNfBufs];
+  uint64_t nf_full[dense_tc::kNfBufs], nf_free[dense_tc::kNfBufs];
   uint64_t mma_done;
   float red[2][2][128];                   // by chunk parity: row maxima / sums of the two warps of a row
   uint32_t nf[dense_tc::kNfBufs][8];   // keys first_pos+1+i whose V is not finite
@@ -244,7 +244,10 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       mbar_init(&ctl.p_full[i], kSoftmaxWarps * CG);
       mbar_init(&ctl.pv_done[i], 1);
     }
-    for (int i = 0; i < kNfBufs; ++i) mbar_init(&ctl.nf_full[i], 1);
+    for (int i = 0; i < kNfBufs; ++i) {
+      mbar_init(&ctl.nf_full[i], 1);
+      mbar_init(&ctl.nf_free[i], kSoftmaxWarps);
+    }
     mbar_init(&ctl.q_full, CG);
     mbar_init(&ctl.q_empty, 1);
     mbar_init(&ctl.o_full, 1);
@@ -399,11 +402,14 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
     int64_t uc = 0;
     while (walk.next(t, p, x)) {
       if (warp_aborted(abort_flag)) break;
-      // not further ahead than Q: the lists of the units before are then no longer read
-      if (!warp_wait_sleep(&ctl.q_empty, (uint32_t)((uc & 1) ^ 1), abort_flag)) break;
-      // keys that only some rows see (at most 255), 32 at a time
+      // A list is free once every softmax warp has taken the one kNfBufs units before.
+      // Those warps take each unit's, so neither side can be two phases behind the
+      // other and mistake one for the next by its parity (paced by q_empty, which
+      // nothing held back for this warp, that was possible in units of a chunk or two).
+      if (!warp_wait_sleep(&ctl.nf_free[uc % kNfBufs], (uint32_t)((uc / kNfBufs & 1) ^ 1), abort_flag)) break;
+      // keys that only some rows see (at most 255), 32 at a time; none in a piece that ends before them
       const int32_t first = t.pos0[x.si] + x.row0 / t.hpg;   // position of the unit's first row
-      const int own = x.kv_len - 1 - first;
+      const int own = p.c1 * KC - 1 > first ? x.kv_len - 1 - first : 0;
       uint32_t word = 0;
       for (int i0 = 0; i0 < own; i0 += 32) {
         const int64_t my_off = i0 + lane < own ? kv_row<PAGED>(a.kv, t, x.si, x.grp, first + 1 + i0 + lane) : -1;
@@ -448,9 +454,17 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       const int32_t first = t.pos0[x.si] + x.row0 / t.hpg;               // of the unit
       const int32_t first_cta = t.pos0[x.si] + (x.row0 + (int)rank * 128) / t.hpg;
       const int32_t kv_len = x.kv_len;
-      // the unit's list of values that are not finite, taken before its first own key
+      // the unit's list of values that are not finite, taken before its first own key,
+      // or at the end of a piece without one (empty then)
       bool nf_taken = false, any_nf = false;
       uint32_t my_nf = 0;
+      auto take_nf = [&]() {
+        nf_taken = true;
+        mbar_wait_fast(&ctl.nf_full[uc % kNfBufs], (uint32_t)((uc / kNfBufs) & 1), abort_flag);
+        my_nf = lane < 8 ? ctl.nf[uc % kNfBufs][lane] : 0u;
+        any_nf = __any_sync(0xffffffffu, my_nf != 0);
+        if (lane == 0) mbar_arrive(&ctl.nf_free[uc % kNfBufs]);
+      };
       // the page of run `lane` of 16 keys of a chunk; 0 where nothing is looked up
       auto page_of_run = [&](int c) -> int32_t {
         const int32_t key = c * KC + lane * 16;
@@ -466,12 +480,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
         const uint32_t bad =
             PAGED ? __ballot_sync(0xffffffffu, next_page < 0 || next_page >= a.kv.n_pages) : 0u;
         next_page = page_of_run(p.c0 + c + 1);
-        if (!nf_taken && j0 + KC - 1 > first) {
-          nf_taken = true;
-          mbar_wait_fast(&ctl.nf_full[uc % kNfBufs], (uint32_t)((uc / kNfBufs) & 1), abort_flag);
-          my_nf = lane < 8 ? ctl.nf[uc % kNfBufs][lane] : 0u;
-          any_nf = __any_sync(0xffffffffu, my_nf != 0);
-        }
+        if (!nf_taken && j0 + KC - 1 > first) take_nf();
         mbar_wait_fast(&ctl.s_done[b], (uint32_t)((gc >> 1) & 1), abort_flag);
         tc_fence_after();
         const bool clear = j0 + KC > kv_len || bad || (any_nf && j0 + KC - 1 > first);
@@ -568,6 +577,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
           if (clear) dense_arrive<CG>(&ctl.p_full[b]); else mbar_arrive_leader<CG>(&ctl.p_full[b]);
         }
       }
+      if (!nf_taken) take_nf();
       float lt = 0.f;
       if (warp_active) {                                     // the row's sum: both warps' parts
         ctl.red[gc & 1][half][li] = l;                       // the last chunk's buffer is the other one
