@@ -294,7 +294,10 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     // ============================================================ MMA issuer
     int64_t gc = 0, uc = 0;                          // chunks and pieces so far
     const uint32_t sb = smem_u32(smem), leader = elect_one();
-    auto wait = [&](uint64_t* bar, int64_t phase) { return warp_wait_fast(bar, (uint32_t)(phase & 1), abort_flag); };
+    // what both CTAs' threads arrive on
+    auto wait = [&](uint64_t* bar, int64_t phase) {
+      return warp_wait_fast<true>(bar, (uint32_t)(phase & 1), abort_flag);
+    };
     // S (kind 0) or dP (kind 1) of the piece's chunk c
     auto scores = [&](int kind, int c, int n) -> bool {
       const int64_t xg = gc + c;
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (clear) mbar_arrive_cluster(&ctl.w_full[b], 0); else mbar_arrive_leader<2>(&ctl.w_full[b]);
+          mbar_arrive_leader<2>(&ctl.w_full[b]);
           if (kByKeys) mbar_arrive(&ctl.st_free[sbuf]);
         }
         if (!kByKeys || --left == 0) {

@@ -114,12 +114,6 @@ inline int dense_box(int page_tokens) {
   return b;
 }
 
-// Arrives on rank 0's barrier after shared-memory writes that its MMAs read.
-template <int CG>
-__device__ __forceinline__ void dense_arrive(uint64_t* bar) {
-  if constexpr (CG == 1) sm100::mbar_arrive(bar); else sm100::mbar_arrive_cluster(bar, 0);
-}
-
 // Loads rows row0 .. row0+n-1 (n <= 128) of a unit's segment and group into a
 // 128-byte swizzled tile, completing n * 512 bytes on rank 0's barrier: a token's
 // heads are consecutive rows of the token-major array, so a whole token is one
@@ -203,8 +197,9 @@ __device__ __forceinline__ void store_cols32(const float (&o)[32], float f, __nv
 }
 
 // mbar_wait_fast by a whole warp, with one answer.
+template <bool kPair = false>
 __device__ __forceinline__ bool warp_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, sm100::mbar_wait_fast(bar, parity, abort_flag));
+  return __all_sync(0xffffffffu, sm100::mbar_wait_fast<kPair>(bar, parity, abort_flag));
 }
 
 // After an abort: copies in flight land within microseconds; the CTA stays for
@@ -335,7 +330,10 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
     // ============================================================ MMA issuer
     int64_t gc = 0, uc = 0;                                  // chunks and pieces so far
     const uint32_t sb = smem_u32(smem), leader = elect_one();
-    auto wait = [&](uint64_t* bar, int64_t phase) { return mbar_wait_fast(bar, (uint32_t)(phase & 1), abort_flag); };
+    // what both CTAs' threads arrive on
+    auto wait = [&](uint64_t* bar, int64_t phase) {
+      return mbar_wait_fast<CG == 2>(bar, (uint32_t)(phase & 1), abort_flag);
+    };
     auto pv = [&](int cx, int n) -> bool {
       const int64_t xg = gc + cx;
       const int b = (int)(xg & 1);
@@ -573,9 +571,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
         mbar_wait_fast(&ctl.v_full[gc % kVSlots], (uint32_t)((gc / kVSlots) & 1), abort_flag);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (clear) dense_arrive<CG>(&ctl.p_full[b]); else mbar_arrive_leader<CG>(&ctl.p_full[b]);
-        }
+        if (lane == 0) mbar_arrive_leader<CG>(&ctl.p_full[b]);
       }
       if (!nf_taken) take_nf();
       float lt = 0.f;

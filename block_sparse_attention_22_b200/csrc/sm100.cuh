@@ -44,15 +44,27 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
                : "memory");
 }
 
+// kPair: acquires at cluster scope, for barriers that threads of the pair's other
+// CTA arrive on (the default form acquires from this CTA's threads alone).
+template <bool kPair = false>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
   return ok != 0;
 }
 
@@ -82,22 +94,33 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 // `kSleepHintNs` until the phase completes, so waiting costs no issue slots.
 constexpr uint32_t kSleepHintNs = 1000000;
 
+template <bool kPair = false>
 __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(kSleepHintNs)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSleepHintNs)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSleepHintNs)
+        : "memory");
   return ok != 0;
 }
 
+template <bool kPair = false>
 __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const long long t0 = clock64();
   while (true) {
-    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (mbar_try_wait_sleep<kPair>(bar, parity)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > kWaitLimitCycles) {
       report_error(kErrWaitTimeout);
@@ -108,9 +131,10 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, 
 }
 
 // mbar_wait_sleep that takes a completed phase without reading the clock.
+template <bool kPair = false>
 __device__ __forceinline__ bool mbar_wait_fast(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_sleep(bar, parity, abort_flag);
+  if (mbar_try_wait<kPair>(bar, parity)) return true;
+  return mbar_wait_sleep<kPair>(bar, parity, abort_flag);
 }
 
 // ------------------------------------------------------------------ TMA
@@ -283,18 +307,16 @@ __device__ __forceinline__ void mbar_expect_tx_leader(uint64_t* bar, uint32_t by
   if constexpr (CG == 1)
     mbar_expect_tx(bar, bytes);
   else
-    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(leader_bar<2>(bar)), "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(leader_bar<2>(bar)),
+                 "r"(bytes)
                  : "memory");
 }
-// Arrives on rank 0's barrier; orders this CTA's accesses and (after
-// tcgen05.fence::before_thread_sync) tensor memory, not shared memory that the
-// other CTA reads itself: those writers use mbar_arrive_cluster.
+// Arrives on rank 0's barrier, releasing to its waiters (mbar_try_wait<true>)
+// this CTA's shared memory, which rank 0's MMAs read, and (after
+// tcgen05.fence::before_thread_sync) its tensor memory.
 template <int CG>
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
-  if constexpr (CG == 1)
-    mbar_arrive(bar);
-  else
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_bar<2>(bar)) : "memory");
+  if constexpr (CG == 1) mbar_arrive(bar); else mbar_arrive_cluster(bar, 0);
 }
 // 2-D tiled load into this CTA that completes on rank 0's barrier.
 template <int CG>
@@ -308,11 +330,6 @@ __device__ __forceinline__ void tma_load_2d_leader(void* dst, const CUtensorMap*
         " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_bar<2>(bar)), "r"(x), "r"(y)
         : "memory");
-}
-// Orders what this thread does next after what another CTA released before its
-// arrival on a barrier this thread has seen complete.
-__device__ __forceinline__ void fence_acquire_cluster() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 // Forms of the tcgen05 operations for one CTA (CG = 1) and a pair (CG = 2).

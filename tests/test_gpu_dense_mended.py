@@ -99,3 +99,31 @@ def test_cut_chunks_without_own_keys_next_to_short_units(heads, groups):
     for (off, n, c, i), (k, v) in zip(segs, kv):
         t = slice(off, off + n)
         check_forward(o[t], lse[t], attend64(q[t], k, v, c, SCALE), score_error(q[t], k, SCALE), BF, i)
+
+
+# ------------------------------------------------------------------ shared memory of a pair's other CTA
+def test_rows_zeroed_by_either_cta_of_a_pair_are_zero_in_the_product():
+    """Every prompt ends inside a chunk and is followed by NaN rows, which the
+    softmax warps of both CTAs zero in their own halves of the operands before
+    the leader's products read them: the same finite bits each time."""
+    heads, groups, gap = 24, 2, 7
+    lens = [130, 257, 300, 61, 1000, 129, 515]
+    x = _prompts(heads, groups, [n + gap for n in lens], seed=5)
+    segs = [(off, n, 0, 0) for off, n in zip(x["offs"], lens)]
+    x["segs"] = qsa.make_segments(segs)
+    used = torch.zeros(x["T"], dtype=torch.bool, device="cuda")
+    for off, n, _, _ in segs:
+        used[off:off + n] = True
+    for name in ("q", "k", "v", "dout"):
+        x[name][~used] = float("nan")
+    runs = []
+    for _ in range(20):
+        o, lse = _forward(x)
+        g = [torch.full_like(x[n], 5.0) for n in ("q", "k", "v")]
+        qsa.qsa_prompt_attn_bwd(x["cfg"], x["segs"], x["T"], x["q"], x["k"], x["v"], o, lse, x["dout"], *g,
+                                workspace(x["cfg"], x["segs"], x["T"], qsa.QSA_OP_PROMPT_ATTN_BWD))
+        runs.append((o, lse, *g))
+    qsa.qsa_device_status()
+    for r in runs:
+        for a, b in zip(r, runs[0]):
+            assert torch.equal(a, b) and bool(torch.isfinite(a).all())
