@@ -286,7 +286,7 @@ def make_pages(k, v, table) -> qsa_pages_t:
 
 
 def _one_device(where, *tensors):
-    """The tensors' device; they are contiguous and on the current one."""
+    """The tensors' device; they are contiguous and, where it is a GPU, on the current one."""
     torch = _torch()
     dev = None
     for t in tensors:
@@ -300,6 +300,14 @@ def _one_device(where, *tensors):
             raise ValueError(f"{where}: tensors on {dev} and {t.device}")
     if dev is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
         raise ValueError(f"{where}: tensors on {dev}, but the current device is {torch.cuda.current_device()}")
+    return dev
+
+
+def _on_gpu(where, *tensors):
+    """_one_device, and that it is a GPU: the kernels take addresses as they are."""
+    dev = _one_device(where, *tensors)
+    if dev.type != "cuda":
+        raise ValueError(f"{where}: tensors on {dev}, not on a GPU")
     return dev
 
 
@@ -340,7 +348,7 @@ def qsa_append_kv(cfg, pages, segs, n_tokens, k, v, q=None, q_out=None, stream=N
     dtype, kv, qo, _ = _layout(where, cfg, n_tokens, pages)
     _check_like(where, "k", k, kv, dtype)
     _check_like(where, "v", v, kv, dtype)
-    dev = _one_device(where, pages.tensors[2], q_out)
+    dev = _on_gpu(where, pages.tensors[2], q_out)
     ld_q = 0
     if q is not None:
         _check_like(where, "q", q, qo, dtype)
@@ -363,7 +371,7 @@ def qsa_paged_attn_fwd(cfg, pages, segs, n_tokens, q, o, lse=None, workspace=Non
     _check_like(where, "o", o, qo, dtype)
     if lse is not None:
         _check_like(where, "lse", lse, stat, _torch().float32)
-    _one_device(where, q, o, lse, workspace, pages.tensors[2])
+    _on_gpu(where, q, o, lse, workspace, pages.tensors[2])
     _check(get_lib().qsa_paged_attn_fwd(cfg, pages, arr, n, n_tokens, q.data_ptr(), o.data_ptr(), _ptr(lse),
                                         _ptr(workspace), _bytes(workspace), _stream(stream)), where)
 
@@ -378,7 +386,7 @@ def qsa_prompt_attn_fwd(cfg, segs, n_tokens, q, k, v, o, lse=None, workspace=Non
         _check_like(where, name, t, shape, dtype)
     if lse is not None:
         _check_like(where, "lse", lse, stat, _torch().float32)
-    _one_device(where, q, k, v, o, lse, workspace)
+    _on_gpu(where, q, k, v, o, lse, workspace)
     _check(get_lib().qsa_prompt_attn_fwd(cfg, arr, n, n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
                                          _ptr(workspace), _bytes(workspace), _stream(stream)), where)
 
@@ -393,7 +401,7 @@ def qsa_prompt_attn_bwd(cfg, segs, n_tokens, q, k, v, o, lse, dout, dq, dk, dv, 
                            ("dk", dk, kv), ("dv", dv, kv)):
         _check_like(where, name, t, shape, dtype)
     _check_like(where, "lse", lse, stat, _torch().float32)
-    _one_device(where, q, k, v, o, lse, dout, dq, dk, dv, workspace)
+    _on_gpu(where, q, k, v, o, lse, dout, dq, dk, dv, workspace)
     _check(get_lib().qsa_prompt_attn_bwd(cfg, arr, n, n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
                                          _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), _bytes(workspace),
                                          _stream(stream)), where)
