@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       mbar_init(&ctl.full[0][i], 2);
       mbar_init(&ctl.full[1][i], 2);
       mbar_init(&ctl.s_done[i], 1);
-      mbar_init(&ctl.w_full[i], kSoftmaxWarps * 2);
+      mbar_init(&ctl.w_full[i], kSoftmaxWarps * 2 + 1);
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&ctl.d_full[i], 1);
@@ -361,6 +361,20 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       mbar_wait(&ctl.mma_done, 0, &never);
     }
     __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ============================================================ rank 1's operand of the gradient's product handed to rank 0
+    // (as the forward's V).  A chunk's arrival waits for the product that used the same
+    // w_full before: with more slots than buffers the operand may be a chunk too early.
+    int64_t gc = 0;
+    for (bool ok = true; ok && next();)
+      for (int c = p.c0; c < p.c1 && ok; ++c, ++gc) {
+        const int64_t last = gc - kBufs;
+        if (R::kN2 > kBufs && last >= 0)
+          ok = warp_wait_fast(&ctl.d_done[last % R::kN2], (uint32_t)((last / R::kN2) & 1), abort_flag);
+        ok = ok && warp_wait_fast(&ctl.d_full[gc % R::kN2], (uint32_t)((gc / R::kN2) & 1), abort_flag);
+        if (ok && lane == 0) mbar_arrive_cluster(&ctl.w_full[gc % kBufs], 0);
+        __syncwarp();
+      }
   } else if (warp == kQWarp) {
     // ============================================================ stationary tiles of the next unit
     int64_t uc = 0;
@@ -447,7 +461,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         if (kBufs == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_leader<2>(&ctl.s_free);
+          if (lane == 0) mbar_arrive_leader<2>(&ctl.s_free, rank);
         }
         // columns lo .. hi-1 of this thread's 64 count
         int lo = 0, hi = 64;
@@ -534,7 +548,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_leader<2>(&ctl.w_full[b]);
+          mbar_arrive_leader<2>(&ctl.w_full[b], rank, clear);
           if (kByKeys) mbar_arrive(&ctl.st_free[sbuf]);
         }
         if (!kByKeys || --left == 0) {
@@ -567,7 +581,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_leader<2>(&ctl.o_free);
+      if (lane == 0) mbar_arrive_leader<2>(&ctl.o_free, rank);
       ++uc;
     }
   }

@@ -25,9 +25,13 @@
 // thread one row and half of a chunk's keys and dims), one TMA producer that
 // fills two 32 KiB slots each of K and V in the order the MMAs consume them
 // (K0, K1, V0, K2, V1, ...), one warp that issues the MMAs (in rank 0), one
-// that loads Q of the next unit and one that checks V of the unit's own tokens.  K completes on rank 0's barrier, V on
-// each CTA's own, where the softmax warps wait for it before they hand over P,
-// so the MMA warp waits once per product and needs no fence.  A product is
+// that loads Q of the next unit and one that checks V of the unit's own tokens.
+// K completes on rank 0's barrier, V on each CTA's own, where the softmax warps
+// wait for it before they hand over P, so the MMA warp waits once per product and
+// needs no fence.  That rank 1's V has landed is released to it by rank 1's own
+// MMA warp, which issues nothing: the softmax warps release their P, which is in
+// tensor memory, without holding up for a release at cluster scope (by them it
+// cost 14 % of a long chunk's time), but for rows they zeroed.  A product is
 // committed to one barrier, which its readers and its slot's producer share.
 // TMEM: two S buffers (each half's P overwrites its own S columns), O in
 // columns 256..511.
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       mbar_init(&ctl.k_full[i], CG);
       mbar_init(&ctl.v_full[i], 1);
       mbar_init(&ctl.s_done[i], 1);
-      mbar_init(&ctl.p_full[i], kSoftmaxWarps * CG);
+      mbar_init(&ctl.p_full[i], CG == 1 ? kSoftmaxWarps : kSoftmaxWarps * 2 + 1);
       mbar_init(&ctl.pv_done[i], 1);
     }
     for (int i = 0; i < kNfBufs; ++i) {
@@ -381,6 +385,15 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       mbar_wait(&ctl.mma_done, 0, &never);
     }
     __syncwarp();
+  } else if (CG == 2 && warp == kMmaWarp) {
+    // ============================================================ rank 1's V handed to rank 0
+    int64_t gc = 0;
+    for (bool ok = true; ok && walk.next(t, p, x);)
+      for (int c = p.c0; c < p.c1 && ok; ++c, ++gc) {
+        ok = warp_wait_fast(&ctl.v_full[gc % kVSlots], (uint32_t)((gc / kVSlots) & 1), abort_flag);
+        if (ok && lane == 0) mbar_arrive_cluster(&ctl.p_full[gc & 1], 0);
+        __syncwarp();
+      }
   } else if (warp == kQWarp) {
     // ============================================================ Q of the next unit
     int64_t uc = 0;
@@ -571,7 +584,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
         mbar_wait_fast(&ctl.v_full[gc % kVSlots], (uint32_t)((gc / kVSlots) & 1), abort_flag);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_leader<CG>(&ctl.p_full[b]);
+        if (lane == 0) mbar_arrive_leader<CG>(&ctl.p_full[b], rank, clear);
       }
       if (!nf_taken) take_nf();
       float lt = 0.f;
@@ -640,7 +653,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_leader<CG>(&ctl.o_free);
+      if (lane == 0) mbar_arrive_leader<CG>(&ctl.o_free, rank);
       ++uc;
     }
   }

@@ -284,7 +284,8 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrives on the barrier at the same shared-memory address of CTA `rank`.
+// Arrives on the barrier at the same shared-memory address of CTA `rank`, releasing
+// what this thread wrote or saw to the barrier's waiters (mbar_try_wait<true>).
 __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
@@ -301,22 +302,28 @@ __device__ __forceinline__ uint32_t leader_bar(uint64_t* bar) {
   if constexpr (CG == 2) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(a));
   return a;
 }
-// Arrives on rank 0's barrier, expecting `bytes` more.
+// Arrives on rank 0's barrier, expecting `bytes` more; releases nothing.
 template <int CG>
 __device__ __forceinline__ void mbar_expect_tx_leader(uint64_t* bar, uint32_t bytes) {
   if constexpr (CG == 1)
     mbar_expect_tx(bar, bytes);
   else
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(leader_bar<2>(bar)),
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(leader_bar<2>(bar)),
                  "r"(bytes)
                  : "memory");
 }
-// Arrives on rank 0's barrier, releasing to its waiters (mbar_try_wait<true>)
-// this CTA's shared memory, which rank 0's MMAs read, and (after
-// tcgen05.fence::before_thread_sync) its tensor memory.
+// Arrives on rank 0's barrier after accesses to this CTA's tensor memory
+// (tcgen05.fence::before_thread_sync orders those before the arrival).  From rank 1
+// it releases no shared memory unless `written`: a release at cluster scope holds the
+// warp up for some 300 cycles.
 template <int CG>
-__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
-  if constexpr (CG == 1) mbar_arrive(bar); else mbar_arrive_cluster(bar, 0);
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar, uint32_t rank, bool written = false) {
+  if (CG == 1 || rank == 0)
+    mbar_arrive(bar);
+  else if (written)
+    mbar_arrive_cluster(bar, 0);
+  else
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar<2>(bar)) : "memory");
 }
 // 2-D tiled load into this CTA that completes on rank 0's barrier.
 template <int CG>
