@@ -52,6 +52,26 @@ qsa_status_t check_dense_segments(const qsa_segment_t* segs, int32_t n_segs, int
   return QSA_OK;
 }
 
+// An array of a call (p null: not given).
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+// No output shares memory with an input or another output: the kernels of a call
+// read their inputs while others of it write results, and some read them twice.
+bool spans_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  auto meet = [](const Span& a, const Span& b) {
+    return a.p && b.p && (const char*)a.p < (const char*)b.p + b.bytes && (const char*)b.p < (const char*)a.p + a.bytes;
+  };
+  for (const Span& o : outs) {
+    for (const Span& i : ins)
+      if (meet(o, i)) return false;
+    for (const Span& other : outs)
+      if (&other != &o && meet(o, other)) return false;
+  }
+  return true;
+}
+
 // ------------------------------------------------------------------ plan
 // Shape of one kind of launch.  For levelling: a unit's fixed cost (loading Q,
 // the epilogue) in chunks, and the fewest chunks a CTA takes of the tail, below
@@ -374,6 +394,11 @@ qsa_status_t run_dense_fwd(const Geo& g, bool tc, const qsa_segment_t* segs, int
   if (r != QSA_OK) return r;
   if (need > 0 && (!ws || ws_bytes < need)) return QSA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return QSA_ERR_INVALID_ARG;
+  const int64_t row = kHeadDim * (tc ? 2 : 4), q_bytes = (int64_t)n_tokens * g.H * row;
+  const int64_t kv_bytes = kv_rows * kv_groups * row;
+  if (!spans_apart({{o, q_bytes}, {lse, (int64_t)n_tokens * g.H * 4}},
+                   {{q, q_bytes}, {kv.k, kv_bytes}, {kv.v, kv_bytes}}))
+    return QSA_ERR_INVALID_ARG;
   CUtensorMap m[4];                      // K, V, Q by whole tokens, Q by parts of one
   DenseTcArgs a;
   if (tc) {
@@ -734,6 +759,12 @@ QSA_API qsa_status_t qsa_prompt_attn_bwd(const qsa_config_t* cfg, const qsa_segm
     if ((s = plan_dense_bwd(g, tc, segs, n_segs, n_tokens, p)) != QSA_OK) return s;
     if (!workspace || ws_bytes < p.bytes) return QSA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return QSA_ERR_INVALID_ARG;
+    const int64_t row = kHeadDim * (tc ? 2 : 4), q_bytes = (int64_t)n_tokens * g.H * row;
+    const int64_t kv_bytes = (int64_t)n_tokens * g.G * row;
+    if (!spans_apart({{dq, q_bytes}, {dk, kv_bytes}, {dv, kv_bytes}},
+                     {{q, q_bytes}, {k, kv_bytes}, {v, kv_bytes}, {o, q_bytes}, {dout, q_bytes},
+                      {lse, (int64_t)n_tokens * g.H * 4}}))
+      return QSA_ERR_INVALID_ARG;
     const DenseBwdArgs a{q, k, v, lse, (const float*)workspace, dout, dq, dk, dv, g.H, g.scale, nullptr};
     return tc ? run_dense_bwd_bf16(g, p, a, o, (char*)workspace, n_tokens, (cudaStream_t)stream)
               : run_dense_bwd_f32(g, p, a, o, (char*)workspace, (cudaStream_t)stream);

@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <mutex>
 #include <functional>
+#include <initializer_list>
 #include <utility>
 #include <vector>
 

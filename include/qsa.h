@@ -379,7 +379,9 @@ qsa_status_t qsa_append_kv(const qsa_config_t* cfg, const qsa_pages_t* pages,
  * A page number outside [0, n_pages) is skipped (its tokens contribute
  * nothing) and reported by qsa_device_status as QSA_ERR_BAD_INDEX; a query
  * left without any key gets o = 0 and lse = -inf.
- * Token rows of different segments must not overlap (QSA_ERR_INVALID_ARG).
+ * Token rows of different segments must not overlap, and o and lse share no
+ * memory with each other or with q, K and V (QSA_ERR_INVALID_ARG); the
+ * workspace shares none with any array.
  * workspace >= qsa_workspace_size(..., QSA_OP_PAGED_ATTN) bytes (may be NULL
  * when that size is 0); contents on entry are ignored; calls whose work may
  * overlap on the GPU need one each.  The result does not depend on the order
@@ -399,8 +401,9 @@ qsa_status_t qsa_paged_attn_fwd(const qsa_config_t* cfg, const qsa_pages_t* page
  *   o[i][h][:] = sum_j softmax_j(scale * q[i][h] . k[j][g]) v[j][g],  lse as above.
  * q, o: device [T][n_q_heads][head_dim]; k, v: device [T][n_kv_groups][head_dim]
  * (I/O dtype, already rotated); lse: device fp32 [T][n_q_heads] or NULL.
- * Rows of no segment are neither read nor written.  Overlaps, workspace
- * (QSA_OP_PROMPT_ATTN) and repeatability as qsa_paged_attn_fwd.
+ * Rows of no segment are neither read nor written.  Overlaps (of token rows and
+ * of arrays), workspace (QSA_OP_PROMPT_ATTN) and repeatability as
+ * qsa_paged_attn_fwd.
  */
 qsa_status_t qsa_prompt_attn_fwd(const qsa_config_t* cfg, const qsa_segment_t* segs,
                                  int32_t n_segs, int32_t n_tokens, const void* q, const void* k,
@@ -416,7 +419,8 @@ qsa_status_t qsa_prompt_attn_fwd(const qsa_config_t* cfg, const qsa_segment_t* s
  * (the sums over i, h: every query head of the group).  q, k, v, o, lse as the
  * forward read and wrote them; dout: device [T][n_q_heads][head_dim].  dq, dk,
  * dv: device, laid out as q, k, v, in the I/O dtype; rows of the segments are
- * written (not accumulated into), other rows are left as they were.  fp32
+ * written (not accumulated into), other rows are left as they were; dq, dk and dv
+ * share no memory with each other or an input (QSA_ERR_INVALID_ARG).  fp32
  * accumulation in a fixed order, one rounding at the end: repeated calls give
  * the same bits.  bf16: P and the score gradients are rounded to bf16 for the
  * tensor-core products (a quarter of the latter with their remainders).  A

@@ -29,3 +29,43 @@ def test_tensors_of_the_host_are_refused():
                                                  _z(3, 2, D), ws)):
         with pytest.raises(ValueError, match="not on a GPU"):
             call()
+
+
+BASE = 1 << 40                # fake addresses, far from each other unless a test moves one; no call here may be valid
+
+
+@pytest.mark.parametrize("dtype,row", [("bf16", 512), ("f32", 1024)])
+def test_outputs_that_share_memory_with_another_array_are_refused(dtype, row):
+    """Ranges of 8 tokens of 24 heads or 2 groups; `row` bytes of a head."""
+    cfg = qsa.make_config(shape(dtype=dtype))
+    lib, T = qsa.get_lib(), 8
+    arr, n = qsa.make_segments([(0, T, 0, 0)])
+    at = {name: BASE + (i << 32) for i, name in enumerate(("q", "k", "v", "o", "lse", "dout", "dq", "dk", "dv", "ws"))}
+    q_end, kv_end = T * 24 * row, T * 2 * row
+
+    def paged(**move):
+        a = dict(at, **move)
+        pages = qsa.qsa_pages_t(a["k"], a["v"], BASE - 4096, 4, 16, 1, 4)
+        return lib.qsa_paged_attn_fwd(ctypes.byref(cfg), ctypes.byref(pages), arr, n, T, a["q"], a["o"], a["lse"],
+                                      a["ws"], 1 << 31, None)
+
+    def prompt(**move):
+        a = dict(at, **move)
+        return lib.qsa_prompt_attn_fwd(ctypes.byref(cfg), arr, n, T, a["q"], a["k"], a["v"], a["o"], a["lse"], a["ws"],
+                                       1 << 31, None)
+
+    def bwd(**move):
+        a = dict(at, **move)
+        return lib.qsa_prompt_attn_bwd(ctypes.byref(cfg), arr, n, T, *(a[x] for x in (
+            "q", "k", "v", "o", "lse", "dout", "dq", "dk", "dv", "ws")), 1 << 31, None)
+
+    bad = qsa.QSA_ERR_INVALID_ARG
+    for call in (paged, prompt):
+        assert call(o=at["q"]) == bad and call(o=at["q"] + q_end - 16) == bad and call(o=at["q"] - q_end + 16) == bad
+        assert call(o=at["k"]) == bad and call(o=at["v"] + kv_end - 16) == bad
+        assert call(lse=at["q"] + 64) == bad and call(lse=at["o"] + q_end - 4) == bad and call(lse=at["k"]) == bad
+    assert paged(o=at["v"] + 4 * 2 * 16 * row - 16) == bad              # the last row of the last page
+    for out, end in (("dq", q_end), ("dk", kv_end), ("dv", kv_end)):
+        for other in ("q", "k", "v", "o", "lse", "dout", "dq", "dk", "dv"):
+            if other != out:
+                assert bwd(**{out: at[other]}) == bad and bwd(**{out: at[other] - end + 16}) == bad, (out, other)
