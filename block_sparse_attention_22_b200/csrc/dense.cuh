@@ -24,6 +24,7 @@ namespace qsa {
 namespace dense {
 constexpr int kMaxGrid = 148;              // CTAs (or CTA pairs) a table is cut for
 constexpr int kPartFloats = kHeadDim + 4;  // a row's partial: 256 sums, maximum and sum of its softmax, 2 unused
+constexpr float kNan = __builtin_nanf("");
 }  // namespace dense
 
 // A kernel that needs nothing from the one launched before it, only what that
@@ -156,7 +157,8 @@ __device__ __forceinline__ int dense_piece_slot(const DenseTable& t, int u, int 
 // Joins the pieces of each cut unit: with m the largest of the pieces' maxima
 // (log2 units), l = sum l_p 2^(m_p - m), o = sum o_p 2^(m_p - m) / l.  A piece
 // without a key of a row has m_p = -inf and l_p = 0 and counts nothing (scores that
-// are all NaN: m_p = -inf, l_p = NaN).  One warp per row,
+// are all NaN: m_p = -inf, l_p = NaN; all -inf: l_p = -1, which counts nothing beside
+// other scores and makes the row NaN, 0 / 0, without them).  One warp per row,
 // 8 dims per lane, for units in kFewPieces or fewer, all read at once; pieces are
 // added in the order of their keys.
 constexpr int kFewPieces = 4;
@@ -213,7 +215,10 @@ __global__ void __launch_bounds__(128)
       acc[4 * h + 3] += w * v[k][h].w;
     }
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;     // l = 0: no key at all
+  float inv = l != 0.f ? 1.f / l : 0.f;           // l = 0: no key at all, or scores of -inf only
+#pragma unroll
+  for (int k = 0; k < kFewPieces; ++k)
+    if (l == 0.f && ml[k].y < 0.f) inv = dense::kNan;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     store4(o + at + 128 * h, acc[4 * h] * inv, acc[4 * h + 1] * inv, acc[4 * h + 2] * inv, acc[4 * h + 3] * inv);
@@ -264,6 +269,8 @@ __global__ void __launch_bounds__(256, 1)
   const float w = mp == -INFINITY ? 0.f : exp2f(mp - m);
   if (threadIdx.x < n) w_s[threadIdx.x] = w;
   const float l = block_reduce(w * lp, false);          // its barriers also order w_s, at_s
+  // l = 0 (the same in every thread): no key at all, or scores of -inf only
+  const bool all_inf = l == 0.f && __syncthreads_or(lp < 0.f);
   float acc[8] = {};
   constexpr int kBatch = 5;                              // pieces in flight: 74 of a long row are two batches
   for (int k0 = warp; k0 < n; k0 += 8 * kBatch) {
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(256, 1)
   float v = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) v += acc_s[k][threadIdx.x];
-  o[at * kHeadDim + threadIdx.x] = IO<T>::from_f(l != 0.f ? v / l : 0.f);      // l = 0: no key at all
+  o[at * kHeadDim + threadIdx.x] = IO<T>::from_f(l != 0.f ? v / l : all_inf ? dense::kNan : 0.f);
   if (lse && threadIdx.x == 0) lse[at] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 

@@ -61,12 +61,12 @@ __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], const uint32_t (&a)[
 // make a row's factors first, in place of the maxima; then a thread joins four
 // dims of every fourth row.
 template <typename T>
-__device__ __forceinline__ void decode_join(const DenseUnit& x, const DensePiece& p, int prows, int64_t head0,
-                                            const unsigned char* smem, float* m_s, float* l_s, T* o, float* lse,
-                                            float* part) {
+__device__ __forceinline__ void decode_join(const DenseTable& t, const KvSource& kv, const DenseUnit& x,
+                                            const DensePiece& p, int64_t head0, const unsigned char* smem, float* m_s,
+                                            float* l_s, T* o, float* lse, float* part) {
   using namespace dense_decode;
   static_assert(kWarps == 8 && kRows * kWarps <= kThreads && kThreads == kHeadDim, "thread layouts below");
-  float* const dst = part + (int64_t)p.part * prows * dense::kPartFloats;      // used by a cut unit's piece only
+  float* const dst = part + (int64_t)p.part * t.prows * dense::kPartFloats;      // used by a cut unit's piece only
   if (threadIdx.x < kRows * kWarps) {
     const int r = threadIdx.x >> 3, at = (threadIdx.x & 7) * kRows + r;
     const float m = m_s[at];
@@ -79,9 +79,11 @@ __device__ __forceinline__ void decode_join(const DenseUnit& x, const DensePiece
     for (int off = 4; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
     m_s[at] = f;
     if ((threadIdx.x & 7) == 0) {
-      l_s[at] = l;
+      const bool all_inf = r < x.nrows && l == 0.f &&
+                           any_key<true>(kv, t, x.si, p.c0 * kKeys, min(x.kv_len, p.c1 * kKeys) - 1);
+      l_s[at] = all_inf ? dense::kNan : l;
       if (r < x.nrows && p.part >= 0)
-        *reinterpret_cast<float2*>(dst + r * dense::kPartFloats + kHeadDim) = make_float2(mr, l);
+        *reinterpret_cast<float2*>(dst + r * dense::kPartFloats + kHeadDim) = make_float2(mr, all_inf ? -1.f : l);
       else if (r < x.nrows && lse)
         lse[head0 + r] = l != 0.f ? (mr + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
       *reinterpret_cast<float2*>(dst + 8 * kOLd) = make_float2(o[j][2], o[j][3]);
     }
     __syncthreads();
-    decode_join(x, p, t.prows, head0, smem, m_s, l_s, a.o, a.lse, a.part);
+    decode_join(t, a.kv, x, p, head0, smem, m_s, l_s, a.o, a.lse, a.part);
     __syncthreads();                                      // shared memory free for the next piece
   }
   dense_wait_last(a.late);
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
       reinterpret_cast<float4*>(o_s + h * kOLd)[lane + 32] = make_float4(o[h][2].x, o[h][2].y, o[h][3].x, o[h][3].y);
     }
     __syncthreads();
-    decode_join(x, p, t.prows, head0, smem, m_s, l_s, a.o, a.lse, a.part);
+    decode_join(t, a.kv, x, p, head0, smem, m_s, l_s, a.o, a.lse, a.part);
     __syncthreads();                                      // shared memory free for the next piece
   }
   dense_wait_last(a.late);

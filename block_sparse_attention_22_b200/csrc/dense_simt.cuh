@@ -59,6 +59,18 @@ __device__ __forceinline__ int64_t kv_row(const KvSource& s, const DenseTable& t
   return ((int64_t)(t.q_offset[si] + j) * t.G + grp) * kHeadDim;
 }
 
+// Whether any of the keys j0 .. j1 of a segment is there to be attended, for rows
+// whose softmax sum is 0: true means that all their scores are -inf.
+template <bool PAGED>
+__device__ __noinline__ bool any_key(const KvSource& s, const DenseTable& t, int si, int32_t j0, int32_t j1) {
+  if (j1 < j0) return false;
+  if (!PAGED) return true;
+  const int32_t* pages = s.table + (int64_t)t.slot[si] * s.max_pages;
+  for (int32_t pi = j0 / s.page_tokens; pi <= j1 / s.page_tokens; ++pi)
+    if (pages[pi] >= 0 && pages[pi] < s.n_pages) return true;
+  return false;
+}
+
 // Copies `rows` rows of 256 floats into shared memory (stride kLd); row r from
 // src(r), zeros where src(r) is null.
 template <typename T, typename Src>
@@ -261,8 +273,10 @@ __global__ void __launch_bounds__(dense_simt::kThreads, 1)
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (ra + i >= x.nrows) continue;
+      const bool all_inf =
+          l[i] == 0.f && any_key<PAGED>(kv, t, si, p.c0 * kKeys, min((int32_t)pos[i], p.c1 * kKeys - 1));
       if (p.part < 0) {
-        const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
+        const float inv = all_inf ? dense::kNan : l[i] != 0.f ? 1.f / l[i] : 0.f;
         const int64_t at = q_at(ra + i);
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj)
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(dense_simt::kThreads, 1)
               make_float4(acc[i][4 * jj], acc[i][4 * jj + 1], acc[i][4 * jj + 2], acc[i][4 * jj + 3]);
         if (tx == 0) {
           dst[kHeadDim] = m[i];
-          dst[kHeadDim + 1] = l[i];
+          dst[kHeadDim + 1] = all_inf ? -1.f : l[i];
         }
       }
     }

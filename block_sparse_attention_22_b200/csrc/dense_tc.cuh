@@ -599,7 +599,10 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       tc_fence_after();
       if (warp_active) {
         const bool whole = p.part < 0;
-        const float inv = !whole ? 1.f : lt != 0.f ? 1.f / lt : 0.f;    // lt = 0: no key at all
+        // lt = 0: no key at all, or scores of -inf only
+        const bool all_inf = active && lt == 0.f && any_key<PAGED>(a.kv, t, x.si, p.c0 * KC, min(pos, p.c1 * KC - 1));
+        __syncwarp();
+        const float inv = !whole ? 1.f : all_inf ? dense::kNan : lt != 0.f ? 1.f / lt : 0.f;
         const int row_q = (int)rank * 128 + quad * 32 + (lane & ~3);   // first row of this lane's quad
         float* part_q = whole ? nullptr : a.part + ((int64_t)p.part * t.prows + row_q) * dense::kPartFloats;
         int64_t at_q[4];
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
           if (!whole) {
             float* st = part_q + (lane & 3) * dense::kPartFloats + kHeadDim;
             st[0] = m;
-            st[1] = lt;
+            st[1] = all_inf ? -1.f : lt;
           } else if (a.lse) {
             a.lse[at] = lt != 0.f ? (m + log2f(lt)) * 0.6931471805599453f : -INFINITY;
           }

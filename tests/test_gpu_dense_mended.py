@@ -127,3 +127,124 @@ def test_rows_zeroed_by_either_cta_of_a_pair_are_zero_in_the_product():
     for r in runs:
         for a, b in zip(r, runs[0]):
             assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+
+
+# ------------------------------------------------------------------ rows whose every score is -inf
+def _paged_with_keys_at_minus_inf(dtype, seqs, page=16, seed=6):
+    """Group 0's keys have -inf in dim 9, its queries something positive there."""
+    sh = shape(24, 2, dtype)
+    dt = torch_dtype(sh)
+    gen = torch.Generator().manual_seed(seed)
+    table, n_pages = make_table([c + n for c, n in seqs], page, gen)
+    kp, vp = (torch.full((n_pages, 2, page, D), 5.0, dtype=dt, device="cuda") for _ in range(2))
+    kv, segs, T = [], [], 0
+    for i, (c, n) in enumerate(seqs):
+        k, v = (_randn(gen, c + n, 2, D, dtype=dt) for _ in range(2))
+        kv.append((k, v))
+        segs.append((T, n, c, i))
+        T += n
+    q = _randn(gen, T, 24, D, dtype=dt)
+    q[..., 9] = q[..., 9].abs() + 0.5
+    x = dict(cfg=qsa.make_config(sh), T=T, q=q, kv=kv, segs_at=segs, segs=qsa.make_segments(segs), table=table, kp=kp,
+             vp=vp, dt=dt, page=page)
+    clean = _run_paged(x)
+    for k, _ in kv:
+        k[:, 0, 9] = -math.inf
+    return x, clean
+
+
+def _run_paged(x):
+    for i, (k, v) in enumerate(x["kv"]):
+        fill_pages(x["kp"], x["vp"], x["table"], x["page"], i, k, v)
+    o, lse = torch.full_like(x["q"], 5.0), torch.full(x["q"].shape[:2], 5.0, device="cuda")
+    qsa.qsa_paged_attn_fwd(x["cfg"], qsa.make_pages(x["kp"], x["vp"], x["table"].cuda()), x["segs"], x["T"], x["q"], o,
+                           lse, workspace(x["cfg"], x["segs"], x["T"], qsa.QSA_OP_PAGED_ATTN))
+    return o, lse
+
+
+KINDS = [[(0, 1), (40, 1), (127, 1)], [(900, 1)] * 60, [(2000, 1)] * 8, [(20000, 1)], [(4000, 5)] * 3, [(0, 3), (30, 7)],
+         [(1500, 300), (0, 200)], [(0, 20)]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs", KINDS, ids=["decode", "few pieces", "many pieces", "long", "short", "first", "chunks",
+                                             "tile"])
+def test_a_row_whose_every_score_is_minus_infinity_is_nan(dtype, seqs):
+    """0 / 0 by the formula, with lse = -inf, whole or cut; the other group's heads
+    keep their bits."""
+    x, (clean, clean_lse) = _paged_with_keys_at_minus_inf(dtype, seqs)
+    o, lse = _run_paged(x)
+    qsa.qsa_device_status()
+    assert bool(torch.isnan(o[:, :12]).all()) and bool((lse[:, :12] == -math.inf).all())
+    assert torch.equal(o[:, 12:], clean[:, 12:]) and torch.equal(lse[:, 12:], clean_lse[:, 12:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs", KINDS[1:], ids=["few pieces", "many pieces", "long", "short", "first", "chunks", "tile"])
+def test_one_finite_score_among_minus_infinities_takes_the_row(dtype, seqs):
+    """Its weight is 1 in whichever piece it lies: o is that key's value, rounded once."""
+    x, _ = _paged_with_keys_at_minus_inf(dtype, seqs)
+    at = []
+    for i, ((c, n), (k, _)) in enumerate(zip(seqs, x["kv"])):
+        at.append(c * (i + 1) // len(seqs))               # visible to every row of the segment
+        k[at[-1], 0, 9] = 0.0
+    o, lse = _run_paged(x)
+    for (off, n, c, i), j in zip(x["segs_at"], at):
+        k, v = x["kv"][i]
+        assert torch.equal(o[off:off + n, :12], v[j, :1].expand(n, 12, D))
+        s = (x["q"][off:off + n, :12].to(F64) * k[j, 0].to(F64)).sum(-1) * SCALE
+        e = score_error(x["q"], torch.where(torch.isfinite(k), k, 0), SCALE)
+        assert bool(((lse[off:off + n, :12].to(F64) - s).abs() <= e + 2.0 ** -20 * (1 + s.abs())).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs", [[(900, 1)] * 30, [(2000, 1)] * 4, [(3000, 5)] * 3, [(100, 200)]],
+                         ids=["decode", "many pieces", "short", "chunks"])
+def test_rows_without_a_key_stay_zero_beside_rows_at_minus_infinity(dtype, seqs):
+    """All pages of the last sequence out of range: no key, o = 0.  All but one
+    of the first one's: still keys, all at -inf, o = NaN."""
+    x, _ = _paged_with_keys_at_minus_inf(dtype, seqs + [(700, 4)])
+    c, n = seqs[0]
+    good = x["table"]
+    for i, (k, v) in enumerate(x["kv"]):
+        fill_pages(x["kp"], x["vp"], good, x["page"], i, k, v)
+    bad = good.clone()
+    bad[0, :] = -1
+    bad[0, c // 2 // 16] = good[0, c // 2 // 16]
+    bad[len(seqs), :] = 1 << 30
+    o, lse = torch.full_like(x["q"], 5.0), torch.full(x["q"].shape[:2], 5.0, device="cuda")
+    qsa.qsa_paged_attn_fwd(x["cfg"], qsa.make_pages(x["kp"], x["vp"], bad.cuda()), x["segs"], x["T"], x["q"], o, lse,
+                           workspace(x["cfg"], x["segs"], x["T"], qsa.QSA_OP_PAGED_ATTN))
+    assert qsa.device_status() == qsa.QSA_ERR_BAD_INDEX
+    assert bool(torch.isnan(o[:n, :12]).all()) and bool((lse[:, :12] == -math.inf).all())
+    assert bool(torch.isfinite(o[:n, 12:]).all()) and bool(torch.isfinite(lse[:n, 12:]).all())
+    assert bool((o[-4:] == 0).all()) and bool((lse[-4:] == -math.inf).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompts_at_minus_infinity_and_their_gradient_are_nan_in_their_rows_alone(dtype):
+    """Keys of the first 30 tokens of the second prompt at -inf in group 0: rows
+    before token 30 have no other score; the rows after it do."""
+    lens = [70, 333, 40]
+    x = _prompts(24, 2, lens, seed=7, dtype=dtype)
+    x["q"][..., 9] = x["q"][..., 9].abs() + 0.5
+    clean = _forward(x)
+    x["k"][70:100, 0, 9] = -math.inf
+    o, lse = _forward(x)
+    hit = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    hit[70:100, :12] = True
+    assert bool(torch.isnan(o[hit]).all()) and bool((lse[hit] == -math.inf).all())
+    assert bool(torch.isfinite(o[~hit]).all()) and bool(torch.isfinite(lse[~hit]).all())
+    for a, b in zip((o, lse), clean):
+        assert torch.equal(a[:70], b[:70]) and torch.equal(a[403:], b[403:]) and torch.equal(a[:, 12:], b[:, 12:])
+    t = slice(100, 403)
+    ref = attend64(x["q"][t, :12], x["k"][t, :1], x["v"][t, :1], 0, SCALE)        # the keys with a weight
+    check_forward(o[t, :12], lse[t, :12], ref, score_error(x["q"][t], x["k"][t], SCALE), x["dt"])
+    g = [torch.full_like(x[n], 5.0) for n in ("q", "k", "v")]
+    qsa.qsa_prompt_attn_bwd(x["cfg"], x["segs"], x["T"], x["q"], x["k"], x["v"], o, lse, x["dout"], *g,
+                            workspace(x["cfg"], x["segs"], x["T"], qsa.QSA_OP_PROMPT_ATTN_BWD))
+    qsa.qsa_device_status()
+    assert bool(torch.isnan(g[0][hit]).all())
+    assert bool(torch.isfinite(g[0][:, 12:]).all()) and bool(torch.isfinite(g[0][:70]).all())
+    for a in g[1:]:
+        assert bool(torch.isfinite(a[100:, 0]).all()) and bool(torch.isfinite(a[:, 1]).all())
