@@ -26,9 +26,9 @@
 // 1.50 with delta's (o comes rounded); the remainders of a quarter of the columns
 // (kLo) are therefore multiplied too, from the columns that dS leaves free: 1.41,
 // for 3% of the training step's time (all remainders: 1.11, 11%).  Rows of few
-// keys have an o as large as v, and delta's error is then several times dS's:
-// where a unit's keys are one chunk, the dQ kernel forms delta as the sum of P dP
-// instead and leaves it for the dK kernel.
+// keys have an o as large as v, and delta's error is then several times dS's: for
+// rows whose keys are all in the first chunk (positions below 128) the dQ kernel
+// forms delta as the sum of P dP instead and leaves it for the dK kernel.
 //
 // Roles per CTA (12 warps): eight softmax warps (two per lane quadrant, each
 // thread one lane and 64 of a chunk's columns), one TMA producer, one warp that
@@ -92,7 +92,7 @@ struct DenseBwdMaps {
 
 struct DenseBwdTcArgs {
   const float* lse2;          // [H][stat rows] lse * log2 e, +inf behind a segment's end
-  float* delta;               // [H][stat rows]; rows of units of one chunk are rewritten by dQ
+  float* delta;               // [H][stat rows]; those of positions below kKeys are rewritten by dQ
   const uint8_t* flags;       // segment_flagged: not for these kernels
   __nv_bfloat16* out;
   float* part;
@@ -493,7 +493,9 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
           dst = lane_addr + kTmemP + half * 64;
           mbar_wait_fast(&ctl.dp_done, (uint32_t)(gc & 1), abort_flag);
           tc_fence_after();
-          if (M == kDq && x.nchunks == 1) {          // delta from the row's own P and dP
+          // Delta from the row's own P and dP, for rows without keys in later chunks.  (edge:
+          // of the CTA, so that both warps of a row meet here.)
+          if (M == kDq && j0 == 0 && edge < kKeys) {
             float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < 64; k += 16) {
@@ -505,8 +507,10 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
             }
             stats[half * 128 + li] = sum;
             named_bar_sync(1 + quad, 64);
-            delta = stats[li] + stats[128 + li];
-            if (active && half == 0) a.delta[sat] = delta;
+            if (own < kKeys) {
+              delta = stats[li] + stats[128 + li];
+              if (active && half == 0) a.delta[sat] = delta;
+            }
             named_bar_sync(1 + quad, 64);            // read before the next unit's sums
           }
           float v[4][16];                            // one wait for all: dS is what the next products wait for

@@ -248,3 +248,42 @@ def test_prompts_at_minus_infinity_and_their_gradient_are_nan_in_their_rows_alon
     assert bool(torch.isfinite(g[0][:, 12:]).all()) and bool(torch.isfinite(g[0][:70]).all())
     for a in g[1:]:
         assert bool(torch.isfinite(a[100:, 0]).all()) and bool(torch.isfinite(a[:, 1]).all())
+
+
+# ------------------------------------------------------------------ delta of the first rows
+@pytest.mark.parametrize("heads,groups", [(8, 8), (6, 2), (24, 2), (10, 5)])
+@pytest.mark.parametrize("lens", [[129], [128, 300, 1], [600, 257]])
+def test_gradients_of_the_first_rows_do_not_carry_the_rounding_of_o(heads, groups, lens):
+    """Every value of a prompt is a permutation of one vector whose dims add up to 0,
+    in eighths, and dout is 1 in all dims, so dP is 0 for every key, exactly: dS, dq
+    and dk are 0, and what is left is delta's error.  From the row's own P and dP,
+    for rows of at most 128 keys, there is none; from a rounded o it was 2^-9 of its
+    parts.  Later rows have it still, and the rounding of P: delta is off by at most
+    (2^-8 + 2^-8 + fp32) sum |v| of a key, which bounds their part of dk."""
+    x = _prompts(heads, groups, lens, seed=8)
+    gen = torch.Generator().manual_seed(9)
+    half = torch.round(torch.randn(D // 2, generator=gen) * 8) / 8
+    order = torch.argsort(torch.rand((x["T"], groups, D), generator=gen), dim=-1)
+    x["v"] = torch.cat([half, -half]).to(BF)[order].cuda()
+    x["dout"] = torch.ones_like(x["dout"])
+    o, lse = _forward(x)
+    g = [torch.full_like(x[n], 5.0) for n in ("q", "k", "v")]
+    qsa.qsa_prompt_attn_bwd(x["cfg"], x["segs"], x["T"], x["q"], x["k"], x["v"], o, lse, x["dout"], *g,
+                            workspace(x["cfg"], x["segs"], x["T"], qsa.QSA_OP_PROMPT_ATTN_BWD))
+    qsa.qsa_device_status()
+    hpg = heads // groups
+    ddelta = 1.1 * 2.0 ** -7 * x["v"][0, 0].to(F64).abs().sum().item()
+    for off, n in zip(x["offs"], lens):
+        assert not g[0][off:off + min(n, 128)].any()
+        if n <= 128:
+            assert not g[1][off:off + n].any()
+            continue
+        t = slice(off, off + n)
+        q, k = x["q"][t].to(F64), x["k"][t].to(F64)
+        for grp in range(groups):
+            tol = torch.zeros((n, D), dtype=F64, device="cuda")
+            for h in range(grp * hpg, (grp + 1) * hpg):
+                s = (q[:, h] @ k[:, grp].t()) * SCALE
+                s.masked_fill_(torch.ones_like(s, dtype=torch.bool).triu(1), -math.inf)
+                tol += SCALE * ddelta * (torch.softmax(s, 1)[128:].t() @ q[128:, h].abs())
+            assert bool((g[1][t, grp].to(F64).abs() <= tol).all()), (grp, n)
