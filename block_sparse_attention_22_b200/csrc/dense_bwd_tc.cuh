@@ -20,15 +20,15 @@
 // dV keys, whose chunks are the group's heads x tiles of 128 tokens from the
 // unit's first key on.  Chunks are 128 wide; the streamed operand of S and dP
 // is split between the CTAs by rows, that of the gradient's product by dims.
-// P and dS are rounded to bf16 for the products and written over the columns
-// they were computed from, so no warp waits for another's reads.  A rounded
-// dS alone makes the error of dq and dk 1.42 times that of rounding the result,
-// 1.50 with delta's (o comes rounded); the remainders of a quarter of the columns
-// (kLo) are therefore multiplied too, from the columns that dS leaves free: 1.41,
-// for 3% of the training step's time (all remainders: 1.11, 11%).  Rows of few
-// keys have an o as large as v, and delta's error is then several times dS's: for
-// rows whose keys are all in the first chunk (positions below 128) the dQ kernel
-// forms delta as the sum of P dP instead and leaves it for the dK kernel.
+// P and dS are rounded to bf16 for the products, once each, and written over the
+// columns they were computed from, so no warp waits for another's reads.  A rounded
+// dS makes the error of dq and dk 1.42 times that of rounding the result alone, as
+// P's does dv's.  (Its remainders could be multiplied too, from the columns that dS
+// leaves free: 1.00 times, but 8.33 ms instead of 7.29 for the two prompts below
+// with their forward.)  Rows of few keys have an o as large as v, and the error of
+// delta = dout . o, o rounded, is then several times dS's: for rows whose keys are
+// all in the first chunk (positions below 128) the dQ kernel forms delta as the sum
+// of P dP instead and leaves it for the dK kernel.
 //
 // Roles per CTA (12 warps): eight softmax warps (two per lane quadrant, each
 // thread one lane and 64 of a chunk's columns), one TMA producer, one warp that
@@ -79,7 +79,6 @@ constexpr int kOffCtl = 3 * kSlotBytes + 2 * kQBytes; // 229376; dV: 5 slots and
 constexpr int kCtlBytes = 3072;
 constexpr int kSmemBytes = kOffCtl + kCtlBytes;       // 232448: the base itself is 1024-byte aligned
 constexpr uint32_t kTmemP = 128, kTmemD = 256;
-constexpr int kLo = 1;                                // k-steps of 16 in each half whose remainders are multiplied too
 using Pair = dense_tc::Shape<2>;
 }  // namespace dense_bwd
 
@@ -330,12 +329,6 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       for (int kk = 0; kk < 8; ++kk)                 // k-steps of 16 chunk columns; each half's start at its columns
         umma_ts_warp<2>(leader, tmem + kTmemD, w + (kk >> 2) * 64 + (kk & 3) * 8, db + kk * 128, Pair::kIdescPV,
                         (c | kk) != 0);
-      if (M != kDv) {
-#pragma unroll
-        for (int kk = 0; kk < 2 * kLo; ++kk)         // the remainders, behind their half's dS
-          umma_ts_warp<2>(leader, tmem + kTmemD, w + (kk / kLo) * 64 + 32 + (kk % kLo) * 8,
-                          db + ((kk / kLo) * 4 + kk % kLo) * 128, Pair::kIdescPV, true);
-      }
       umma_commit_warp<2>(leader, &ctl.d_done[slot]);
       if (c == n - 1) umma_commit_warp<2>(leader, &ctl.o_full);
       return true;
@@ -537,13 +530,6 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(w[k + 2 * i], w[k + 2 * i + 1]);
           tmem_st16u(dst + k / 2, pk);
-          if (M != kDv && k < 16 * kLo) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              pk[i] = pack_bf16x2(w[k + 2 * i] - __uint_as_float(pk[i] << 16),
-                                  w[k + 2 * i + 1] - __uint_as_float(pk[i] & 0xffff0000u));
-            tmem_st16u(dst + 32 + k / 2, pk);
-          }
         }
         tmem_wait_st();
         const bool clear = j0 + kKeys > seg_n;

@@ -424,8 +424,8 @@ qsa_status_t qsa_prompt_attn_fwd(const qsa_config_t* cfg, const qsa_segment_t* s
  * written (not accumulated into), other rows are left as they were; dq, dk and dv
  * share no memory with each other or an input (QSA_ERR_INVALID_ARG).  fp32
  * accumulation in a fixed order, one rounding at the end: repeated calls give
- * the same bits.  bf16: P and the score gradients are rounded to bf16 for the
- * tensor-core products (a quarter of the latter with their remainders).  A
+ * the same bits.  bf16: P and the score gradients P (dout . v - delta) are
+ * rounded to bf16, once each, for the tensor-core products.  A
  * prompt that holds infinities or NaN in k, v, lse or dout . o is done on CUDA
  * cores, where only the pairs it enters see them.  workspace: QSA_OP_PROMPT_ATTN_BWD.
  */
