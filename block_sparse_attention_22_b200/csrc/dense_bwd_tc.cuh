@@ -358,13 +358,13 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     // ============================================================ rank 1's operand of the gradient's product handed to rank 0
     // (as the forward's V).  A chunk's arrival waits for the product that used the same
     // w_full before: with more slots than buffers the operand may be a chunk too early.
-    int64_t gc = 0;
+    uint32_t gc = 0;
     for (bool ok = true; ok && next();)
       for (int c = p.c0; c < p.c1 && ok; ++c, ++gc) {
-        const int64_t last = gc - kBufs;
-        if (R::kN2 > kBufs && last >= 0)
-          ok = warp_wait_fast(&ctl.d_done[last % R::kN2], (uint32_t)((last / R::kN2) & 1), abort_flag);
-        ok = ok && warp_wait_fast(&ctl.d_full[gc % R::kN2], (uint32_t)((gc / R::kN2) & 1), abort_flag);
+        const uint32_t last = gc - kBufs;
+        if (R::kN2 > kBufs && gc >= kBufs)
+          ok = warp_wait_fast(&ctl.d_done[last % R::kN2], last / R::kN2 & 1, abort_flag);
+        ok = ok && warp_wait_fast(&ctl.d_full[gc % R::kN2], gc / R::kN2 & 1, abort_flag);
         if (ok && lane == 0) mbar_arrive_cluster(&ctl.w_full[gc % kBufs], 0);
         __syncwarp();
       }
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         if (kBufs == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_leader<2>(&ctl.s_free, rank);
+          if (lane == 0) mbar_arrive_leader<2>(&ctl.s_free);
         }
         // columns lo .. hi-1 of this thread's 64 count
         int lo = 0, hi = 64;
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_leader<2>(&ctl.w_full[b], rank, clear);
+          mbar_arrive_leader<2>(&ctl.w_full[b], clear);
           if (kByKeys) mbar_arrive(&ctl.st_free[sbuf]);
         }
         if (!kByKeys || --left == 0) {
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_leader<2>(&ctl.o_free, rank);
+      if (lane == 0) mbar_arrive_leader<2>(&ctl.o_free);
       ++uc;
     }
   }

@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
         mbar_wait_fast(&ctl.v_full[gc % kVSlots], (uint32_t)((gc / kVSlots) & 1), abort_flag);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_leader<CG>(&ctl.p_full[b], rank, clear);
+        if (lane == 0) mbar_arrive_leader<CG>(&ctl.p_full[b], clear);
       }
       if (!nf_taken) take_nf();
       float lt = 0.f;
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_leader<CG>(&ctl.o_free, rank);
+      if (lane == 0) mbar_arrive_leader<CG>(&ctl.o_free);
       ++uc;
     }
   }

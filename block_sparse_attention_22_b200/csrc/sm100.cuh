@@ -317,8 +317,8 @@ __device__ __forceinline__ void mbar_expect_tx_leader(uint64_t* bar, uint32_t by
 // it releases no shared memory unless `written`: a release at cluster scope holds the
 // warp up for some 300 cycles.
 template <int CG>
-__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar, uint32_t rank, bool written = false) {
-  if (CG == 1 || rank == 0)
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar, bool written = false) {
+  if (CG == 1 || cluster_ctarank() == 0)
     mbar_arrive(bar);
   else if (written)
     mbar_arrive_cluster(bar, 0);
