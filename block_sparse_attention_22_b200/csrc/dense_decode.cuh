@@ -307,9 +307,10 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
 // rows and of every head's O, reads each head's q from shared memory (two reads
 // for 32 products), and the 4 x HP sums over the lanes are reduced together, halving
 // their number with each exchange.  Lane h then does head h's softmax.  HP: heads,
-// rounded up to 4.  Bound by the instructions per key, not HBM, from 12 heads on:
-// 24 heads in two groups, 16 sequences of 8000 keys 112 us (0.72 of the HBM rate),
-// 8 of 2000 keys 24 us; 8 heads in 8 groups reach 0.92.
+// rounded up to 4.  Bound by the instructions per key, not HBM, from 12 heads on: 16
+// sequences of 8000 keys take 110 us with 24 heads in two groups (0.74 of the HBM
+// rate) and 142 us with 32 (0.57), 8 of 2000 keys 25 us; 8 heads in 8 groups read at
+// the HBM rate.
 namespace dense_decode {
 constexpr int kStep = 4;                              // keys
 constexpr int kF32Slots = 6, kF32SlotBytes = kStep * kHeadDim * 4;
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
     dense_decode_f32_kernel(const __grid_constant__ DenseTable t, const __grid_constant__ DenseDecodeF32Args a) {
   using namespace dense_decode;
   using namespace sm100;
+  constexpr int kHeads = HP == 16 ? 8 : HP;             // whose scores are formed together: 16 would spill
   extern __shared__ __align__(1024) unsigned char smem_1k[];
   unsigned char* const smem = smem_1k;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -378,17 +380,17 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
   DensePiece p;
   DenseUnit x;
   while (walk.next(t, p, x)) {
-    const int64_t head0 = (int64_t)t.q_offset[x.si] * a.H + x.grp * t.hpg;
+    auto head0 = [&]() { return (int64_t)t.q_offset[x.si] * a.H + x.grp * t.hpg; };
     for (int i = threadIdx.x; i < kRows * (kHeadDim / 4); i += kThreads) {     // rows beyond the heads zero
       const bool in = i / (kHeadDim / 4) < x.nrows;
-      cp_async16(smem_u32(q_s) + i * 16, a.q + head0 * kHeadDim + (in ? i * 4 : 0), in ? 16u : 0u);
+      cp_async16(smem_u32(q_s) + i * 16, a.q + head0() * kHeadDim + (in ? i * 4 : 0), in ? 16u : 0u);
     }
     // this warp's keys: 16 of each chunk, in steps of 4 (step j: chunk j / 4)
     const int32_t key0 = p.c0 * kKeys + warp * kTile;
     const int nc = min(p.c1 - p.c0, max(0, (x.kv_len - key0 + kKeys - 1) / kKeys)), n = nc * (kTile / kStep);
     int32_t look0 = -32;
-    int64_t my_row = -1;
-    auto chunk_row = [&](int c) -> int64_t {              // first cache row of this warp's 16 keys of chunk c
+    int32_t my_row = -1;                                  // cache rows fit 32 bits (they are TMA coordinates elsewhere)
+    auto chunk_row = [&](int c) -> int32_t {              // first cache row of this warp's 16 keys of chunk c
       if (c - look0 >= 32) {
         look0 = c;
         const int32_t key = key0 + (c + lane) * kKeys;
@@ -397,15 +399,15 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
           const int32_t pi = key / a.kv.page_tokens;
           const int32_t page = a.kv.table[(int64_t)t.slot[x.si] * a.kv.max_pages + pi];
           if (page >= 0 && page < a.kv.n_pages)
-            my_row = ((int64_t)page * t.G + x.grp) * a.kv.page_tokens + (key - pi * a.kv.page_tokens);
+            my_row = (page * t.G + x.grp) * a.kv.page_tokens + (key - pi * a.kv.page_tokens);
           else
             report_error(kErrBadIndex);
         }
       }
       return __shfl_sync(0xffffffffu, my_row, c - look0);
     };
-    auto load = [&](int j) {                              // K and V of step j, one group each
-      int64_t row = -1;
+    auto load = [&](int j) -> uint32_t {                  // K and V of step j, one group each; 1: no page
+      int32_t row = -1;
       int valid = 0;
       if (j < n) {
         row = chunk_row(j / (kTile / kStep));
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
 #pragma unroll
       for (int is_v = 0; is_v < 2; ++is_v) {
         if (j < n) {
-          const float* src = (const float*)(is_v ? a.kv.v : a.kv.k) + (valid > 0 ? row : 0) * kHeadDim + lane * 4;
+          const float* src = (const float*)(is_v ? a.kv.v : a.kv.k) + (int64_t)(valid > 0 ? row : 0) * kHeadDim + lane * 4;
           const uint32_t dst = smem_u32(ring + (2 * j + is_v) % kF32Slots * kF32SlotBytes) + lane * 16;
 #pragma unroll
           for (int r = 0; r < kStep; ++r)
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
         }
         cp_async_commit();
       }
-      return row;
+      return row < 0 ? 1u : 0u;
     };
     float2 o[HP][4];                                      // dims 4 lane .. +3 and 128 + 4 lane .. +3
 #pragma unroll
@@ -434,17 +436,16 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[h][k] = make_float2(0.f, 0.f);
     float m = -INFINITY, l = 0.f;                         // of head `lane`
-    int64_t rows_ahead[3];                                // of the steps in flight, oldest first
+    uint32_t bad_ahead = 0;                               // bit per step in flight, the oldest in bit 0
 #pragma unroll
-    for (int j = 0; j < 3; ++j) rows_ahead[j] = load(j);
+    for (int j = 0; j < 3; ++j) bad_ahead |= load(j) << j;
     cp_async_wait<5>();
     __syncthreads();                                      // q written
     for (int j = 0; j < n; ++j) {
-      const bool bad = rows_ahead[0] < 0;
+      const bool bad = bad_ahead & 1;
       // ---- scores
       cp_async_wait<5>();
       __syncwarp();
-      float dots[HP * kStep];
       {
         const float4* ks = reinterpret_cast<const float4*>(ring + (2 * j) % kF32Slots * kF32SlotBytes) + lane;
         float4 k0[kStep], k1[kStep];
@@ -454,23 +455,27 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
           k1[r] = ks[r * 64 + 32];
         }
 #pragma unroll
-        for (int h = 0; h < HP; ++h) {
-          const float4 q0 = reinterpret_cast<const float4*>(q_s + h * kHeadDim)[lane];
-          const float4 q1 = reinterpret_cast<const float4*>(q_s + h * kHeadDim)[lane + 32];
+        for (int h0 = 0; h0 < HP; h0 += kHeads) {
+          float dots[kHeads * kStep];
 #pragma unroll
-          for (int r = 0; r < kStep; ++r) {
-            float2 s = fma2(lo2(q0), lo2(k0[r]), make_float2(0.f, 0.f));
-            s = fma2(hi2(q0), hi2(k0[r]), s);
-            s = fma2(lo2(q1), lo2(k1[r]), s);
-            s = fma2(hi2(q1), hi2(k1[r]), s);
-            dots[h * kStep + r] = s.x + s.y;
+          for (int h = 0; h < kHeads; ++h) {
+            const float4 q0 = reinterpret_cast<const float4*>(q_s + (h0 + h) * kHeadDim)[lane];
+            const float4 q1 = reinterpret_cast<const float4*>(q_s + (h0 + h) * kHeadDim)[lane + 32];
+#pragma unroll
+            for (int r = 0; r < kStep; ++r) {
+              float2 s = fma2(lo2(q0), lo2(k0[r]), make_float2(0.f, 0.f));
+              s = fma2(hi2(q0), hi2(k0[r]), s);
+              s = fma2(lo2(q1), lo2(k1[r]), s);
+              s = fma2(hi2(q1), hi2(k1[r]), s);
+              dots[h * kStep + r] = s.x + s.y;
+            }
           }
+          int base = h0 * kStep;
+          reduce_halving<kHeads * kStep, 16>(dots, base);
+#pragma unroll
+          for (int i = 0; i < reduce_left(kHeads * kStep, 16); ++i) p_s[base + i] = dots[i];
         }
       }
-      int base = 0;
-      reduce_halving<HP * kStep, 16>(dots, base);
-#pragma unroll
-      for (int i = 0; i < reduce_left(HP * kStep, 16); ++i) p_s[base + i] = dots[i];
       __syncwarp();
       // ---- softmax of head `lane`
       bool need = false;
@@ -536,9 +541,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
         }
       }
       __syncwarp();                                       // the step's slots and P are read
-      rows_ahead[0] = rows_ahead[1];
-      rows_ahead[1] = rows_ahead[2];
-      rows_ahead[2] = load(j + 3);
+      bad_ahead = bad_ahead >> 1 | load(j + 3) << 2;
     }
     // ---- join the warps
     cp_async_wait_all();
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
       reinterpret_cast<float4*>(o_s + h * kOLd)[lane + 32] = make_float4(o[h][2].x, o[h][2].y, o[h][3].x, o[h][3].y);
     }
     __syncthreads();
-    decode_join(t, a.kv, x, p, head0, smem, m_s, l_s, a.o, a.lse, a.part);
+    decode_join(t, a.kv, x, p, head0(), smem, m_s, l_s, a.o, a.lse, a.part);
     __syncthreads();                                      // shared memory free for the next piece
   }
   dense_wait_last(a.late);
