@@ -18,8 +18,8 @@ qsa_status_t check_pages(const qsa_config_t* c, const qsa_pages_t* p) {
     return QSA_ERR_INVALID_ARG;
   if (p->n_pages <= 0 || p->page_tokens <= 0 || p->n_rows <= 0 || p->max_pages <= 0) return QSA_ERR_INVALID_ARG;
   if (p->page_tokens % 16 != 0) return QSA_ERR_UNSUPPORTED;
-  // cache rows are TMA coordinates (int32)
-  if ((int64_t)p->n_pages * c->n_kv_groups > INT32_MAX / p->page_tokens) return QSA_ERR_UNSUPPORTED;
+  // cache rows are TMA coordinates (int32, with room for a box behind the last)
+  if ((int64_t)p->n_pages * c->n_kv_groups > (INT32_MAX - 512) / p->page_tokens) return QSA_ERR_UNSUPPORTED;
   return QSA_OK;
 }
 

@@ -145,8 +145,10 @@ typedef struct {
 /* A paged K/V cache (device memory, caller-owned).  Position p of the sequence
  * in table row `slot` lives in page table[slot][p / page_tokens], at row
  * p % page_tokens of that page.  Pages may be shared by table rows that only
- * read them.  A slot cache of qsa_cache_t is the case page_tokens = n_cap,
- * n_pages = n_slots, table[slot] = { slot }. */
+ * read them.  A slot cache of qsa_cache_t whose n_cap is a multiple of 16 is the
+ * case page_tokens = n_cap, n_pages = n_slots, table[slot] = { slot }.
+ * n_pages * n_kv_groups * page_tokens is at most 2^31 - 513
+ * (QSA_ERR_UNSUPPORTED beyond, and for other page_tokens). */
 typedef struct {
   void* k;                /* [n_pages][n_kv_groups][page_tokens][head_dim]  keys, rotated */
   void* v;                /* [n_pages][n_kv_groups][page_tokens][head_dim]  values        */

@@ -69,3 +69,17 @@ def test_outputs_that_share_memory_with_another_array_are_refused(dtype, row):
         for other in ("q", "k", "v", "o", "lse", "dout", "dq", "dk", "dv"):
             if other != out:
                 assert bwd(**{out: at[other]}) == bad and bwd(**{out: at[other] - end + 16}) == bad, (out, other)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page,n_pages", [(16, (2 ** 31 - 256) // 32), (16, (2 ** 31 - 512 + 32) // 32), (2 ** 30 - 16, 1)])
+def test_caches_whose_rows_leave_no_room_for_a_box_are_unsupported(dtype, page, n_pages):
+    """Refused as what they are, not by the failure of a tensor map."""
+    cfg = qsa.make_config(shape(dtype=dtype))
+    arr, n = qsa.make_segments([(0, 8, 0, 0)])
+    assert 2 ** 31 - 512 <= n_pages * 2 * page < 2 ** 31
+    pages = qsa.qsa_pages_t(BASE, BASE << 1, BASE - 4096, n_pages, page, 1, 1)
+    assert qsa.get_lib().qsa_paged_attn_fwd(ctypes.byref(cfg), ctypes.byref(pages), arr, n, 8, BASE + 4096, BASE + (1 << 30),
+                                            None, None, 0, None) == qsa.QSA_ERR_UNSUPPORTED
+    assert qsa.get_lib().qsa_append_kv(ctypes.byref(cfg), ctypes.byref(pages), arr, n, 8, BASE, 512, BASE, 512, None, 0, None,
+                                       None) == qsa.QSA_ERR_UNSUPPORTED
