@@ -655,7 +655,7 @@ QSA_API qsa_status_t qsa_append_kv(const qsa_config_t* cfg, const qsa_pages_t* p
                                    int32_t n_segs, int32_t n_tokens, const void* k, int64_t ld_k, const void* v,
                                    int64_t ld_v, const void* q, int64_t ld_q, void* q_out, void* stream) {
   return guarded([&]() -> qsa_status_t {
-    qsa_status_t s = check_cfg(cfg);
+    qsa_status_t s = check_cfg(cfg, false);
     if (s != QSA_OK) return s;
     if ((s = check_pages(cfg, pages)) != QSA_OK) return s;
     if ((s = check_dense_segments(segs, n_segs, n_tokens, pages, false)) != QSA_OK) return s;
@@ -709,7 +709,7 @@ QSA_API qsa_status_t qsa_paged_attn_fwd(const qsa_config_t* cfg, const qsa_pages
                                         int32_t n_segs, int32_t n_tokens, const void* q, void* o, float* lse,
                                         void* workspace, size_t ws_bytes, void* stream) {
   return guarded([&]() -> qsa_status_t {
-    qsa_status_t s = check_cfg(cfg);
+    qsa_status_t s = check_cfg(cfg, false);
     if (s != QSA_OK) return s;
     if ((s = check_pages(cfg, pages)) != QSA_OK) return s;
     if ((s = check_dense_segments(segs, n_segs, n_tokens, pages, false)) != QSA_OK) return s;
@@ -727,7 +727,7 @@ QSA_API qsa_status_t qsa_prompt_attn_fwd(const qsa_config_t* cfg, const qsa_segm
                                          int32_t n_tokens, const void* q, const void* k, const void* v, void* o,
                                          float* lse, void* workspace, size_t ws_bytes, void* stream) {
   return guarded([&]() -> qsa_status_t {
-    qsa_status_t s = check_cfg(cfg);
+    qsa_status_t s = check_cfg(cfg, false);
     if (s != QSA_OK) return s;
     if ((s = check_dense_segments(segs, n_segs, n_tokens, nullptr, true)) != QSA_OK) return s;
     if (seg_rows(segs, n_segs) == 0) return QSA_OK;
@@ -746,7 +746,7 @@ QSA_API qsa_status_t qsa_prompt_attn_bwd(const qsa_config_t* cfg, const qsa_segm
                                          const float* lse, const void* dout, void* dq, void* dk, void* dv,
                                          void* workspace, size_t ws_bytes, void* stream) {
   return guarded([&]() -> qsa_status_t {
-    qsa_status_t s = check_cfg(cfg);
+    qsa_status_t s = check_cfg(cfg, false);
     if (s != QSA_OK) return s;
     if ((s = check_dense_segments(segs, n_segs, n_tokens, nullptr, true)) != QSA_OK) return s;
     if (seg_rows(segs, n_segs) == 0) return QSA_OK;

@@ -46,7 +46,8 @@ int rope_dims_of(const qsa_config_t* c) {
   return d - (d & 1);
 }
 
-qsa_status_t check_cfg(const qsa_config_t* c) {
+// indexer: the call rotates idx_dim vectors (the dense attention has none).
+qsa_status_t check_cfg(const qsa_config_t* c, bool indexer = true) {
   if (!c) return QSA_ERR_INVALID_ARG;
   if (c->r <= 0 || c->budget_tokens <= 0 || c->n_q_heads <= 0 || c->n_kv_groups <= 0 ||
       c->head_dim <= 0 || c->idx_heads <= 0 || c->idx_dim <= 0)
@@ -61,7 +62,7 @@ qsa_status_t check_cfg(const qsa_config_t* c) {
   if (c->n_q_heads / c->n_kv_groups > kMaxHpg) return QSA_ERR_UNSUPPORTED;
   if (c->budget_tokens / c->r > kMaxBudgetBlocks) return QSA_ERR_UNSUPPORTED;
   if (rope_dims_of(c) / 2 > kMaxRopeHalf) return QSA_ERR_UNSUPPORTED;
-  if (c->dtype == QSA_DTYPE_BF16 && rope_dims_of(c) / 2 > tc_index::kMaxRopeHalf) return QSA_ERR_UNSUPPORTED;
+  if (indexer && c->dtype == QSA_DTYPE_BF16 && rope_dims_of(c) / 2 > tc_index::kMaxRopeHalf) return QSA_ERR_UNSUPPORTED;
   return QSA_OK;
 }
 
@@ -984,7 +985,8 @@ QSA_API qsa_status_t qsa_sparse_attn_bwd(const qsa_config_t* cfg, const qsa_cach
 
 QSA_API size_t qsa_workspace_size(const qsa_config_t* cfg, const qsa_segment_t* segs,
                                   int32_t n_segs, int32_t n_tokens, qsa_op_t op) {
-  if (check_cfg(cfg) != QSA_OK || check_segments(segs, n_segs, n_tokens, nullptr, 0) != QSA_OK)
+  const bool indexer = op != QSA_OP_PAGED_ATTN && op != QSA_OP_PROMPT_ATTN && op != QSA_OP_PROMPT_ATTN_BWD;
+  if (check_cfg(cfg, indexer) != QSA_OK || check_segments(segs, n_segs, n_tokens, nullptr, 0) != QSA_OK)
     return SIZE_MAX;
   const Geo g = make_geo(cfg, nullptr);
   switch (op) {

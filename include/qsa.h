@@ -52,7 +52,8 @@
  *     no-op (QSA_OK).
  *   - Supported shapes: r == 4, head_dim == 256, n_q_heads/n_kv_groups <= 16,
  *     idx_heads == 4, idx_dim in {64, 128}, budget_tokens a multiple of r with
- *     budget_tokens/r <= 512.
+ *     budget_tokens/r <= 512; in bf16 at most 64 rotated dims of idx_dim (the
+ *     append and the dense attention have no such limit).
  *
  * Token batch.  A call processes T query tokens given as segments: segment i
  * holds q_len consecutive positions pos0 .. pos0+q_len-1 of the sequence in

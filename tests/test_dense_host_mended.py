@@ -83,3 +83,25 @@ def test_caches_whose_rows_leave_no_room_for_a_box_are_unsupported(dtype, page, 
                                             None, None, 0, None) == qsa.QSA_ERR_UNSUPPORTED
     assert qsa.get_lib().qsa_append_kv(ctypes.byref(cfg), ctypes.byref(pages), arr, n, 8, BASE, 512, BASE, 512, None, 0, None,
                                        None) == qsa.QSA_ERR_UNSUPPORTED
+
+
+def test_a_rotation_of_all_dims_is_not_held_to_the_indexers_limit():
+    """idx_dim 128 in bf16: the indexer rotates at most 64 dims, the append any number
+    of the head's.  Calls that are refused later, or do nothing, show what the
+    configuration's check says."""
+    sh = shape(rope_fraction=1.0)
+    sh.idx_dim = 128
+    cfg = qsa.make_config(sh)
+    lib = qsa.get_lib()
+    one, none = qsa.make_segments([(0, 8, 0, 0)]), qsa.make_segments([])
+    pages = qsa.qsa_pages_t(BASE, BASE << 1, BASE - 4096, 4, 16, 1, 4)
+    assert lib.qsa_append_kv(ctypes.byref(cfg), ctypes.byref(pages), *none, 0, BASE, 512, BASE, 512, None, 0, None,
+                             None) == qsa.QSA_OK
+    assert lib.qsa_paged_attn_fwd(ctypes.byref(cfg), ctypes.byref(pages), *none, 0, BASE, BASE, None, None, 0,
+                                  None) == qsa.QSA_OK
+    for op in (qsa.QSA_OP_PAGED_ATTN, qsa.QSA_OP_PROMPT_ATTN, qsa.QSA_OP_PROMPT_ATTN_BWD):
+        assert qsa.workspace_size(cfg, one, 8, op) < 1 << 40
+    assert qsa.workspace_size(cfg, one, 8, qsa.QSA_OP_FORWARD) == ctypes.c_size_t(-1).value
+    assert lib.qsa_prompt_attn_fwd(ctypes.byref(cfg), *none, 0, BASE, BASE, BASE, BASE, None, None, 0,
+                                   None) == qsa.QSA_OK
+    assert lib.qsa_prompt_attn_bwd(ctypes.byref(cfg), *one, 8, *([BASE] * 9), None, 0, None) == qsa.QSA_ERR_WORKSPACE

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import block_sparse_attention_22_b200 as qsa
-from dense_testlib import (D, F64, attend64, check_forward, fill_pages, make_table, score_error, shape, torch_dtype,
-                           workspace)
+from dense_testlib import (D, F64, attend64, check_forward, fill_pages, make_table, rotate64, score_error, shape,
+                           torch_dtype, workspace)
 
 pytestmark = pytest.mark.gpu
 SCALE = 1.0 / math.sqrt(D)
@@ -287,3 +287,25 @@ def test_gradients_of_the_first_rows_do_not_carry_the_rounding_of_o(heads, group
                 s.masked_fill_(torch.ones_like(s, dtype=torch.bool).triu(1), -math.inf)
                 tol += SCALE * ddelta * (torch.softmax(s, 1)[128:].t() @ q[128:, h].abs())
             assert bool((g[1][t, grp].to(F64).abs() <= tol).all()), (grp, n)
+
+
+# ------------------------------------------------------------------ rotations beyond the indexer's
+@pytest.mark.parametrize("frac", [1.0, 0.6])
+def test_append_rotates_more_dims_than_the_indexer_can(frac):
+    """idx_dim 128 in bf16.  A rotated value: cos, sin and two products and a sum in
+    fp32 (2^-24 each) of |a| + |b|, one rounding."""
+    sh = shape(24, 2, "bf16", frac)
+    sh.idx_dim = 128
+    cfg, gen = qsa.make_config(sh), torch.Generator().manual_seed(12)
+    kp, vp = (torch.zeros((3, 2, 16, D), dtype=BF, device="cuda") for _ in range(2))
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    k, v, q = _randn(gen, 40, 2, D), _randn(gen, 40, 2, D), _randn(gen, 40, 24, D)
+    q_out, pos = torch.empty_like(q), torch.arange(40, device="cuda")
+    qsa.qsa_append_kv(cfg, qsa.make_pages(kp, vp, table), qsa.make_segments([(0, 40, 0, 0)]), 40, k, v, q, q_out)
+    qsa.qsa_device_status()
+    pg = table[0].long()[pos // 16]
+    for got, x in ((kp[pg, :, pos % 16], k), (q_out, q)):
+        ref = rotate64(x, pos, frac)
+        tol = 2.0 ** -8 * ref.abs() * 1.001 + 8 * 2.0 ** -24 * x.to(F64).abs().amax(dim=-1, keepdim=True)
+        assert bool(((got.to(F64) - ref).abs() <= tol).all())
+    assert torch.equal(vp[pg, :, pos % 16], v)
