@@ -328,12 +328,13 @@ def _check_like(where, name, t, shape, dtype):
 
 
 def _token_stride(where, name, t) -> int:
-    """Elements between a [T, heads, D] tensor's tokens; its heads are dense."""
+    """Elements between a [T, heads, D] tensor's tokens; its heads are dense.  The stride of a
+    dim of size 1 means nothing."""
     n, heads, dim = t.shape
     ld, sh, sd = t.stride()
-    if n and (sd != 1 or sh != dim):
+    if n and (sd != 1 or (heads > 1 and sh != dim)):
         raise ValueError(f"{where}: the heads of a token of {name} are not contiguous")
-    return max(ld, heads * dim) if n <= 1 else ld
+    return heads * dim if n <= 1 else ld
 
 
 def _bytes(t) -> int:

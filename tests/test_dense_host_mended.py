@@ -105,3 +105,13 @@ def test_a_rotation_of_all_dims_is_not_held_to_the_indexers_limit():
     assert lib.qsa_prompt_attn_fwd(ctypes.byref(cfg), *none, 0, BASE, BASE, BASE, BASE, None, None, 0,
                                    None) == qsa.QSA_OK
     assert lib.qsa_prompt_attn_bwd(ctypes.byref(cfg), *one, 8, *([BASE] * 9), None, 0, None) == qsa.QSA_ERR_WORKSPACE
+
+
+def test_strides_of_dims_of_size_one_are_not_looked_at():
+    """One group's [1, T, D] array seen as [T, 1, D], and one token cut from a longer row."""
+    assert qsa._token_stride("append", "k", _z(1, 5, D).transpose(0, 1)) == D
+    assert qsa._token_stride("append", "k", _z(1, 2 * D + 3)[:, :2 * D].view(1, 2, D)) == 2 * D
+    assert qsa._token_stride("append", "k", _z(4, 2 * D + 8)[:, :2 * D].view(4, 2, D)) == 2 * D + 8
+    for bad in (_z(5, 2, 2 * D)[..., ::2], _z(2, 5, D).transpose(0, 1), _z(5, 4, D)[:, ::2]):
+        with pytest.raises(ValueError):
+            qsa._token_stride("append", "k", bad)

@@ -309,3 +309,17 @@ def test_append_rotates_more_dims_than_the_indexer_can(frac):
         tol = 2.0 ** -8 * ref.abs() * 1.001 + 8 * 2.0 ** -24 * x.to(F64).abs().amax(dim=-1, keepdim=True)
         assert bool(((got.to(F64) - ref).abs() <= tol).all())
     assert torch.equal(vp[pg, :, pos % 16], v)
+
+
+# ------------------------------------------------------------------ strides of dims of size 1
+def test_append_of_one_group_or_one_token_takes_any_stride_of_the_dim_of_size_one():
+    gen = torch.Generator().manual_seed(13)
+    for groups, T, k, v in (
+            (1, 5, _randn(gen, 1, 5, D).transpose(0, 1), _randn(gen, 1, 5, D).transpose(0, 1)),
+            (2, 1, _randn(gen, 1, 2 * D + 3)[:, :2 * D].view(1, 2, D), _randn(gen, 1, 2 * D + 3)[:, :2 * D].view(1, 2, D))):
+        cfg = qsa.make_config(shape(12 * groups, groups, "bf16", 0.0))
+        kp, vp = (torch.zeros((1, groups, 16, D), dtype=BF, device="cuda") for _ in range(2))
+        pages = qsa.make_pages(kp, vp, torch.zeros((1, 1), dtype=torch.int32, device="cuda"))
+        qsa.qsa_append_kv(cfg, pages, qsa.make_segments([(0, T, 3, 0)]), T, k, v)
+        assert torch.equal(kp[0, :, 3:3 + T], k.transpose(0, 1)) and torch.equal(vp[0, :, 3:3 + T], v.transpose(0, 1))
+        assert not kp[0, :, :3].any() and not kp[0, :, 3 + T:].any()
