@@ -592,7 +592,16 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
       !make_dense_map(&tq, a.q, rows, 1, g.hpg) || !make_dense_map(&to, a.dout, rows, 1, g.hpg) ||
       !make_dense_map(&rq, a.q, rows, 1, g.hpg & -g.hpg) || !make_dense_map(&ro, a.dout, rows, 1, g.hpg & -g.hpg))
     return QSA_ERR_CUDA;
-  qsa_status_t r = for_each_table(
+  // launches for the flagged segments, not levelled; rows and keys split alike, by the
+  // number of segments (n_tokens * H in 31 bits is far from the limit on units)
+  std::vector<DenseLaunch> rows_l, keys_l;
+  size_t part = 0;
+  DenseKind kr = dense_bwd_kind(false, false), kk = dense_bwd_kind(false, true);
+  kr.level = kk.level = false;
+  qsa_status_t r = plan_launches(g, p.segs, kr, rows_l, part);
+  if (r == QSA_OK) r = plan_launches(g, p.segs, kk, keys_l, part);
+  if (r != QSA_OK) return r;
+  r = for_each_table(
       p.segs.data(), (int)p.segs.size(),
       [&](const qsa_segment_t& s) { return cdiv(s.q_len, dense_bwd::kStatTile) * dense_bwd::kStatTile; },
       [&](const SegTable& t) -> cudaError_t {
@@ -615,15 +624,7 @@ qsa_status_t run_dense_bwd_bf16(const Geo& g, const DenseBwdPlan& p, DenseBwdArg
   b.out = (B*)a.dk;
   if ((r = run_dense_grad_tc<dense_bwd::kDk>(p, {mq, mo, mq, mk, mv, mk, mv}, b, parts2, st)) != QSA_OK) return r;
   cudaError_t e = launch_bwd_joins<B>(g, p, a, parts, parts2, parts, 0, flags, st);
-  // the flagged segments; their launches are not levelled
   a.flags = flags;
-  std::vector<DenseLaunch> rows_l, keys_l;
-  size_t part = 0;
-  DenseKind kr = dense_bwd_kind(false, false), kk = dense_bwd_kind(false, true);
-  kr.level = kk.level = false;
-  if ((r = plan_launches(g, p.segs, kr, rows_l, part)) != QSA_OK) return r;
-  if ((r = plan_launches(g, p.segs, kk, keys_l, part)) != QSA_OK) return r;
-  if (rows_l.size() != keys_l.size()) return QSA_ERR_UNSUPPORTED;
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(dense_bwd_flagged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              dense_simt::kBwdSmem);

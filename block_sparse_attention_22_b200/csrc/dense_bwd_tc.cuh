@@ -145,8 +145,9 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
   const int cta = blockIdx.x / 2;
 
   // ---------------------------------------------------------------- set-up
-  if (smem_u32(smem) & 1023u) {                      // the swizzled tiles need it; the same in both CTAs
+  if (smem_u32(smem) & 1023u) {                      // as in the forward
     report_error(kErrWaitTimeout);
+    pdl_wait();
     return;
   }
   if (threadIdx.x == 0) {
@@ -355,9 +356,10 @@ __global__ void __launch_bounds__(dense_bwd::kThreads, 1)
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    // ============================================================ rank 1's operand of the gradient's product handed to rank 0
-    // (as the forward's V).  A chunk's arrival waits for the product that used the same
-    // w_full before: with more slots than buffers the operand may be a chunk too early.
+    // ============================================================ rank 1's operand handed to rank 0
+    // That of the gradient's product, as the forward's V.  A chunk's arrival waits for
+    // the product that used the same w_full before: with more slots than buffers the
+    // operand may be a chunk too early.
     uint32_t gc = 0;
     for (bool ok = true; ok && next();)
       for (int c = p.c0; c < p.c1 && ok; ++c, ++gc) {

@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(dense_decode::kThreads, 1)
 #pragma unroll
       for (int is_v = 0; is_v < 2; ++is_v) {
         if (j < n) {
-          const float* src = (const float*)(is_v ? a.kv.v : a.kv.k) + (int64_t)(valid > 0 ? row : 0) * kHeadDim + lane * 4;
+          const int64_t at = (int64_t)(valid > 0 ? row : 0) * kHeadDim + lane * 4;
+          const float* src = (const float*)(is_v ? a.kv.v : a.kv.k) + at;
           const uint32_t dst = smem_u32(ring + (2 * j + is_v) % kF32Slots * kF32SlotBytes) + lane * 16;
 #pragma unroll
           for (int r = 0; r < kStep; ++r)

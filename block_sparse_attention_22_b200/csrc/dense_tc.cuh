@@ -13,8 +13,10 @@
 // in the sparse kernels); the row sum adds the unrounded values in fp32.
 //
 // Two forms (CG = CTAs per unit):
-//   CG = 1  128 rows, chunks of 64 keys, one CTA: units of few rows (decode),
-//           bound by the HBM reads of K and V.
+//   CG = 1  128 rows, chunks of 64 keys, one CTA: segments of 2 to 128 rows
+//           (a few tokens each; prompts of one), where no longer ones are in the
+//           call.  Single tokens over a cache have kernels of their own
+//           (dense_decode.cuh).
 //   CG = 2  256 rows, chunks of 128 keys, a CTA pair (cta_group::2): each CTA
 //           owns 128 rows, loads half of K's keys and half of V's dims, and
 //           the pair's MMAs read both halves, so a key crosses L2 once per
@@ -46,9 +48,9 @@
 // Every mbarrier wait is bounded; a timeout records an error and the CTA
 // drains and returns.
 //
-// Measured (24 heads, 2 groups): a 4096-token chunk over 128K keys 9.96 ms, 1.30
+// Measured (24 heads, 2 groups): a 4096-token chunk over 128K keys 9.93 ms, 1.31
 // PFLOP/s, 0.94 of sustained cuBLAS under the same power cap; two prompts of 8192
-// 1.30 ms, where the softmax (2400 cycles a chunk, its exponentials 1024 on
+// 1.29 ms, where the softmax (2400 cycles a chunk, its exponentials 1024 on
 // MUFU) outlasts the products' 2048 and a unit's change costs 5 us.
 #pragma once
 #include "qsa_internal.cuh"
@@ -231,8 +233,11 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
   const int cta = blockIdx.x / CG;
 
   // ---------------------------------------------------------------- set-up
-  if (smem_u32(smem) & 1023u) {                      // the swizzled tiles need it; the same in every CTA
+  // The swizzled tiles need the alignment that smem_1k asks for; the same in every CTA.
+  // Without it there is no result, which is what a wait that gave up tells the host.
+  if (smem_u32(smem) & 1023u) {
     report_error(kErrWaitTimeout);
+    pdl_wait();
     return;
   }
   if (threadIdx.x == 0) {
@@ -264,8 +269,8 @@ __global__ void __launch_bounds__(dense_tc::kThreads, 1)
 
   DenseWalk walk;
   walk.init(t, cta);
-  DensePiece p;
-  DenseUnit x;
+  DensePiece p = {};
+  DenseUnit x = {};
   if (warp == kProducerWarp) {
     // ============================================================ TMA producer
     // A slot is 256 / box boxes of `box` keys x 64 dims, one per lane.  A chunk's

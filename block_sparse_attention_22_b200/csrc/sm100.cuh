@@ -358,53 +358,7 @@ __device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols) 
   else
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols));
 }
-// D[tmem] (+)= A[smem] * B[smem]
-template <int CG>
-__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        bool accumulate) {
-  if constexpr (CG == 1) {
-    umma_bf16(d_tmem, a_desc, b_desc, idesc, accumulate);
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
-  }
-}
-// D[tmem] (+)= A[tmem] * B[smem]
-template <int CG>
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                        bool accumulate) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
-}
-// Arrives once on `bar` (of both CTAs of a pair) when every MMA this thread
-// issued so far has completed.
-template <int CG>
-__device__ __forceinline__ void umma_commit_cg(uint64_t* bar) {
-  if constexpr (CG == 1) {
-    umma_commit(bar);
-  } else {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
-  }
-}
-
-// The pair's form on this CTA's barrier alone.
+// umma_commit for the pair's MMAs, on this CTA's barrier alone.
 __device__ __forceinline__ void umma_commit_pair_local(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
@@ -412,7 +366,10 @@ __device__ __forceinline__ void umma_commit_pair_local(uint64_t* bar) {
 
 // Forms that a whole warp calls with the same operands and one thread executes
 // (`leader`: nonzero in that thread alone).  The operands stay in uniform
-// registers, which a branch around the instruction would prevent.
+// registers, which a branch around the instruction would prevent.  ss, ts:
+// D[tmem] (+)= A B with A in shared or tensor memory, B in shared memory; commit:
+// arrives once on `bar` (of both CTAs of a pair) when every MMA issued so far by
+// the thread has completed.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t e;
   asm volatile(
@@ -475,13 +432,6 @@ __device__ __forceinline__ void umma_commit_warp(uint32_t leader, uint64_t* bar)
             smem_u32(bar)),
         "h"((uint16_t)3), "r"(leader)
         : "memory");
-}
-// Brings a box into L2.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y)
-               : "memory");
 }
 
 // ------------------------------------------------------------------ misc
