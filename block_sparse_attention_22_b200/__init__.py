@@ -278,15 +278,16 @@ def make_pages(k, v, table) -> qsa_pages_t:
         raise ValueError("make_pages: k and v are [n_pages, G, page_tokens, D] of one dtype, table is [rows, max_pages]")
     if str(table.dtype) != "torch.int32":
         raise ValueError("make_pages: table is int32")
-    _one_device("make_pages", k, v, table)
+    _one_device("make_pages", k, v, table, host_too=True)
     pages = qsa_pages_t(_ptr(k), _ptr(v), _ptr(table), k.shape[0], k.shape[2], table.shape[0], table.shape[1])
     pages.tensors = (k, v, table)
     pages.layout = (k.dtype, k.shape[1], k.shape[3], k.device)
     return pages
 
 
-def _one_device(where, *tensors):
-    """The tensors' device; they are contiguous and, where it is a GPU, on the current one."""
+def _one_device(where, *tensors, host_too=False):
+    """The tensors' device; they are contiguous and on the current GPU, whose kernels take their
+    addresses as they are (host_too: or on the host)."""
     torch = _torch()
     dev = None
     for t in tensors:
@@ -298,16 +299,11 @@ def _one_device(where, *tensors):
             dev = t.device
         elif t.device != dev:
             raise ValueError(f"{where}: tensors on {dev} and {t.device}")
-    if dev is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        raise ValueError(f"{where}: tensors on {dev}, but the current device is {torch.cuda.current_device()}")
-    return dev
-
-
-def _on_gpu(where, *tensors):
-    """_one_device, and that it is a GPU: the kernels take addresses as they are."""
-    dev = _one_device(where, *tensors)
     if dev.type != "cuda":
-        raise ValueError(f"{where}: tensors on {dev}, not on a GPU")
+        if not host_too:
+            raise ValueError(f"{where}: tensors on {dev}, not on a GPU")
+    elif dev.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: tensors on {dev}, but the current device is {torch.cuda.current_device()}")
     return dev
 
 
@@ -349,7 +345,7 @@ def qsa_append_kv(cfg, pages, segs, n_tokens, k, v, q=None, q_out=None, stream=N
     dtype, kv, qo, _ = _layout(where, cfg, n_tokens, pages)
     _check_like(where, "k", k, kv, dtype)
     _check_like(where, "v", v, kv, dtype)
-    dev = _on_gpu(where, pages.tensors[2], q_out)
+    dev = _one_device(where, pages.tensors[2], q_out)
     ld_q = 0
     if q is not None:
         _check_like(where, "q", q, qo, dtype)
@@ -372,7 +368,7 @@ def qsa_paged_attn_fwd(cfg, pages, segs, n_tokens, q, o, lse=None, workspace=Non
     _check_like(where, "o", o, qo, dtype)
     if lse is not None:
         _check_like(where, "lse", lse, stat, _torch().float32)
-    _on_gpu(where, q, o, lse, workspace, pages.tensors[2])
+    _one_device(where, q, o, lse, workspace, pages.tensors[2])
     _check(get_lib().qsa_paged_attn_fwd(cfg, pages, arr, n, n_tokens, q.data_ptr(), o.data_ptr(), _ptr(lse),
                                         _ptr(workspace), _bytes(workspace), _stream(stream)), where)
 
@@ -387,7 +383,7 @@ def qsa_prompt_attn_fwd(cfg, segs, n_tokens, q, k, v, o, lse=None, workspace=Non
         _check_like(where, name, t, shape, dtype)
     if lse is not None:
         _check_like(where, "lse", lse, stat, _torch().float32)
-    _on_gpu(where, q, k, v, o, lse, workspace)
+    _one_device(where, q, k, v, o, lse, workspace)
     _check(get_lib().qsa_prompt_attn_fwd(cfg, arr, n, n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
                                          _ptr(workspace), _bytes(workspace), _stream(stream)), where)
 
@@ -402,7 +398,7 @@ def qsa_prompt_attn_bwd(cfg, segs, n_tokens, q, k, v, o, lse, dout, dq, dk, dv, 
                            ("dk", dk, kv), ("dv", dv, kv)):
         _check_like(where, name, t, shape, dtype)
     _check_like(where, "lse", lse, stat, _torch().float32)
-    _on_gpu(where, q, k, v, o, lse, dout, dq, dk, dv, workspace)
+    _one_device(where, q, k, v, o, lse, dout, dq, dk, dv, workspace)
     _check(get_lib().qsa_prompt_attn_bwd(cfg, arr, n, n_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
                                          _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), _bytes(workspace),
                                          _stream(stream)), where)
