@@ -24,8 +24,8 @@
 // columns they were computed from, so no warp waits for another's reads.  A rounded
 // dS makes the error of dq and dk 1.42 times that of rounding the result alone, as
 // P's does dv's.  (Its remainders could be multiplied too, from the columns that dS
-// leaves free: 1.00 times, but 8.33 ms instead of 7.29 for the two prompts below
-// with their forward.)  Rows of few keys have an o as large as v, and the error of
+// leaves free: 1.00 times, but 8.33 ms instead of 7.29, in the same minute, for the
+// two prompts below with their forward.)  Rows of few keys have an o as large as v, and the error of
 // delta = dout . o, o rounded, is then several times dS's: for rows whose keys are
 // all in the first chunk (positions below 128) the dQ kernel forms delta as the sum
 // of P dP instead and leaves it for the dK kernel.
@@ -44,8 +44,8 @@
 // anything: their scores are replaced and their operand rows zeroed in shared
 // memory.  Every mbarrier wait is bounded.
 //
-// Measured (two prompts of 8192, 24 heads, 2 groups): dQ 1.75 ms, dV 1.35, dK 2.1,
-// 6.6 TFLOP issued in 5.2 ms, the tensor pipe 73 to 84 % active at the 1.3 to 1.5
+// Measured (two prompts of 8192, 24 heads, 2 groups): dQ 1.62 ms, dV 1.34, dK 2.05,
+// 6.6 TFLOP issued in 5.0 ms, the tensor pipe 72 to 80 % active at the 1.3 to 1.5
 // GHz that the power cap leaves.
 #pragma once
 #include <type_traits>

@@ -48,9 +48,9 @@
 // Every mbarrier wait is bounded; a timeout records an error and the CTA
 // drains and returns.
 //
-// Measured (24 heads, 2 groups): a 4096-token chunk over 128K keys 9.93 ms, 1.31
+// Measured (24 heads, 2 groups): a 4096-token chunk over 128K keys 10.0 ms, 1.30
 // PFLOP/s, 0.94 of sustained cuBLAS under the same power cap; two prompts of 8192
-// 1.29 ms, where the softmax (2400 cycles a chunk, its exponentials 1024 on
+// 1.30 ms, where the softmax (2400 cycles a chunk, its exponentials 1024 on
 // MUFU) outlasts the products' 2048 and a unit's change costs 5 us.
 #pragma once
 #include "qsa_internal.cuh"

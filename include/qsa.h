@@ -391,6 +391,9 @@ qsa_status_t qsa_append_kv(const qsa_config_t* cfg, const qsa_pages_t* pages,
  * when that size is 0); contents on entry are ignored; calls whose work may
  * overlap on the GPU need one each.  The result does not depend on the order
  * in which the GPU runs the work: repeated calls give the same bits.
+ * Sums and softmax statistics are fp32.  bf16: the weights exp(s - max) are
+ * rounded to bf16 for the tensor-core product with V (not in lse or the sum
+ * that divides it), which makes o's error 1.2 to 1.45 times that of rounding it.
  */
 qsa_status_t qsa_paged_attn_fwd(const qsa_config_t* cfg, const qsa_pages_t* pages,
                                 const qsa_segment_t* segs, int32_t n_segs, int32_t n_tokens,
@@ -407,7 +410,7 @@ qsa_status_t qsa_paged_attn_fwd(const qsa_config_t* cfg, const qsa_pages_t* page
  * q, o: device [T][n_q_heads][head_dim]; k, v: device [T][n_kv_groups][head_dim]
  * (I/O dtype, already rotated); lse: device fp32 [T][n_q_heads] or NULL.
  * Rows of no segment are neither read nor written.  Overlaps (of token rows and
- * of arrays), workspace (QSA_OP_PROMPT_ATTN) and repeatability as
+ * of arrays), workspace (QSA_OP_PROMPT_ATTN), repeatability and roundings as
  * qsa_paged_attn_fwd.
  */
 qsa_status_t qsa_prompt_attn_fwd(const qsa_config_t* cfg, const qsa_segment_t* segs,
