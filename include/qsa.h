@@ -382,8 +382,8 @@ qsa_status_t qsa_append_kv(const qsa_config_t* cfg, const qsa_pages_t* pages,
  * A page number outside [0, n_pages) is skipped (its tokens contribute
  * nothing) and reported by qsa_device_status as QSA_ERR_BAD_INDEX; a query
  * left without any key gets o = 0 and lse = -inf.  A query whose every score is
- * -inf (infinities in q or K) gets the formula's o = NaN and lse = -inf; the
- * sparse attention gives o = 0 there.
+ * -inf (infinities in q or K) gets the formula's o = NaN, 0 / 0, and lse = -inf
+ * (the sparse attention leaves such rows open: 0 or NaN, by the kernel).
  * Token rows of different segments must not overlap, and o and lse share no
  * memory with each other or with q, K and V (QSA_ERR_INVALID_ARG); the
  * workspace shares none with any array.
