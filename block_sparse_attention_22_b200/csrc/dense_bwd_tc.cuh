@@ -76,7 +76,7 @@ template <Grad M> struct Ring {
   static constexpr int kStats = M == kDv ? 4 : 2;     // buffers of row statistics
 };
 constexpr int kOffCtl = 3 * kSlotBytes + 2 * kQBytes; // 229376; dV: 5 slots and one tile
-constexpr int kCtlBytes = 3072;
+constexpr int kCtlBytes = 3 * 1024;
 constexpr int kSmemBytes = kOffCtl + kCtlBytes;       // 232448: the base itself is 1024-byte aligned
 constexpr uint32_t kTmemP = 128, kTmemD = 256;
 using Pair = dense_tc::Shape<2>;

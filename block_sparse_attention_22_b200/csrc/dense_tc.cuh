@@ -72,7 +72,7 @@ constexpr int kQBytes = 65536;                        // 128 rows x 256 dims, 4 
 constexpr int kOffV = kKSlots * kSlotBytes;
 constexpr int kOffQ = kSlots * kSlotBytes;            // 131072
 constexpr int kOffCtl = kOffQ + kQBytes;              // 196608
-constexpr int kCtlBytes = 3072;
+constexpr int kCtlBytes = 3 * 1024;
 constexpr int kSmemBytes = kOffCtl + kCtlBytes;       // 199680: the base itself is 1024-byte aligned
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
 constexpr int kNfBufs = 4;                            // units whose non-finite lists may be in use at once, or made ahead
